@@ -73,6 +73,8 @@ typedef enum moe_status {
 #define MOE_DEVERR_WAIT_TIMEOUT 0x2  /* a pipeline wait gave up: results of that call are invalid */
 #define MOE_DEVERR_Y_RANGE 0x4       /* moe_forward, tiled paths: a down-GEMM output beyond the fp16
                                         range of its intermediate y was clipped to +-65504 */
+#define MOE_DEVERR_BAD_LOGIT 0x8     /* moe_route, moe_layer: a router logit was NaN or +inf; that expert
+                                        was not chosen for that token */
 
 /* Expert-GEMM path. AUTO picks from the static shape, a = T_max*k/E routed
  * rows per expert on average: M-small for a <= 8, single-CTA tiles for
@@ -330,6 +332,151 @@ moe_status_t moe_weight_bytes(const moe_problem_t *problem, int32_t layout, size
  * saturation at 448). */
 moe_status_t moe_quantize_weights(const moe_problem_t *problem, const void *W13, const void *W2,
                                   void *W13_mx, void *W2_mx, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The block around the expert execution: the norm of the residual stream
+ * before it, the router, and the way back into the residual stream (norm,
+ * gate, residual scale), each as its own entry point and, for a few tokens,
+ * together with the experts as one call (moe_layer). The conventions above
+ * hold: device pointers, 16-byte alignment, no allocation, no host
+ * synchronisation, legal inside stream capture, statuses fail closed. An
+ * operator reads and writes the rows t < T only (T as d_num_tokens gives it,
+ * T_max when that is NULL). The pages leave the router and the norms outside
+ * the path (TileOps page, Summary: routing weights kept outside expert
+ * compute); the formulas below are the usual ones of such models.
+ * ------------------------------------------------------------------------ */
+
+typedef enum moe_dtype {
+    MOE_DTYPE_BF16 = 0,
+    MOE_DTYPE_FP32 = 1
+} moe_dtype_t;
+
+/* The gate g of moe_norm_residual and moe_layer. */
+typedef enum moe_gate {
+    MOE_GATE_NONE = 0,     /* 1 */
+    MOE_GATE_CHANNEL = 1,  /* g[H], w_dtype: one value per channel (a learned layer scale) */
+    MOE_GATE_TOKEN = 2,    /* g[T_max] fp32: one value per token */
+    MOE_GATE_ELEMENT = 3   /* g[T_max, H] bf16, rows gate_stride apart */
+} moe_gate_t;
+
+typedef struct moe_norm_problem {
+    int32_t T_max;          /* maximum tokens, >= 1 */
+    int32_t H;              /* hidden size, a multiple of 64, at most 32768 */
+    int32_t h_dtype;        /* moe_dtype_t of the residual stream (h and h_out) */
+    int32_t w_dtype;        /* moe_dtype_t of the norm weights and of the channel gate */
+    int32_t unit_offset;    /* 1: a norm multiplies by 1 + w instead of w */
+    int32_t norm_block;     /* moe_norm_residual, moe_layer: 1: y is normalised, 0: taken as it is */
+    int32_t gate;           /* moe_gate_t */
+    float eps;              /* > 0, finite */
+    float residual_scale;   /* s, finite */
+    int64_t h_stride;       /* elements between rows: 0 means H; else >= H and a multiple of 8 */
+    int64_t y_stride;
+    int64_t x_stride;       /* of x (moe_norm) and x_next */
+    int64_t out_stride;     /* of h_out */
+    int64_t gate_stride;    /* of an ELEMENT gate */
+} moe_norm_problem_t;
+
+/*
+ * Norm before the block: x[t, m] = bf16( h[t, m] * r_t * w[m] ),
+ * r_t = 1 / sqrt( mean_m h[t, m]^2 + eps ), in fp32 with one rounding.
+ *   h[T_max, H] of h_dtype, w[H] of w_dtype or NULL (no weight),
+ *   x[T_max, H] bf16 out; x must not overlap h.
+ * norm_block, gate and residual_scale are not read.
+ */
+moe_status_t moe_norm(const moe_norm_problem_t *problem, const void *h, const void *w, const int32_t *d_num_tokens,
+                      void *x, void *stream);
+
+/*
+ * Back into the residual stream, and the next norm in the same pass:
+ *   n[t, m]      = y[t, m] * r(y_t) * w_post[m]      (norm_block; else y[t, m])
+ *   h_out[t, m]  = h[t, m] + s * g * n[t, m]
+ *   x_next[t, m] = bf16( h'[t, m] * r(h'_t) * w_next[m] ), h' = h_out before its rounding
+ * in fp32, one rounding per output.
+ *   y[T_max, H] bf16 (moe_forward's out), gate as `gate` says (NULL for
+ *   MOE_GATE_NONE), w_post and w_next [H] or NULL (no weight), h_out of
+ *   h_dtype, x_next bf16 or NULL (not computed). h_out may be h itself, with
+ *   the same stride; no other buffers may overlap.
+ */
+moe_status_t moe_norm_residual(const moe_norm_problem_t *problem, const void *h, const void *y, const void *w_post,
+                               const void *gate, const void *w_next, const int32_t *d_num_tokens, void *h_out,
+                               void *x_next, void *stream);
+
+/* Score of an expert from its logit. */
+typedef enum moe_score {
+    MOE_SCORE_SOFTMAX = 0,  /* softmax over all E experts */
+    MOE_SCORE_SIGMOID = 1
+} moe_score_t;
+
+typedef struct moe_router_problem {
+    int32_t T_max;        /* maximum tokens, >= 1 */
+    int32_t E;            /* experts, 1..1024 */
+    int32_t k;            /* experts per token, 1..64, at most topk_group * E / n_group */
+    int32_t H;            /* hidden size, multiple of 64 */
+    int32_t score;        /* moe_score_t */
+    int32_t renormalize;  /* 1: a token's k scores are divided by their sum */
+    int32_t n_group;      /* groups of consecutive experts, 1..32, dividing E; 1: no groups */
+    int32_t topk_group;   /* groups kept per token, 1..n_group */
+    int32_t group_top;    /* a group's value is the sum of its 1 or 2 largest keys */
+    float scale;          /* the weights are multiplied by it; finite */
+} moe_router_problem_t;
+
+/* Bytes of workspace of moe_route (pure host). Zero-filled before its first
+ * use, like every workspace; holds the device error word at its start. */
+moe_status_t moe_route_workspace_size(const moe_router_problem_t *problem, size_t *bytes);
+
+/*
+ * Router: logits[t, e] = sum_m x[t, m] w_router[e, m] in fp32, the score of
+ * each expert, and the k experts of the largest keys.
+ *  - key = score + bias; without a bias and with group_top = 1 the logit
+ *    itself (the same order, with no ties from rounding the score);
+ *  - n_group > 1: only the topk_group groups of the largest value keep their
+ *    experts (ties to the lower group);
+ *  - ids in descending key order, ties to the lower expert;
+ *  - weight = scale * score (without the bias), divided by the sum of the
+ *    chosen scores when renormalize is set.
+ * An expert whose key is -inf or NaN is never chosen: a bias of -inf switches
+ * an expert off. A token with fewer than k such experts gets id -1 (a dropped
+ * slot for moe_dispatch) and weight 0 in the remaining places. A logit that
+ * is NaN or +inf sets MOE_DEVERR_BAD_LOGIT and is taken as -inf.
+ *   x[T_max, H] bf16, w_router[E, H] bf16, bias[E] fp32 or NULL,
+ *   topk_ids[T_max, k] int32 and topk_weights[T_max, k] fp32 out,
+ *   logits[T_max, E] fp32 out or NULL.
+ * Deterministic. ws as moe_route_workspace_size says; the calls that share
+ * one workspace are ordered on one stream.
+ */
+moe_status_t moe_route(const moe_router_problem_t *problem, const void *x, const void *w_router, const float *bias,
+                       const int32_t *d_num_tokens, int32_t *topk_ids, float *topk_weights, float *logits, void *ws,
+                       size_t ws_bytes, void *stream);
+
+#define MOE_LAYER_MAX_TOKENS 128
+
+/* The three parts agree in T_max (at most MOE_LAYER_MAX_TOKENS), H, E and k;
+ * H is at most 16384. */
+typedef struct moe_layer_problem {
+    moe_problem_t experts;
+    moe_router_problem_t router;
+    moe_norm_problem_t norm;
+} moe_layer_problem_t;
+
+moe_status_t moe_layer_workspace_size(const moe_layer_problem_t *problem, size_t *bytes);
+
+/*
+ * The whole block for a few tokens (a decode step):
+ *   v = h * r(h) * w_pre            the norm, unrounded
+ *   ids, weights = the router on v  (as moe_route, but on v before its rounding)
+ *   y = the experts on bf16(v), weighted and summed, unrounded
+ *   h_out, x_next                   as moe_norm_residual, from y before its rounding
+ * Arguments as in moe_norm, moe_route, moe_forward and moe_norm_residual;
+ * w_pre, w_post and w_next follow norm.w_dtype. topk_ids, topk_weights,
+ * expert_offsets and perm are outputs. More tokens than MOE_LAYER_MAX_TOKENS
+ * return MOE_ERR_SHAPE: call moe_norm, moe_route, moe_forward and
+ * moe_norm_residual in turn (there the router reads the rounded x).
+ */
+moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const void *w_pre, const void *w_router,
+                       const float *bias, const void *W13, const void *W2, const void *w_post, const void *gate,
+                       const void *w_next, const int32_t *d_num_tokens, int32_t *topk_ids, float *topk_weights,
+                       int32_t *expert_offsets, int32_t *perm, void *h_out, void *x_next, void *ws, size_t ws_bytes,
+                       void *stream);
 
 /* Read the sticky device error word of `ws` into *host_code (0 = none).
  * Synchronises `stream` (the only entry point that does). */

@@ -29,6 +29,16 @@ MOE_FORWARD_ONE_KERNEL = 2
 MOE_DEVERR_BAD_EXPERT_ID = 0x1
 MOE_DEVERR_WAIT_TIMEOUT = 0x2
 MOE_DEVERR_Y_RANGE = 0x4
+MOE_DEVERR_BAD_LOGIT = 0x8
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP32 = 1
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+MOE_GATE_ELEMENT = 3
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_LAYER_MAX_TOKENS = 128
 
 #: every symbol include/moe.h declares
 EXPORTED_SYMBOLS = (
@@ -47,6 +57,12 @@ EXPORTED_SYMBOLS = (
     "moe_last_device_error",
     "moe_clear_device_error",
     "moe_status_string",
+    "moe_norm",
+    "moe_norm_residual",
+    "moe_route_workspace_size",
+    "moe_route",
+    "moe_layer_workspace_size",
+    "moe_layer",
 )
 
 
@@ -85,6 +101,88 @@ class Problem(ctypes.Structure):
         return (f"Problem(T_max={self.T_max}, E={self.E}, k={self.k}, H={self.H}, I={self.I}, "
                 f"capacity={self.capacity}, path={self.path}, weight_layout={self.weight_layout}, "
                 f"forward_form={self.forward_form})")
+
+
+_DTYPE_CODES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_FP32}
+
+
+def _dtype_code(dtype) -> int:
+    """moe_dtype_t of a torch dtype (or the code itself)."""
+    if isinstance(dtype, int):
+        return dtype
+    if dtype not in _DTYPE_CODES:
+        raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, not {dtype}")
+    return _DTYPE_CODES[dtype]
+
+
+class NormProblem(ctypes.Structure):
+    """``moe_norm_problem_t``: sizes, types, gate kind, eps, residual scale and row strides (0 = H)."""
+
+    _fields_ = [
+        ("T_max", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("h_dtype", ctypes.c_int32),
+        ("w_dtype", ctypes.c_int32),
+        ("unit_offset", ctypes.c_int32),
+        ("norm_block", ctypes.c_int32),
+        ("gate", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("residual_scale", ctypes.c_float),
+        ("h_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("gate_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, T_max, H, h_dtype=torch.bfloat16, w_dtype=torch.bfloat16, eps=1e-6, unit_offset=False,
+             norm_block=False, gate=MOE_GATE_NONE, residual_scale=1.0, h_stride=0, y_stride=0, x_stride=0,
+             out_stride=0, gate_stride=0):
+        return cls(int(T_max), int(H), _dtype_code(h_dtype), _dtype_code(w_dtype), int(unit_offset), int(norm_block),
+                   int(gate), float(eps), float(residual_scale), int(h_stride), int(y_stride), int(x_stride),
+                   int(out_stride), int(gate_stride))
+
+    @property
+    def h_torch(self):
+        return torch.float32 if self.h_dtype == MOE_DTYPE_FP32 else torch.bfloat16
+
+    @property
+    def w_torch(self):
+        return torch.float32 if self.w_dtype == MOE_DTYPE_FP32 else torch.bfloat16
+
+
+class RouterProblem(ctypes.Structure):
+    """``moe_router_problem_t``: sizes, score, groups and weight scale."""
+
+    _fields_ = [
+        ("T_max", ctypes.c_int32),
+        ("E", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("n_group", ctypes.c_int32),
+        ("topk_group", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+    @classmethod
+    def make(cls, T_max, E, k, H, score=MOE_SCORE_SOFTMAX, renormalize=True, n_group=1, topk_group=1, group_top=1,
+             scale=1.0):
+        return cls(int(T_max), int(E), int(k), int(H), int(score), int(renormalize), int(n_group), int(topk_group),
+                   int(group_top), float(scale))
+
+
+class LayerProblem(ctypes.Structure):
+    """``moe_layer_problem_t``: the experts', the router's and the norms' descriptions together."""
+
+    _fields_ = [("experts", Problem), ("router", RouterProblem), ("norm", NormProblem)]
+
+    @classmethod
+    def make(cls, experts: Problem, router: RouterProblem, norm: NormProblem):
+        return cls(experts, router, norm)
 
 
 class Profile(ctypes.Structure):
@@ -145,6 +243,20 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.moe_last_device_error.restype = st
     lib.moe_clear_device_error.argtypes = [_vp, _vp]
     lib.moe_clear_device_error.restype = st
+    NP, RP, LP = ctypes.POINTER(NormProblem), ctypes.POINTER(RouterProblem), ctypes.POINTER(LayerProblem)
+    sz = ctypes.POINTER(ctypes.c_size_t)
+    lib.moe_norm.argtypes = [NP] + [_vp] * 5
+    lib.moe_norm.restype = st
+    lib.moe_norm_residual.argtypes = [NP] + [_vp] * 9
+    lib.moe_norm_residual.restype = st
+    lib.moe_route_workspace_size.argtypes = [RP, sz]
+    lib.moe_route_workspace_size.restype = st
+    lib.moe_route.argtypes = [RP] + [_vp] * 8 + [ctypes.c_size_t, _vp]
+    lib.moe_route.restype = st
+    lib.moe_layer_workspace_size.argtypes = [LP, sz]
+    lib.moe_layer_workspace_size.restype = st
+    lib.moe_layer.argtypes = [LP] + [_vp] * 17 + [ctypes.c_size_t, _vp]
+    lib.moe_layer.restype = st
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -183,6 +295,26 @@ def _need(t, name: str, dtype, numel: int):
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.numel() < numel:
         raise ValueError(f"{name} holds {t.numel()} elements; the problem needs at least {numel}")
+
+
+def _need_rows(t, name: str, dtype, rows: int, cols: int, stride: int) -> int | None:
+    """Pointer of a [rows, cols] tensor whose rows lie ``stride`` elements
+    apart (0 = cols, contiguous), checked as _need does."""
+    if t is None or isinstance(t, int):
+        return t
+    stride = stride or cols
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (device memory), not on {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.is_contiguous() and stride == cols:
+        if t.numel() < rows * cols:
+            raise ValueError(f"{name} holds {t.numel()} elements; the problem needs at least {rows * cols}")
+    elif (t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols or t.stride(1) != 1 or
+          (rows > 1 and t.stride(0) != stride)):
+        raise ValueError(f"{name} must be [{rows}, {cols}] with rows {stride} elements apart, not "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
 
 
 def _need_weights(problem, W13, W2):
@@ -347,6 +479,98 @@ def moe_quantize_weights(problem, W13, W2, W13_mx=None, W2_mx=None, stream=None)
     _check(load_library().moe_quantize_weights(ctypes.byref(problem), _ptr(W13), _ptr(W2), _ptr(W13_mx),
                                                _ptr(W2_mx), _stream(stream)), "moe_quantize_weights")
     return W13_mx, W2_mx
+
+
+def moe_norm(problem: NormProblem, h, w, x, d_num_tokens=None, stream=None):
+    """x = norm(h) * w; see include/moe.h."""
+    p = problem
+    h = _need_rows(h, "h", p.h_torch, p.T_max, p.H, p.h_stride)
+    _need(w, "w", p.w_torch, p.H)
+    _need(d_num_tokens, "d_num_tokens", torch.int32, 1)
+    x = _need_rows(x, "x", torch.bfloat16, p.T_max, p.H, p.x_stride)
+    _check(load_library().moe_norm(ctypes.byref(p), h, _ptr(w), _ptr(d_num_tokens), x, _stream(stream)), "moe_norm")
+
+
+def _need_residual(p: NormProblem, h, w_post, gate, w_next, h_out, x_next):
+    """Checked pointers (h, gate, h_out, x_next) of the way back into the residual stream."""
+    _need(w_post, "w_post", p.w_torch, p.H)
+    _need(w_next, "w_next", p.w_torch, p.H)
+    if p.gate == MOE_GATE_CHANNEL:
+        _need(gate, "gate", p.w_torch, p.H)
+        gate = _ptr(gate)
+    elif p.gate == MOE_GATE_TOKEN:
+        _need(gate, "gate", torch.float32, p.T_max)
+        gate = _ptr(gate)
+    elif p.gate == MOE_GATE_ELEMENT:
+        gate = _need_rows(gate, "gate", torch.bfloat16, p.T_max, p.H, p.gate_stride)
+    elif gate is not None:
+        raise ValueError("gate given, but the problem has none")
+    return (_need_rows(h, "h", p.h_torch, p.T_max, p.H, p.h_stride), gate,
+            _need_rows(h_out, "h_out", p.h_torch, p.T_max, p.H, p.out_stride),
+            _need_rows(x_next, "x_next", torch.bfloat16, p.T_max, p.H, p.x_stride))
+
+
+def moe_norm_residual(problem: NormProblem, h, y, h_out, w_post=None, gate=None, w_next=None, x_next=None,
+                      d_num_tokens=None, stream=None):
+    """h_out = h + scale * gate * norm(y) * w_post, and x_next = norm(h_out) * w_next; see include/moe.h."""
+    p = problem
+    h, gate, h_out, x_next = _need_residual(p, h, w_post, gate, w_next, h_out, x_next)
+    y = _need_rows(y, "y", torch.bfloat16, p.T_max, p.H, p.y_stride)
+    _need(d_num_tokens, "d_num_tokens", torch.int32, 1)
+    _check(load_library().moe_norm_residual(ctypes.byref(p), h, y, _ptr(w_post), gate, _ptr(w_next),
+                                            _ptr(d_num_tokens), h_out, x_next, _stream(stream)), "moe_norm_residual")
+
+
+def moe_route_workspace_size(problem: RouterProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_route_workspace_size(ctypes.byref(problem), ctypes.byref(n)),
+           "moe_route_workspace_size")
+    return n.value
+
+
+def _need_router(p: RouterProblem, w_router, bias, topk_ids, topk_weights, d_num_tokens):
+    _need(w_router, "w_router", torch.bfloat16, p.E * p.H)
+    _need(bias, "bias", torch.float32, p.E)
+    _need(topk_ids, "topk_ids", torch.int32, p.T_max * p.k)
+    _need(topk_weights, "topk_weights", torch.float32, p.T_max * p.k)
+    _need(d_num_tokens, "d_num_tokens", torch.int32, 1)
+
+
+def moe_route(problem: RouterProblem, x, w_router, topk_ids, topk_weights, ws, bias=None, logits=None,
+              d_num_tokens=None, stream=None):
+    """Logits, the k experts of the largest keys and their weights; see include/moe.h."""
+    p = problem
+    _need(x, "x", torch.bfloat16, p.T_max * p.H)
+    _need_router(p, w_router, bias, topk_ids, topk_weights, d_num_tokens)
+    _need(logits, "logits", torch.float32, p.T_max * p.E)
+    _need(ws, "ws", None, 0)
+    _check(load_library().moe_route(ctypes.byref(p), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(d_num_tokens),
+                                    _ptr(topk_ids), _ptr(topk_weights), _ptr(logits), _ptr(ws),
+                                    ws.numel() * ws.element_size(), _stream(stream)), "moe_route")
+
+
+def moe_layer_workspace_size(problem: LayerProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_layer_workspace_size(ctypes.byref(problem), ctypes.byref(n)),
+           "moe_layer_workspace_size")
+    return n.value
+
+
+def moe_layer(problem: LayerProblem, h, w_pre, w_router, W13, W2, topk_ids, topk_weights, expert_offsets, perm, h_out,
+              ws, bias=None, w_post=None, gate=None, w_next=None, x_next=None, d_num_tokens=None, stream=None):
+    """Norm, router, experts and the way back into the residual stream, for a few tokens; see include/moe.h."""
+    p = problem
+    h, gate, h_out, x_next = _need_residual(p.norm, h, w_post, gate, w_next, h_out, x_next)
+    _need(w_pre, "w_pre", p.norm.w_torch, p.norm.H)
+    _need_router(p.router, w_router, bias, topk_ids, topk_weights, d_num_tokens)
+    _need_weights(p.experts, W13, W2)
+    _need(expert_offsets, "expert_offsets", torch.int32, p.experts.E + 1)
+    _need(perm, "perm", torch.int32, p.experts.cap)
+    _need(ws, "ws", None, 0)
+    _check(load_library().moe_layer(ctypes.byref(p), h, _ptr(w_pre), _ptr(w_router), _ptr(bias), _ptr(W13), _ptr(W2),
+                                    _ptr(w_post), gate, _ptr(w_next), _ptr(d_num_tokens), _ptr(topk_ids),
+                                    _ptr(topk_weights), _ptr(expert_offsets), _ptr(perm), h_out, x_next, _ptr(ws),
+                                    ws.numel() * ws.element_size(), _stream(stream)), "moe_layer")
 
 
 def moe_last_device_error(ws, stream=None) -> int:

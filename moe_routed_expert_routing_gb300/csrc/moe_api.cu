@@ -412,6 +412,8 @@ long long dispatch_blocks(const moe_problem_t &p)
 
 moe_status_t validate_device() { return check_device(); }
 
+size_t workspace_header_bytes() { return kHeaderBytes; }
+
 bool use_pdl(const moe_problem_t &problem)
 {
     int path = 0, tile_rows = 0;

@@ -212,6 +212,44 @@ cudaError_t launch_fused_small(const GemmProblem &up, const GemmProblem &down, i
 // and `slots` = T_max * k routed slots fit next to its pipeline on this device.
 bool fused_mega_fits(int E, long long slots, bool mxfp8);
 
+// ---- norms around the block (norm.cu) ----
+struct NormArgs {
+    const void *h;             // residual stream, bf16 or fp32
+    const void *y;             // block output, bf16 (null: norm of h only)
+    const void *w_post;        // null: no weight
+    const void *gate;
+    const void *w_next;        // weight of x_next (moe_norm: of x); null: no weight
+    const int32_t *d_num_tokens;
+    void *h_out;
+    void *x;                   // x_next (moe_norm: x), bf16; null: not computed
+    float *x_f32;              // x before its rounding, or null: not wanted
+    int T_max, H;
+    int h_f32, w_f32, unit_offset, norm_block, gate_kind;
+    float eps, scale;
+    long long h_stride, y_stride, x_stride, out_stride, gate_stride;
+};
+
+// x = norm(h) (y null), or h_out = h + s * g * norm(y) and x = norm(h_out).
+cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t stream, bool pdl);
+
+// ---- router (route.cu) ----
+struct RouteArgs {
+    const void *x;             // [T_max, H] bf16 (fp32 when x_f32 is set)
+    const void *w;             // [E, H] bf16
+    const float *bias;         // null: none
+    const int32_t *d_num_tokens;
+    int32_t *ids;
+    float *weights;
+    float *logits;             // [T_max, E]: the caller's or the workspace's
+    int32_t *err;
+    int T_max, E, k, H;
+    int sigmoid, renormalize, n_group, topk_group, group_top;
+    int x_f32;
+    float scale;
+};
+
+cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t stream, bool pdl);
+
 // number of SMs of the current device (cached)
 int device_sm_count();
 
@@ -222,6 +260,9 @@ int capacity_of(const moe_problem_t &problem);
 // blocks of the multi-block dispatch: one per kDispatchSlotsPerBlock routed slots
 long long dispatch_blocks(const moe_problem_t &problem);
 moe_status_t validate_device();
+// bytes at the start of every workspace: the device error word and the
+// counters that kernels leave at zero (moe_clear_device_error clears them)
+size_t workspace_header_bytes();
 // whether launches for this problem use programmatic dependent launch (M-small path)
 bool use_pdl(const moe_problem_t &problem);
 
