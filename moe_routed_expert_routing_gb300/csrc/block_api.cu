@@ -88,16 +88,16 @@ moe_status_t check_router(const moe_router_problem_t *p)
     return MOE_OK;
 }
 
-// Workspace of moe_route: the header (error word and counters), then the logits.
+// Workspace of moe_route: the header (error word and counters), then the router's scratch.
 struct RouteLayout {
-    size_t logits, total;
+    size_t part, total;
 };
 
 RouteLayout route_layout(const moe_router_problem_t &p)
 {
     RouteLayout L;
-    L.logits = workspace_header_bytes();
-    L.total = align_up(L.logits + sizeof(float) * static_cast<size_t>(p.T_max) * p.E);
+    L.part = workspace_header_bytes();
+    L.total = align_up(L.part + sizeof(float) * route_scratch_floats(p.T_max, p.E, p.H));
     return L;
 }
 
@@ -114,6 +114,7 @@ RouteArgs route_args(const moe_router_problem_t &p)
     a.topk_group = p.topk_group;
     a.group_top = p.group_top;
     a.scale = p.scale;
+    a.x_stride = p.H;
     return a;
 }
 
@@ -134,7 +135,7 @@ moe_status_t check_layer(const moe_layer_problem_t *p)
 // Workspace of moe_layer: the one of moe_forward (header first), then the
 // normalised rows, the logits and the block's output.
 struct LayerLayout {
-    size_t forward, x, x_f32, logits, y, total;
+    size_t forward, x, part, y, total;
 };
 
 moe_status_t layer_layout(const moe_layer_problem_t &p, LayerLayout *L)
@@ -146,10 +147,8 @@ moe_status_t layer_layout(const moe_layer_problem_t &p, LayerLayout *L)
     size_t o = align_up(L->forward);
     L->x = o;
     o = align_up(o + 2 * T * H);
-    L->x_f32 = o;
-    o = align_up(o + 4 * T * H);
-    L->logits = o;
-    o = align_up(o + 4 * T * p.experts.E);
+    L->part = o;
+    o = align_up(o + sizeof(float) * route_scratch_floats(p.experts.T_max, p.experts.E, p.experts.H));
     L->y = o;
     o = align_up(o + 2 * T * H);
     L->total = o;
@@ -269,9 +268,11 @@ moe_status_t moe_route(const moe_router_problem_t *problem, const void *x, const
     a.d_num_tokens = d_num_tokens;
     a.ids = topk_ids;
     a.weights = topk_weights;
-    a.logits = logits ? logits : at<float>(ws, L.logits);
+    a.logits = logits;
     a.err = at<int32_t>(ws, 0);
-    return cuda_status(launch_route(a, device_sm_count(), static_cast<cudaStream_t>(stream), false));
+    a.counters = at<int32_t>(ws, route_counters_offset());
+    a.part = at<float>(ws, L.part);
+    return cuda_status(launch_route(a, device_sm_count(), static_cast<cudaStream_t>(stream), true));
 }
 
 moe_status_t moe_layer_workspace_size(const moe_layer_problem_t *problem, size_t *bytes)
@@ -307,46 +308,41 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
         return MOE_ERR_ALIGN;
     LayerLayout L = {};
     if ((st = layer_layout(p, &L)) != MOE_OK || (st = check_ws(ws, ws_bytes, L.total)) != MOE_OK ||
-        (st = validate_device()) != MOE_OK)
+        (st = validate_device()) != MOE_OK || (st = check_forward(p.experts)) != MOE_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int sms = device_sm_count();
     void *x = at<void>(ws, L.x);
     NormArgs n = norm_args(p.norm, d_num_tokens);
-    n.x_stride = p.norm.H;
     n.h = h;
-    n.w_next = w_pre;
-    n.x = x;
-    n.x_f32 = at<float>(ws, L.x_f32);
-    if ((st = cuda_status(launch_norm(n, sms, s, false))) != MOE_OK)
-        return st;
-    RouteArgs r = route_args(p.router);
-    r.x = n.x_f32;
-    r.x_f32 = 1;
-    r.w = w_router;
-    r.bias = bias;
-    r.d_num_tokens = d_num_tokens;
-    r.ids = topk_ids;
-    r.weights = topk_weights;
-    r.logits = at<float>(ws, L.logits);
-    r.err = at<int32_t>(ws, 0);
-    if ((st = cuda_status(launch_route(r, sms, s, false))) != MOE_OK)
-        return st;
-    void *y = at<void>(ws, L.y);
-    st = moe_forward(&p.experts, x, topk_ids, topk_weights, d_num_tokens, W13, W2, expert_offsets, perm, y, ws,
-                     L.forward, stream);
-    if (st != MOE_OK)
-        return st;
-    n = norm_args(p.norm, d_num_tokens);
-    n.y_stride = p.norm.H;
-    n.h = h;
-    n.y = y;
     n.w_post = w_post;
     n.gate = gate;
     n.w_next = w_next;
     n.h_out = h_out;
     n.x = x_next;
-    return cuda_status(launch_norm(n, sms, s, false));
+    // the norm, the router and the rounded rows in one kernel
+    RouteArgs r = route_args(p.router);
+    r.x = h;
+    r.x_stride = stride_of(p.norm.h_stride, p.norm.H);
+    r.normed = 1;
+    r.x_f32 = p.norm.h_dtype == MOE_DTYPE_FP32;
+    r.w_f32 = p.norm.w_dtype == MOE_DTYPE_FP32;
+    r.unit_offset = p.norm.unit_offset;
+    r.w_pre = w_pre;
+    r.eps = p.norm.eps;
+    r.x_out = x;
+    r.w = w_router;
+    r.bias = bias;
+    r.d_num_tokens = d_num_tokens;
+    r.ids = topk_ids;
+    r.weights = topk_weights;
+    r.err = at<int32_t>(ws, 0);
+    r.counters = at<int32_t>(ws, route_counters_offset());
+    r.part = at<float>(ws, L.part);
+    if ((st = cuda_status(launch_route(r, sms, s, true))) != MOE_OK)
+        return st;
+    return enqueue_forward(p.experts, x, topk_ids, topk_weights, d_num_tokens, W13, W2, expert_offsets, perm,
+                           at<void>(ws, L.y), ws, s, nullptr, &n);
 }
 
 }  // extern "C"

@@ -1,0 +1,235 @@
+// combine_residual.cu -- the end of moe_layer: the routing-weighted top-k sum
+// of the experts' rows (as combine.cu), normed, gated and scaled into the
+// residual stream, and the next block's norm, in one pass.
+//
+//   y[t, m] = sum_{j = 0..k-1} w[t, j] * y_sorted[inv[t*k + j], m]      (fp32, kept unrounded)
+//   h'      = h + s * g * (y * r(y) * w_post),  x_next = h' * r(h') * w_next
+//
+// A token's row goes over a cluster of eight CTAs: at one token a single SM
+// would have to pull all k rows (688 KB in 4 K parts at k=6, H=7168) through
+// its own L2 port. The two row sums meet through distributed shared memory;
+// each thread keeps its columns of y and h' in registers between them.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "moe_internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kClusterCtas = 8;
+constexpr int kTailThreads = 256;
+constexpr int kTailVecs = 2;      // float4 columns per thread: H <= 8 * 256 * 2 * 4 = 16384
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Sum of v over the cluster's threads, the same bits in every CTA: per warp,
+// per CTA in warp order, then over the CTAs in rank order. slot: this sum's own shared word.
+__device__ __forceinline__ float cluster_sum(float v, float *s_warp, float *slot)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0)
+        s_warp[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float c = 0.f;
+        for (int i = 0; i < kTailThreads / 32; ++i)
+            c += s_warp[i];
+        *slot = c;
+    }
+    cluster_sync();
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < kClusterCtas; ++i)
+        total += ld_cluster_f32(map_to_cta(smem_u32(slot), i));
+    return total;
+}
+
+__device__ __forceinline__ void load4(const void *p, bool f32, size_t i, float (&f)[4])
+{
+    if (f32) {
+        const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i);
+        f[0] = __uint_as_float(v.x << 16);
+        f[1] = __uint_as_float(v.x & 0xffff0000u);
+        f[2] = __uint_as_float(v.y << 16);
+        f[3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ void store4_bf16(void *p, size_t i, const float (&f)[4])
+{
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+    uint2 o;
+    o.x = *reinterpret_cast<const uint32_t *>(&lo);
+    o.y = *reinterpret_cast<const uint32_t *>(&hi);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + i) = o;
+}
+
+__device__ __forceinline__ void weight4(const NormArgs &a, const void *w, int m, float (&f)[4])
+{
+    if (!w) {
+        f[0] = f[1] = f[2] = f[3] = 1.f;
+        return;
+    }
+    load4(w, a.w_f32, m, f);
+    if (a.unit_offset)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = 1.f + f[i];
+}
+
+// Y: fp32, or fp16 (the tiled paths' intermediate). kParts: K parts of fp32 y,
+// part_stride elements apart, summed in part order as in combine.cu.
+template <typename Y, int kParts>
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThreads)
+    combine_residual_kernel(const Y *y_sorted, const int32_t *inv, const float *w, const __grid_constant__ NormArgs a,
+                            int k, size_t part_stride)
+{
+    __shared__ float s_warp[2][kTailThreads / 32];
+    __shared__ float s_slot[2];
+    pdl_wait();
+    pdl_trigger();
+    int T = a.T_max;
+    if (a.d_num_tokens) {
+        T = *a.d_num_tokens;
+        T = T < 0 ? 0 : (T > a.T_max ? a.T_max : T);
+    }
+    const int t = blockIdx.x / kClusterCtas;
+    if (t >= T)      // the whole cluster
+        return;
+    const int cols = a.H / kClusterCtas;             // a multiple of 8
+    const int m0 = static_cast<int>(cluster_ctarank()) * cols;
+    float y[kTailVecs][4];
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < kTailVecs; ++v) {
+        const int c = 4 * (threadIdx.x + v * kTailThreads);
+        y[v][0] = y[v][1] = y[v][2] = y[v][3] = 0.f;
+        if (c >= cols)
+            continue;
+        for (int j0 = 0; j0 < k; j0 += 4) {
+            float f[4][kParts][4];
+            int row[4];
+            float wj[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                row[q] = j0 + q < k ? inv[t * k + j0 + q] : -1;
+                wj[q] = j0 + q < k ? w[t * k + j0 + q] : 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+                    if (row[q] >= 0) {
+                        const Y *src = y_sorted + p * part_stride + static_cast<size_t>(row[q]) * a.H + m0 + c;
+                        if constexpr (sizeof(Y) == 2) {
+                            const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                            const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+                            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+                            f[q][p][0] = lo.x; f[q][p][1] = lo.y; f[q][p][2] = hi.x; f[q][p][3] = hi.y;
+                        } else {
+                            const float4 u = *reinterpret_cast<const float4 *>(src);
+                            f[q][p][0] = u.x; f[q][p][1] = u.y; f[q][p][2] = u.z; f[q][p][3] = u.w;
+                        }
+                    }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (row[q] < 0)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float s = f[q][0][i];
+#pragma unroll
+                    for (int p = 1; p < kParts; ++p)
+                        s = __fadd_rn(s, f[q][p][i]);
+                    y[v][i] = __fadd_rn(y[v][i], __fmul_rn(wj[q], s));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sum = fmaf(y[v][i], y[v][i], sum);
+    }
+    const float r_y = a.norm_block ? 1.f / sqrtf(cluster_sum(sum, s_warp[0], &s_slot[0]) / a.H + a.eps) : 1.f;
+    sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < kTailVecs; ++v) {
+        const int c = 4 * (threadIdx.x + v * kTailThreads);
+        if (c >= cols)
+            continue;
+        const int m = m0 + c;
+        float h[4], wp[4], g[4] = {1.f, 1.f, 1.f, 1.f};
+        load4(a.h, a.h_f32, t * a.h_stride + m, h);
+        if (a.norm_block)
+            weight4(a, a.w_post, m, wp);
+        else
+            wp[0] = wp[1] = wp[2] = wp[3] = 1.f;
+        if (a.gate_kind == MOE_GATE_CHANNEL)
+            load4(a.gate, a.w_f32, m, g);
+        else if (a.gate_kind == MOE_GATE_TOKEN)
+            g[0] = g[1] = g[2] = g[3] = static_cast<const float *>(a.gate)[t];
+        else if (a.gate_kind == MOE_GATE_ELEMENT)
+            load4(a.gate, false, t * a.gate_stride + m, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[v][i] = h[i] + a.scale * g[i] * (y[v][i] * r_y * wp[i]);
+            sum = fmaf(y[v][i], y[v][i], sum);
+        }
+        const size_t o = t * a.out_stride + m;
+        if (a.h_f32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.h_out) + o) =
+                make_float4(y[v][0], y[v][1], y[v][2], y[v][3]);
+        else
+            store4_bf16(a.h_out, o, y[v]);
+    }
+    if (a.x) {
+        const float r = 1.f / sqrtf(cluster_sum(sum, s_warp[1], &s_slot[1]) / a.H + a.eps);
+#pragma unroll
+        for (int v = 0; v < kTailVecs; ++v) {
+            const int c = 4 * (threadIdx.x + v * kTailThreads);
+            if (c >= cols)
+                continue;
+            float wn[4];
+            weight4(a, a.w_next, m0 + c, wn);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                wn[i] = y[v][i] * r * wn[i];
+            store4_bf16(a.x, t * a.x_stride + m0 + c, wn);
+        }
+    }
+    cluster_sync();   // no CTA leaves while another may still read its sums
+}
+
+}  // namespace
+
+cudaError_t launch_combine_residual(const void *y_sorted, bool y_f16, const int32_t *inv, const float *topk_weights,
+                                    const NormArgs &a, int k, int parts, size_t part_stride, cudaStream_t stream,
+                                    bool pdl)
+{
+    if ((y_f16 && parts != 1) || a.H > kClusterCtas * kTailThreads * kTailVecs * 4)
+        return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(a.T_max) * kClusterCtas), block(kTailThreads);
+    if (y_f16)
+        return launch_k(combine_residual_kernel<__half, 1>, grid, block, 0, stream, pdl,
+                        static_cast<const __half *>(y_sorted), inv, topk_weights, a, k, size_t(0));
+    auto kern = parts == 4 ? combine_residual_kernel<float, 4>
+                           : (parts == 2 ? combine_residual_kernel<float, 2> : combine_residual_kernel<float, 1>);
+    if (parts != 1 && parts != 2 && parts != 4)
+        return cudaErrorInvalidValue;
+    return launch_k(kern, grid, block, 0, stream, pdl, static_cast<const float *>(y_sorted), inv, topk_weights, a, k,
+                    part_stride);
+}
+
+}  // namespace moe

@@ -25,11 +25,12 @@ struct Layout {
 // it without the problem: the error word, then the fused decode kernel's
 // per-expert readiness counts and its three GPU-wide counters (CTAs through
 // their GEMM units, CTAs at the tail, units handed out), then the separate
-// grouped GEMMs' two (units handed out, CTAs at the tail). The kernels leave
+// grouped GEMMs' two (units handed out, CTAs at the tail), then the few-token
+// router's two (CTAs through with their units, CTAs out). The kernels leave
 // the counters at zero after every launch.
 constexpr size_t kReadyOffset = kAlign;
 constexpr size_t kCountersOffset = kReadyOffset + sizeof(int32_t) * kMaxExperts;
-constexpr size_t kHeaderBytes = (kCountersOffset + 5 * sizeof(int32_t) + kAlign - 1) / kAlign * kAlign;
+constexpr size_t kHeaderBytes = (kCountersOffset + 7 * sizeof(int32_t) + kAlign - 1) / kAlign * kAlign;
 
 void resolve(const moe_problem_t &p, int *path, int *tile_rows);
 
@@ -414,11 +415,129 @@ moe_status_t validate_device() { return check_device(); }
 
 size_t workspace_header_bytes() { return kHeaderBytes; }
 
+size_t route_counters_offset() { return kCountersOffset + 5 * sizeof(int32_t); }
+
 bool use_pdl(const moe_problem_t &problem)
 {
     int path = 0, tile_rows = 0;
     resolve(problem, &path, &tile_rows);
     return path == MOE_PATH_SMALL_M;
+}
+
+moe_status_t check_forward(const moe_problem_t &p)
+{
+    const moe_status_t st = check_form(p);
+    return st != MOE_OK ? st : check_layout_path(p);
+}
+
+moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_t *topk_ids,
+                             const float *topk_weights, const int32_t *d_num_tokens, const void *W13, const void *W2,
+                             int32_t *expert_offsets, int32_t *perm, void *out, void *ws, cudaStream_t s,
+                             void *const *stage_events, const NormArgs *tail)
+{
+    moe_status_t st = MOE_OK;
+    const Layout L = layout_of(p);
+    const int sms = device_sm_count();
+    int32_t *inv = at<int32_t>(ws, L.inv);
+    void *x_sorted = at<void>(ws, L.x_sorted);
+    float *y_sorted = at<float>(ws, L.y_sorted);
+    auto mark = [&](int i) { return record_stage(stage_events, i, s); };
+    int path = 0, tile_rows = 0;
+    resolve(p, &path, &tile_rows);
+    // decode-size batches (M-small, 16-row token tiles) whose dispatch tables
+    // fit in shared memory: the whole call is one persistent kernel (local
+    // dispatch in every CTA, both GEMMs, combine); its stage marks all fall
+    // after it.
+    if (use_megakernel(p)) {
+        MegaParams mp;
+        mp.ids = topk_ids;
+        mp.topk_w = topk_weights;
+        mp.d_num_tokens = d_num_tokens;
+        mp.T_max = p.T_max;
+        mp.expert_offsets_out = expert_offsets;
+        mp.perm_out = perm;
+        mp.out = out;
+        if ((st = mark(0)) != MOE_OK)
+            return st;
+        st = enqueue_expert_compute(p, x, nullptr, W13, W2, y_sorted, ws, s, nullptr, nullptr, nullptr, true, &mp);
+        for (int i = 1; st == MOE_OK && i < 6; ++i)
+            st = mark(i);
+        if (st == MOE_OK && tail) {
+            NormArgs n = *tail;
+            n.y = out;
+            n.y_stride = p.H;
+            st = cuda_status(launch_norm(n, sms, s, false));
+        }
+        return st;
+    }
+    // a down GEMM that splits K leaves its parts in the workspace's y buffers;
+    // the combine sums them in part order
+    const int parts = down_split_k(p, path, tile_rows, sms);
+    // decode-size batches (M-small, 16-row token tiles): both GEMMs run as one
+    // persistent kernel whose down units wait on per-expert counts (zero at
+    // every launch: the kernel clears them at its tail). Measured in one
+    // process against two launches: -1.3% per decode step; +2% on 32-row
+    // tiles, which keep two launches.
+    const bool fused_mlp = fused_mlp_of(p, path, tile_rows);
+    if ((st = mark(0)) != MOE_OK)
+        return st;
+    st = cuda_status(launch_dispatch(topk_ids, d_num_tokens, p.T_max, p.k, p.E, at<int32_t>(ws, L.block_counts),
+                                     at<int32_t>(ws, L.block_base), expert_offsets, perm, inv,
+                                     at<int32_t>(ws, L.err), s, use_pdl(p)));
+    if (st != MOE_OK || (st = mark(1)) != MOE_OK)
+        return st;
+    // On the M-small path the gate-up GEMM gathers its few rows per tile from x
+    // itself (tile::gather4, at most 16 per stage). The tiled paths read a
+    // materialised x_sorted: at 32 gather4 per 128-row stage the TMA issue rate,
+    // not the data, limited the gate-up GEMM (4.5x slower on the large shape).
+    const bool fused_gather = gemm_gathers_rows(p, path, tile_rows);
+    if (!fused_gather)
+        st = cuda_status(launch_gather_rows(x, perm, expert_offsets, p.E, p.k, p.H, capacity_of(p), x_sorted, sms, s,
+                                            use_pdl(p)));
+    if (st != MOE_OK || (st = mark(2)) != MOE_OK)
+        return st;
+    // tiled paths: y between the down GEMM and the combine in fp16 (half the
+    // bytes of the largest intermediate; within the output tolerance). The
+    // M-small path keeps fp32 (its y is small).
+    const bool y_f16 = path != MOE_PATH_SMALL_M;
+    // A few tokens with bf16 weights, whose dispatch tables fit the fused
+    // kernel's shared memory and whose gate-up units fit one wave on one SM
+    // fewer (so the fused kernel starts beside the dispatch block): the fused
+    // kernel dispatches the call's slots itself (the stable dispatch, the
+    // same tables) and starts its GEMM units without waiting for the dispatch
+    // kernel, which runs beside it for the caller's expert_offsets and perm
+    // and the combine's inv. Measured at one token, E=384, H=7168, I=3072, in
+    // one process, outputs bit-identical: 126.6 vs 127.5 us per call; at
+    // eight tokens (full grid) +1.9 us, so those keep the plain form.
+    const bool dispatch_beside = fused_mlp && megakernel_possible(p) && p.weight_layout != MOE_WEIGHTS_MXFP8 &&
+                                 fused_grid_sms(false, false, capacity_of(p), p.E, p.I, tile_rows, sms) < sms;
+    if (dispatch_beside) {
+        MegaParams mp;
+        mp.ids = topk_ids;
+        mp.topk_w = topk_weights;
+        mp.d_num_tokens = d_num_tokens;
+        mp.T_max = p.T_max;
+        mp.expert_offsets_out = expert_offsets;
+        mp.perm_out = perm;
+        mp.out = out;
+        mp.combine_apart = true;
+        st = enqueue_expert_compute(p, x, nullptr, W13, W2, y_sorted, ws, s, stage_events, nullptr, nullptr, true,
+                                    &mp);
+    } else {
+        st = enqueue_expert_compute(p, fused_gather ? x : x_sorted, expert_offsets, W13, W2, y_sorted, ws, s,
+                                    stage_events, nullptr, fused_gather ? perm : nullptr, fused_mlp, nullptr,
+                                    y_f16);
+    }
+    if (st != MOE_OK || (st = mark(4)) != MOE_OK)
+        return st;
+    if (tail)
+        return cuda_status(launch_combine_residual(y_sorted, y_f16, inv, topk_weights, *tail, p.k, parts,
+                                                   static_cast<size_t>(capacity_of(p)) * p.H, s, use_pdl(p)));
+    st = cuda_status(launch_combine(y_sorted, y_f16, inv, topk_weights, d_num_tokens, p.T_max, p.k, p.H, out, sms,
+                                    s, use_pdl(p), parts, static_cast<size_t>(capacity_of(p)) * p.H, true));
+    if (st != MOE_OK)
+        return st;
+    return mark(5);
 }
 
 }  // namespace moe
@@ -564,102 +683,10 @@ static moe_status_t forward_impl(const moe_problem_t *problem, const void *x, co
         return st;
     if ((st = check_device()) != MOE_OK)
         return st;
-    if ((st = check_form(p)) != MOE_OK || (st = check_layout_path(p)) != MOE_OK)
+    if ((st = check_forward(p)) != MOE_OK)
         return st;
-    const Layout L = layout_of(p);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int sms = device_sm_count();
-    int32_t *inv = at<int32_t>(ws, L.inv);
-    void *x_sorted = at<void>(ws, L.x_sorted);
-    float *y_sorted = at<float>(ws, L.y_sorted);
-    auto mark = [&](int i) { return record_stage(stage_events, i, s); };
-    int path = 0, tile_rows = 0;
-    resolve(p, &path, &tile_rows);
-    // decode-size batches (M-small, 16-row token tiles) whose dispatch tables
-    // fit in shared memory: the whole call is one persistent kernel (local
-    // dispatch in every CTA, both GEMMs, combine); its stage marks all fall
-    // after it.
-    if (use_megakernel(p)) {
-        MegaParams mp;
-        mp.ids = topk_ids;
-        mp.topk_w = topk_weights;
-        mp.d_num_tokens = d_num_tokens;
-        mp.T_max = p.T_max;
-        mp.expert_offsets_out = expert_offsets;
-        mp.perm_out = perm;
-        mp.out = out;
-        if ((st = mark(0)) != MOE_OK)
-            return st;
-        st = enqueue_expert_compute(p, x, nullptr, W13, W2, y_sorted, ws, s, nullptr, nullptr, nullptr, true, &mp);
-        for (int i = 1; st == MOE_OK && i < 6; ++i)
-            st = mark(i);
-        return st;
-    }
-    // a down GEMM that splits K leaves its parts in the workspace's y buffers;
-    // the combine sums them in part order
-    const int parts = down_split_k(p, path, tile_rows, sms);
-    // decode-size batches (M-small, 16-row token tiles): both GEMMs run as one
-    // persistent kernel whose down units wait on per-expert counts (zero at
-    // every launch: the kernel clears them at its tail). Measured in one
-    // process against two launches: -1.3% per decode step; +2% on 32-row
-    // tiles, which keep two launches.
-    const bool fused_mlp = fused_mlp_of(p, path, tile_rows);
-    if ((st = mark(0)) != MOE_OK)
-        return st;
-    st = cuda_status(launch_dispatch(topk_ids, d_num_tokens, p.T_max, p.k, p.E, at<int32_t>(ws, L.block_counts),
-                                     at<int32_t>(ws, L.block_base), expert_offsets, perm, inv,
-                                     at<int32_t>(ws, L.err), s, use_pdl(p)));
-    if (st != MOE_OK || (st = mark(1)) != MOE_OK)
-        return st;
-    // On the M-small path the gate-up GEMM gathers its few rows per tile from x
-    // itself (tile::gather4, at most 16 per stage). The tiled paths read a
-    // materialised x_sorted: at 32 gather4 per 128-row stage the TMA issue rate,
-    // not the data, limited the gate-up GEMM (4.5x slower on the large shape).
-    const bool fused_gather = gemm_gathers_rows(p, path, tile_rows);
-    if (!fused_gather)
-        st = cuda_status(launch_gather_rows(x, perm, expert_offsets, p.E, p.k, p.H, capacity_of(p), x_sorted, sms, s,
-                                            use_pdl(p)));
-    if (st != MOE_OK || (st = mark(2)) != MOE_OK)
-        return st;
-    // tiled paths: y between the down GEMM and the combine in fp16 (half the
-    // bytes of the largest intermediate; within the output tolerance). The
-    // M-small path keeps fp32 (its y is small).
-    const bool y_f16 = path != MOE_PATH_SMALL_M;
-    // A few tokens with bf16 weights, whose dispatch tables fit the fused
-    // kernel's shared memory and whose gate-up units fit one wave on one SM
-    // fewer (so the fused kernel starts beside the dispatch block): the fused
-    // kernel dispatches the call's slots itself (the stable dispatch, the
-    // same tables) and starts its GEMM units without waiting for the dispatch
-    // kernel, which runs beside it for the caller's expert_offsets and perm
-    // and the combine's inv. Measured at one token, E=384, H=7168, I=3072, in
-    // one process, outputs bit-identical: 126.6 vs 127.5 us per call; at
-    // eight tokens (full grid) +1.9 us, so those keep the plain form.
-    const bool dispatch_beside = fused_mlp && megakernel_possible(p) && p.weight_layout != MOE_WEIGHTS_MXFP8 &&
-                                 fused_grid_sms(false, false, capacity_of(p), p.E, p.I, tile_rows, sms) < sms;
-    if (dispatch_beside) {
-        MegaParams mp;
-        mp.ids = topk_ids;
-        mp.topk_w = topk_weights;
-        mp.d_num_tokens = d_num_tokens;
-        mp.T_max = p.T_max;
-        mp.expert_offsets_out = expert_offsets;
-        mp.perm_out = perm;
-        mp.out = out;
-        mp.combine_apart = true;
-        st = enqueue_expert_compute(p, x, nullptr, W13, W2, y_sorted, ws, s, stage_events, nullptr, nullptr, true,
-                                    &mp);
-    } else {
-        st = enqueue_expert_compute(p, fused_gather ? x : x_sorted, expert_offsets, W13, W2, y_sorted, ws, s,
-                                    stage_events, nullptr, fused_gather ? perm : nullptr, fused_mlp, nullptr,
-                                    y_f16);
-    }
-    if (st != MOE_OK || (st = mark(4)) != MOE_OK)
-        return st;
-    st = cuda_status(launch_combine(y_sorted, y_f16, inv, topk_weights, d_num_tokens, p.T_max, p.k, p.H, out, sms,
-                                    s, use_pdl(p), parts, static_cast<size_t>(capacity_of(p)) * p.H, true));
-    if (st != MOE_OK)
-        return st;
-    return mark(5);
+    return enqueue_forward(p, x, topk_ids, topk_weights, d_num_tokens, W13, W2, expert_offsets, perm, out, ws,
+                           static_cast<cudaStream_t>(stream), stage_events, nullptr);
 }
 
 moe_status_t moe_forward(const moe_problem_t *problem, const void *x, const int32_t *topk_ids,

@@ -222,7 +222,6 @@ struct NormArgs {
     const int32_t *d_num_tokens;
     void *h_out;
     void *x;                   // x_next (moe_norm: x), bf16; null: not computed
-    float *x_f32;              // x before its rounding, or null: not wanted
     int T_max, H;
     int h_f32, w_f32, unit_offset, norm_block, gate_kind;
     float eps, scale;
@@ -232,21 +231,66 @@ struct NormArgs {
 // x = norm(h) (y null), or h_out = h + s * g * norm(y) and x = norm(h_out).
 cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t stream, bool pdl);
 
+// The end of moe_layer (combine_residual.cu): combine into an unrounded y, then
+// as launch_norm with that y; y_sorted, inv, parts as launch_combine takes them.
+cudaError_t launch_combine_residual(const void *y_sorted, bool y_f16, const int32_t *inv, const float *topk_weights,
+                                    const NormArgs &a, int k, int parts, size_t part_stride, cudaStream_t stream,
+                                    bool pdl);
+
 // ---- router (route.cu) ----
 struct RouteArgs {
-    const void *x;             // [T_max, H] bf16 (fp32 when x_f32 is set)
+    const void *x;             // [T_max, H] bf16; moe_layer: the residual stream, x_f32 of either type
     const void *w;             // [E, H] bf16
     const float *bias;         // null: none
     const int32_t *d_num_tokens;
     int32_t *ids;
     float *weights;
-    float *logits;             // [T_max, E]: the caller's or the workspace's
+    float *logits;             // [T_max, E], or null: not wanted
     int32_t *err;
+    int32_t *counters;         // two, zero at launch and at exit (few tokens)
+    float *part;               // workspace, route_scratch_floats() of them
     int T_max, E, k, H;
     int sigmoid, renormalize, n_group, topk_group, group_top;
-    int x_f32;
     float scale;
+    // moe_layer: the router reads x * r(x) * w_pre before its rounding, and
+    // writes the rounded rows to x_out
+    int normed, x_f32, w_f32, unit_offset;
+    const void *w_pre;         // null: no weight
+    void *x_out;               // [T_max, H] bf16
+    long long x_stride;
+    float eps;
 };
+
+// The few-token kernel's split of [T_max, E, H]: units of 16 experts x one
+// slice of H x up to 64 tokens, about one per SM.
+struct RouteSplit {
+    int tiles;                 // 8-token tiles of a unit: 1, 2, 4 or 8
+    int chunks, groups, slices;
+};
+
+constexpr int kRouteFewTokens = 128;
+
+inline RouteSplit route_split(int T_max, int E, int H)
+{
+    RouteSplit r;
+    r.tiles = T_max <= 8 ? 1 : (T_max <= 16 ? 2 : (T_max <= 32 ? 4 : 8));
+    r.chunks = (T_max + 8 * r.tiles - 1) / (8 * r.tiles);
+    r.groups = (E + 15) / 16;
+    const int blocks = H / 64;
+    const int want = 152 / (r.groups * r.chunks);
+    r.slices = want < 1 ? 1 : (want < blocks ? want : blocks);
+    return r;
+}
+
+// Floats of scratch: the slices' partial logits and sums of squares (few
+// tokens), or the logits.
+inline size_t route_scratch_floats(int T_max, int E, int H)
+{
+    const size_t T = static_cast<size_t>(T_max);
+    if (T_max > kRouteFewTokens)
+        return T * E;
+    return static_cast<size_t>(route_split(T_max, E, H).slices) * T * (E + 1);
+}
 
 cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t stream, bool pdl);
 
@@ -260,9 +304,21 @@ int capacity_of(const moe_problem_t &problem);
 // blocks of the multi-block dispatch: one per kDispatchSlotsPerBlock routed slots
 long long dispatch_blocks(const moe_problem_t &problem);
 moe_status_t validate_device();
+// What moe_forward refuses beyond its pointers and workspace: a forward form
+// or weight layout that the shape cannot take.
+moe_status_t check_forward(const moe_problem_t &problem);
+// moe_forward after its checks. With `tail`, the combine's place is taken by
+// launch_combine_residual: `out` is scratch, and the block's output goes into
+// the residual stream as `tail` says.
+moe_status_t enqueue_forward(const moe_problem_t &problem, const void *x, const int32_t *topk_ids,
+                             const float *topk_weights, const int32_t *d_num_tokens, const void *W13, const void *W2,
+                             int32_t *expert_offsets, int32_t *perm, void *out, void *ws, cudaStream_t stream,
+                             void *const *stage_events, const NormArgs *tail);
 // bytes at the start of every workspace: the device error word and the
 // counters that kernels leave at zero (moe_clear_device_error clears them)
 size_t workspace_header_bytes();
+// byte offset in that header of the router's two counters
+size_t route_counters_offset();
 // whether launches for this problem use programmatic dependent launch (M-small path)
 bool use_pdl(const moe_problem_t &problem);
 

@@ -98,12 +98,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a)
         if (!a.x)
             continue;
         const float r = rsqrtf(block_sum(q) / a.H + a.eps);
-        for (int m = threadIdx.x; m < a.H; m += kNormThreads) {
-            const float v = row[m] * r * weight_at(a, a.w_next, m);
-            static_cast<__nv_bfloat16 *>(a.x)[static_cast<size_t>(t) * a.x_stride + m] = __float2bfloat16_rn(v);
-            if (a.x_f32)
-                a.x_f32[static_cast<size_t>(t) * a.H + m] = v;
-        }
+        for (int m = threadIdx.x; m < a.H; m += kNormThreads)
+            static_cast<__nv_bfloat16 *>(a.x)[static_cast<size_t>(t) * a.x_stride + m] =
+                __float2bfloat16_rn(row[m] * r * weight_at(a, a.w_next, m));
     }
 }
 

@@ -1,8 +1,29 @@
 // route.cu -- the router: logits of every expert, scores, and the k experts
 // of the largest keys with their weights.
+//
+//   logits[t, e] = sum_m x[t, m] w[e, m]        (x = h * r(h) * w_pre in moe_layer)
+//
+// Few tokens (T_max <= 128): one cooperative kernel. The router's weights are
+// the bytes that matter (5.5 MB at E=384, H=7168) and must come from every
+// SM at once, so a unit is 16 experts x a slice of H, about one unit per SM;
+// the slices' partial logits meet in the workspace behind one grid-wide
+// count, and then one CTA per token sums them in slice order and selects.
+// Products run on mma.sync m16n8k16 with the experts on M and 8 tokens on N:
+// at these sizes the tensor work is nothing, and fragments taken straight
+// from global memory need no staging. A dot product may take its terms in any
+// order, so each thread loads 16 consecutive bytes of a row and calls them
+// its fragment's K positions, for weights and tokens alike: every load is 16
+// bytes and nothing is permuted.
+//
+// In moe_layer the token operand is u = h * w_pre without r(h), which the sum
+// does not need before its end: logits = r * sum u w. u is split exactly into
+// bf16 parts (two when both factors are bf16: their product has 16 bits; three
+// parts, 24 bits, otherwise), one MMA each, so the router sees the normalised
+// row unrounded and no CTA waits for r.
 #include <cuda_bf16.h>
 
 #include "moe_internal.h"
+#include "ptx.cuh"
 
 namespace moe {
 
@@ -21,7 +42,7 @@ __device__ __forceinline__ int token_count(const int32_t *d_num_tokens, int T_ma
 }
 
 // logits[t, e] = sum_m x[t, m] w[e, m]: 64 x 64 tiles, 16-wide K steps, 4 x 4 per thread.
-__global__ void __launch_bounds__(256) logits_kernel(const RouteArgs a)
+__global__ void __launch_bounds__(256) logits_kernel(const RouteArgs a, float *logits)
 {
     __shared__ float sx[16][65], sw[16][65];
     const int T = token_count(a.d_num_tokens, a.T_max);
@@ -36,8 +57,7 @@ __global__ void __launch_bounds__(256) logits_kernel(const RouteArgs a)
             const size_t xi = static_cast<size_t>(t0 + r) * a.H + m0 + c;
             float v = 0.f;
             if (t0 + r < T)
-                v = a.x_f32 ? static_cast<const float *>(a.x)[xi]
-                            : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.x)[xi]);
+                v = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.x)[xi]);
             sx[c][r] = v;
             sw[c][r] = e0 + r < a.E ? __bfloat162float(static_cast<const __nv_bfloat16 *>(
                                           a.w)[static_cast<size_t>(e0 + r) * a.H + m0 + c])
@@ -56,7 +76,7 @@ __global__ void __launch_bounds__(256) logits_kernel(const RouteArgs a)
     for (int i = 0; i < 4; ++i)
         for (int j = 0; j < 4; ++j)
             if (t0 + ty * 4 + i < T && e0 + tx * 4 + j < a.E)
-                a.logits[static_cast<size_t>(t0 + ty * 4 + i) * a.E + e0 + tx * 4 + j] = acc[i][j];
+                logits[static_cast<size_t>(t0 + ty * 4 + i) * a.E + e0 + tx * 4 + j] = acc[i][j];
 }
 
 // A float as an unsigned integer of the same order; 0 for what may not be
@@ -88,13 +108,18 @@ __device__ __forceinline__ float warp_max(float v)
 // log of the sigmoid, without overflow or a loss of small values
 __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.f) - log1pf(expf(-fabsf(l))); }
 
-// One warp selects for one token: lane i holds the logits of experts i, i + 32, ...
-// s_key[E]: this warp's scratch, used with groups only.
+// One warp selects for one token whose logits lie in logits[E]; lane i holds
+// experts i, i + 32, ... s_key[E]: this warp's scratch, used with groups only
+// (it may be logits itself).
 template <int kPer>
-__device__ void select_experts(const RouteArgs &a, int t, float (&l)[kPer], float *s_key)
+__device__ __noinline__ void select_experts(const RouteArgs &a, int t, const float *logits, float *s_key)
 {
     const int lane = threadIdx.x & 31;
+    float l[kPer];
     bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        l[i] = lane + 32 * i < a.E ? logits[lane + 32 * i] : 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const bool real = lane + 32 * i < a.E;
@@ -226,41 +251,330 @@ __device__ void select_experts(const RouteArgs &a, int t, float (&l)[kPer], floa
     }
 }
 
+__device__ __forceinline__ void select_any(const RouteArgs &a, int t, const float *logits, float *s_key)
+{
+    if (a.E <= 128)
+        select_experts<4>(a, t, logits, s_key);
+    else if (a.E <= 256)
+        select_experts<8>(a, t, logits, s_key);
+    else if (a.E <= 512)
+        select_experts<16>(a, t, logits, s_key);
+    else
+        select_experts<32>(a, t, logits, s_key);
+}
+
+// ------------------------------------------------------------ many tokens
+
 constexpr int kSelectWarps = 4;
 
-template <int kPer>
-__global__ void __launch_bounds__(32 * kSelectWarps) select_kernel(const RouteArgs a)
+__global__ void __launch_bounds__(32 * kSelectWarps) select_kernel(const __grid_constant__ RouteArgs a,
+                                                                   const float *logits)
 {
-    __shared__ float s_key[kSelectWarps][kPer * 32];
+    extern __shared__ float s_keys[];   // [kSelectWarps][E], with groups only
     const int T = token_count(a.d_num_tokens, a.T_max);
-    const int t = blockIdx.x * kSelectWarps + (threadIdx.x >> 5);
-    if (t >= T)
-        return;
-    const int lane = threadIdx.x & 31;
-    float l[kPer];
+    const int warp = threadIdx.x >> 5;
+    const int t = blockIdx.x * kSelectWarps + warp;
+    if (t < T)
+        select_any(a, t, logits + static_cast<size_t>(t) * a.E, s_keys + warp * a.E);
+}
+
+// ------------------------------------------------------------- few tokens
+
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ float2 unpack_bf16(uint32_t u)
+{
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// Eight consecutive values of a bf16 or fp32 row.
+__device__ __forceinline__ void load8(const void *p, bool f32, size_t i, float (&f)[8])
+{
+    if (f32) {
+        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        const float4 x = __ldg(q), y = __ldg(q + 1);
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+    } else {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i));
+        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        l[i] = lane + 32 * i < a.E ? a.logits[static_cast<size_t>(t) * a.E + lane + 32 * i] : 0.f;
-    select_experts<kPer>(a, t, l, s_key[threadIdx.x >> 5]);
+        for (int j = 0; j < 4; ++j) {
+            const float2 g = unpack_bf16(v[j]);
+            f[2 * j] = g.x;
+            f[2 * j + 1] = g.y;
+        }
+    }
+}
+
+__device__ __forceinline__ void load_weight8(const RouteArgs &a, int m, float (&w)[8])
+{
+    if (!a.w_pre) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = 1.f;
+        return;
+    }
+    load8(a.w_pre, a.w_f32, m, w);
+    if (a.unit_offset)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = 1.f + w[i];
+}
+
+// kTiles: 8-token tiles of a unit. kParts: bf16 parts of the token operand;
+// 1: x as it is (moe_route), 2 or 3: u = h * w_pre (moe_layer).
+template <int kTiles, int kParts>
+__global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_constant__ RouteArgs a,
+                                                                   const RouteSplit sp, uint64_t wait_limit_ns)
+{
+    constexpr int kTok = 8 * kTiles;
+    __shared__ float s_acc[kFewWarps][16][kTok + 1];
+    __shared__ float s_sq[kFewWarps][kTok];
+    __shared__ float s_logits[kMaxExperts];
+    __shared__ int s_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, q = lane & 3;
+    const int E = a.E, H = a.H;
+    const int units = sp.groups * sp.slices * sp.chunks;
+    const int blocks64 = H / 64;
+    const __nv_bfloat16 *w = static_cast<const __nv_bfloat16 *>(a.w);
+    // this CTA's first weights on their way into L2 before the wait for the
+    // previous kernel (a prefetch reads nothing that kernel could still write)
+    if (static_cast<int>(blockIdx.x) < units) {
+        const int u = blockIdx.x;
+        const int e0 = (u % sp.groups) * 16, s = (u / sp.groups) % sp.slices;
+        const int m0 = 64 * (s * blocks64 / sp.slices), m1 = 64 * ((s + 1) * blocks64 / sp.slices);
+        const int lines = (m1 - m0) / 64;    // of 128 bytes, per row
+        for (int i = threadIdx.x; i < 16 * lines; i += kFewThreads)
+            if (e0 + i / lines < E)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(w + static_cast<size_t>(e0 + i / lines) * H + m0 +
+                                                              64 * (i % lines)));
+    }
+    pdl_wait();
+    pdl_trigger();
+    const int T = token_count(a.d_num_tokens, a.T_max);
+
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const int e0 = (u % sp.groups) * 16, s = (u / sp.groups) % sp.slices;
+        const int t0 = (u / sp.groups / sp.slices) * kTok;
+        if (t0 >= T)
+            break;
+        const int b0 = 2 * (s * blocks64 / sp.slices), b1 = 2 * ((s + 1) * blocks64 / sp.slices);   // 32-wide blocks
+        float acc[kTiles][4] = {};
+        float sq[kTiles] = {};
+        const bool lo_row = e0 + g < E, hi_row = e0 + g + 8 < E;
+        const uint4 *w_lo = reinterpret_cast<const uint4 *>(w + static_cast<size_t>(e0 + g) * H + 8 * q);
+        const uint4 *w_hi = reinterpret_cast<const uint4 *>(w + static_cast<size_t>(e0 + g + 8) * H + 8 * q);
+        const bool squares = kParts > 1 && e0 == 0;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        constexpr int kAhead = 4;            // weight blocks in flight per warp
+        for (int bb = b0 + warp; bb < b1; bb += kAhead * kFewWarps) {
+            uint4 wl[kAhead], wh[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int b = bb + i * kFewWarps;
+                wl[i] = (b < b1 && lo_row) ? __ldg(w_lo + 4 * b) : zero;
+                wh[i] = (b < b1 && hi_row) ? __ldg(w_hi + 4 * b) : zero;
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int b = bb + i * kFewWarps;
+                if (b >= b1)
+                    break;
+                const int m = 32 * b + 8 * q;
+                float wp[8];
+                if (kParts > 1)
+                    load_weight8(a, m, wp);
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                    const int t = t0 + 8 * j + g;
+                    const bool real = t < T;
+                    if (kParts == 1) {
+                        const uint4 xv = real ? __ldg(reinterpret_cast<const uint4 *>(
+                                                    static_cast<const __nv_bfloat16 *>(a.x) + t * a.x_stride + m))
+                                              : zero;
+                        mma_bf16(acc[j], wl[i].x, wh[i].x, wl[i].y, wh[i].y, xv.x, xv.y);
+                        mma_bf16(acc[j], wl[i].z, wh[i].z, wl[i].w, wh[i].w, xv.z, xv.w);
+                    } else {
+                        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        if (real)
+                            load8(a.x, a.x_f32, t * a.x_stride + m, f);
+                        if (squares)
+#pragma unroll
+                            for (int v = 0; v < 8; ++v)
+                                sq[j] = fmaf(f[v], f[v], sq[j]);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            f[v] *= wp[v];
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part) {
+                            uint32_t p[4];
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                p[v] = pack_bf16(f[2 * v], f[2 * v + 1]);
+                                const float2 taken = unpack_bf16(p[v]);
+                                f[2 * v] -= taken.x;
+                                f[2 * v + 1] -= taken.y;
+                            }
+                            mma_bf16(acc[j], wl[i].x, wh[i].x, wl[i].y, wh[i].y, p[0], p[1]);
+                            mma_bf16(acc[j], wl[i].z, wh[i].z, wl[i].w, wh[i].w, p[2], p[3]);
+                        }
+                    }
+                }
+            }
+        }
+        // the warps' sums (rows g and g + 8, tokens 2q and 2q + 1 of each tile) meet in shared memory
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+            s_acc[warp][g][8 * j + 2 * q] = acc[j][0];
+            s_acc[warp][g][8 * j + 2 * q + 1] = acc[j][1];
+            s_acc[warp][g + 8][8 * j + 2 * q] = acc[j][2];
+            s_acc[warp][g + 8][8 * j + 2 * q + 1] = acc[j][3];
+            if (squares) {
+                float v = sq[j];
+                v += __shfl_xor_sync(kFull, v, 1);
+                v += __shfl_xor_sync(kFull, v, 2);
+                if (q == 0)
+                    s_sq[warp][8 * j + g] = v;
+            }
+        }
+        __syncthreads();
+        float *part = a.part + static_cast<size_t>(s) * a.T_max * E;
+        for (int i = threadIdx.x; i < 16 * kTok; i += kFewThreads) {
+            const int r = i & 15, c = i >> 4;
+            if (e0 + r < E && t0 + c < T) {
+                float v = 0.f;
+#pragma unroll
+                for (int x = 0; x < kFewWarps; ++x)
+                    v += s_acc[x][r][c];
+                part[static_cast<size_t>(t0 + c) * E + e0 + r] = v;
+            }
+        }
+        if (squares)
+            for (int c = threadIdx.x; c < kTok; c += kFewThreads)
+                if (t0 + c < T) {
+                    float v = 0.f;
+                    for (int x = 0; x < kFewWarps; ++x)
+                        v += s_sq[x][c];
+                    a.part[static_cast<size_t>(sp.slices) * a.T_max * E + static_cast<size_t>(s) * a.T_max + t0 + c] = v;
+                }
+        __syncthreads();
+    }
+
+    // all units' partial sums are in the workspace once every CTA has counted
+    // itself; only the CTAs that select for a token wait (bounded)
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s_flag = 0;
+        atom_add_acq_rel_gpu(a.counters, 1);
+        if (static_cast<int>(blockIdx.x) < T) {
+            const uint64_t since = global_timer_ns();
+            while (ld_acquire_gpu(a.counters) < static_cast<int>(gridDim.x))
+                if (global_timer_ns() - since > wait_limit_ns) {
+                    s_flag = 1;
+                    atomicOr(a.err, MOE_DEVERR_WAIT_TIMEOUT);
+                    break;
+                }
+        }
+        // the last CTA past its wait returns the counters to zero
+        if (atom_add_acq_rel_gpu(a.counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+            a.counters[0] = 0;
+            a.counters[1] = 0;
+        }
+    }
+    __syncthreads();
+    if (s_flag)
+        return;
+    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+        float r = 1.f;
+        if (kParts > 1) {
+            float v = 0.f;
+            for (int s = 0; s < sp.slices; ++s)
+                v += __ldcg(a.part + static_cast<size_t>(sp.slices) * a.T_max * E + static_cast<size_t>(s) * a.T_max + t);
+            r = 1.f / sqrtf(v / H + a.eps);
+        }
+        for (int e = threadIdx.x; e < E; e += kFewThreads) {
+            float v = 0.f;
+            for (int s = 0; s < sp.slices; ++s)
+                v += __ldcg(a.part + (static_cast<size_t>(s) * a.T_max + t) * E + e);
+            v *= r;
+            s_logits[e] = v;
+            if (a.logits)
+                a.logits[static_cast<size_t>(t) * E + e] = v;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            select_any(a, t, s_logits, s_logits);
+        } else if (kParts > 1) {
+            // the normalised row for the experts, rounded to bf16 (their MMAs' operand type)
+            for (int m = 8 * (threadIdx.x - 32); m < H; m += 8 * (kFewThreads - 32)) {
+                float f[8], wp[8];
+                load8(a.x, a.x_f32, t * a.x_stride + m, f);
+                load_weight8(a, m, wp);
+                uint4 o;
+                o.x = pack_bf16(f[0] * r * wp[0], f[1] * r * wp[1]);
+                o.y = pack_bf16(f[2] * r * wp[2], f[3] * r * wp[3]);
+                o.z = pack_bf16(f[4] * r * wp[4], f[5] * r * wp[5]);
+                o.w = pack_bf16(f[6] * r * wp[6], f[7] * r * wp[7]);
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) + static_cast<size_t>(t) * H + m) = o;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int kTiles>
+cudaError_t launch_few(const RouteArgs &a, const RouteSplit &sp, int num_sms, cudaStream_t stream, bool pdl)
+{
+    const bool exact16 = !a.x_f32 && !a.unit_offset && (!a.w_pre || !a.w_f32);
+    auto kern = !a.normed ? route_few_kernel<kTiles, 1>
+                          : (exact16 ? route_few_kernel<kTiles, 2> : route_few_kernel<kTiles, 3>);
+    return launch_k_coresident(kern, static_cast<long long>(sp.groups) * sp.slices * sp.chunks, dim3(kFewThreads), 0,
+                               stream, pdl, num_sms, a, sp, kWaitLimitNs);
 }
 
 }  // namespace
 
 cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t stream, bool pdl)
 {
-    (void)num_sms;
-    (void)pdl;
-    cudaError_t e = launch_k(logits_kernel, dim3((a.T_max + 63) / 64, (a.E + 63) / 64), dim3(256), 0, stream, false, a);
+    if (a.T_max <= kRouteFewTokens) {
+        const RouteSplit sp = route_split(a.T_max, a.E, a.H);
+        switch (sp.tiles) {
+        case 1:
+            return launch_few<1>(a, sp, num_sms, stream, pdl);
+        case 2:
+            return launch_few<2>(a, sp, num_sms, stream, pdl);
+        case 4:
+            return launch_few<4>(a, sp, num_sms, stream, pdl);
+        default:
+            return launch_few<8>(a, sp, num_sms, stream, pdl);
+        }
+    }
+    float *logits = a.logits ? a.logits : a.part;
+    cudaError_t e = launch_k(logits_kernel, dim3((a.T_max + 63) / 64, (a.E + 63) / 64), dim3(256), 0, stream, false, a,
+                             logits);
     if (e != cudaSuccess)
         return e;
-    const dim3 grid((a.T_max + kSelectWarps - 1) / kSelectWarps), block(32 * kSelectWarps);
-    if (a.E <= 128)
-        return launch_k(select_kernel<4>, grid, block, 0, stream, false, a);
-    if (a.E <= 256)
-        return launch_k(select_kernel<8>, grid, block, 0, stream, false, a);
-    if (a.E <= 512)
-        return launch_k(select_kernel<16>, grid, block, 0, stream, false, a);
-    return launch_k(select_kernel<32>, grid, block, 0, stream, false, a);
+    return launch_k(select_kernel, dim3((a.T_max + kSelectWarps - 1) / kSelectWarps), dim3(32 * kSelectWarps),
+                    a.n_group > 1 ? sizeof(float) * kSelectWarps * a.E : 0, stream, false, a, logits);
 }
 
 }  // namespace moe
