@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["moe_api.cu", "dispatch.cu", "dispatch_noalloc.cu", "combine.cu", "grouped_gemm.cu", "weights_pack.cu",
-           "weights_mx.cu", "norm.cu", "route.cu", "combine_residual.cu", "block_api.cu"]
+           "weights_mx.cu", "norm.cu", "route.cu", "route_gemm.cu", "combine_residual.cu", "block_api.cu"]
 HEADERS = ["ptx.cuh", "moe_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

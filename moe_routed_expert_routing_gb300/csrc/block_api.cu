@@ -206,7 +206,7 @@ moe_status_t moe_norm(const moe_norm_problem_t *problem, const void *h, const vo
     a.h = h;
     a.w_next = w;
     a.x = x;
-    return cuda_status(launch_norm(a, device_sm_count(), static_cast<cudaStream_t>(stream), false));
+    return cuda_status(launch_norm(a, device_sm_count(), static_cast<cudaStream_t>(stream), true));
 }
 
 moe_status_t moe_norm_residual(const moe_norm_problem_t *problem, const void *h, const void *y, const void *w_post,
@@ -232,7 +232,7 @@ moe_status_t moe_norm_residual(const moe_norm_problem_t *problem, const void *h,
     a.w_next = w_next;
     a.h_out = h_out;
     a.x = x_next;
-    return cuda_status(launch_norm(a, device_sm_count(), static_cast<cudaStream_t>(stream), false));
+    return cuda_status(launch_norm(a, device_sm_count(), static_cast<cudaStream_t>(stream), true));
 }
 
 moe_status_t moe_route_workspace_size(const moe_router_problem_t *problem, size_t *bytes)

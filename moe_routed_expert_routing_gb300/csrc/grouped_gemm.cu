@@ -2257,6 +2257,11 @@ cudaError_t run_fused(const GemmProblem &up, const GemmProblem &down, int32_t *r
 
 }  // namespace
 
+bool make_tile_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows)
+{
+    return make_map(m, base, rows, cols, box_rows);
+}
+
 cudaError_t launch_grouped_gemm(const GemmProblem &p, int num_sms, cudaStream_t stream)
 {
     if (p.w_mxfp8)   // MXFP8 weights run through the fused M-small kernel only

@@ -466,7 +466,7 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
             NormArgs n = *tail;
             n.y = out;
             n.y_stride = p.H;
-            st = cuda_status(launch_norm(n, sms, s, false));
+            st = cuda_status(launch_norm(n, sms, s, true));
         }
         return st;
     }

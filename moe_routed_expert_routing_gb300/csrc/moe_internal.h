@@ -292,7 +292,44 @@ inline size_t route_scratch_floats(int T_max, int E, int H)
     return static_cast<size_t>(route_split(T_max, E, H).slices) * T * (E + 1);
 }
 
+// The tensor-core logits' tile (route_gemm.cu): experts of a tile and the CTAs
+// of a cluster that share one 128-token tile's K.
+struct RouteTile {
+    int experts, slices;
+};
+
+// The pair with the shortest estimate: waves of CTAs over 152 SMs, each its K
+// blocks at the larger of their MMA cycles and their operand bytes at 64 a
+// cycle, plus the exchange of the partial rows and a fixed start and end.
+inline RouteTile route_tile(int T_max, int E, int H)
+{
+    RouteTile best = {64, 1};
+    double best_cycles = 1e30;
+    for (int n = 64; n <= 256; n += 64) {
+        if (n > 64 && n - 64 >= E)
+            break;
+        for (int s = 1; s <= 8 && s <= H / 64; s *= 2) {
+            const double ctas = static_cast<double>((T_max + 127) / 128) * ((E + n - 1) / n) * s;
+            const double waves = static_cast<double>(static_cast<long long>((ctas + 151) / 152));
+            const double block = 2.0 * n > 2.0 * (128 + n) ? 2.0 * n : 2.0 * (128 + n);
+            const double cycles = waves * (3000.0 + (H / 64 + s - 1) / s * block + (s > 1 ? 128.0 * n * 4 / 32 : 0));
+            if (cycles < best_cycles) {
+                best_cycles = cycles;
+                best = {n, s};
+            }
+        }
+    }
+    return best;
+}
+
+// logits[t, e] for the rows t < T (T_max > kRouteFewTokens)
+cudaError_t launch_route_gemm(const RouteArgs &a, float *logits, cudaStream_t stream, bool pdl);
+
 cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t stream, bool pdl);
+
+// 2-D bf16 tensor map [rows, cols] (cols contiguous), box of 64 columns x
+// box_rows rows, 128-byte swizzle (grouped_gemm.cu).
+bool make_tile_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 
 // number of SMs of the current device (cached)
 int device_sm_count();

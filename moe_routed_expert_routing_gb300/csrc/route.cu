@@ -15,6 +15,9 @@
 // its fragment's K positions, for weights and tokens alike: every load is 16
 // bytes and nothing is permuted.
 //
+// More tokens: logits on the tensor cores (route_gemm.cu), then a warp per
+// token selects.
+//
 // In moe_layer the token operand is u = h * w_pre without r(h), which the sum
 // does not need before its end: logits = r * sum u w. u is split exactly into
 // bf16 parts (two when both factors are bf16: their product has 16 bits; three
@@ -39,44 +42,6 @@ __device__ __forceinline__ int token_count(const int32_t *d_num_tokens, int T_ma
         T = T < 0 ? 0 : (T > T_max ? T_max : T);
     }
     return T;
-}
-
-// logits[t, e] = sum_m x[t, m] w[e, m]: 64 x 64 tiles, 16-wide K steps, 4 x 4 per thread.
-__global__ void __launch_bounds__(256) logits_kernel(const RouteArgs a, float *logits)
-{
-    __shared__ float sx[16][65], sw[16][65];
-    const int T = token_count(a.d_num_tokens, a.T_max);
-    const int t0 = blockIdx.x * 64, e0 = blockIdx.y * 64;
-    if (t0 >= T)
-        return;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int m0 = 0; m0 < a.H; m0 += 16) {
-        for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-            const int r = i >> 4, c = i & 15;
-            const size_t xi = static_cast<size_t>(t0 + r) * a.H + m0 + c;
-            float v = 0.f;
-            if (t0 + r < T)
-                v = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.x)[xi]);
-            sx[c][r] = v;
-            sw[c][r] = e0 + r < a.E ? __bfloat162float(static_cast<const __nv_bfloat16 *>(
-                                          a.w)[static_cast<size_t>(e0 + r) * a.H + m0 + c])
-                                    : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] += sx[c][ty * 4 + i] * sw[c][tx * 4 + j];
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j)
-            if (t0 + ty * 4 + i < T && e0 + tx * 4 + j < a.E)
-                logits[static_cast<size_t>(t0 + ty * 4 + i) * a.E + e0 + tx * 4 + j] = acc[i][j];
 }
 
 // A float as an unsigned integer of the same order; 0 for what may not be
@@ -112,7 +77,7 @@ __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.f) - l
 // experts i, i + 32, ... s_key[E]: this warp's scratch, used with groups only
 // (it may be logits itself).
 template <int kPer>
-__device__ __noinline__ void select_experts(const RouteArgs &a, int t, const float *logits, float *s_key)
+__device__ __forceinline__ void select_body(const RouteArgs &a, int t, const float *logits, float *s_key)
 {
     const int lane = threadIdx.x & 31;
     float l[kPer];
@@ -208,7 +173,10 @@ __device__ __noinline__ void select_experts(const RouteArgs &a, int t, const flo
         const uint32_t top = __reduce_max_sync(kFull, best);
         if (top == 0u)
             break;
-        const int e = __reduce_min_sync(kFull, best == top ? at : 1 << 30);
+        const unsigned holders = __ballot_sync(kFull, best == top);
+        int e = __shfl_sync(kFull, at, __ffs(holders) - 1);
+        if (holders & (holders - 1))    // a tie between lanes
+            e = __reduce_min_sync(kFull, best == top ? at : 1 << 30);
         val = __shfl_sync(kFull, val, e & 31);
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
@@ -251,6 +219,14 @@ __device__ __noinline__ void select_experts(const RouteArgs &a, int t, const flo
     }
 }
 
+// The four sizes of the few-token kernel, as calls: inlined, each of its twelve
+// instances would hold four copies.
+template <int kPer>
+__device__ __noinline__ void select_experts(const RouteArgs &a, int t, const float *logits, float *s_key)
+{
+    select_body<kPer>(a, t, logits, s_key);
+}
+
 __device__ __forceinline__ void select_any(const RouteArgs &a, int t, const float *logits, float *s_key)
 {
     if (a.E <= 128)
@@ -267,15 +243,21 @@ __device__ __forceinline__ void select_any(const RouteArgs &a, int t, const floa
 
 constexpr int kSelectWarps = 4;
 
+// A warp per token, one instance per 128, 256, 512 or 1024 experts: with the
+// registers of the largest (128) only 16 warps fit on an SM, and the chain of
+// warp-wide reductions is latency.
+template <int kPer>
 __global__ void __launch_bounds__(32 * kSelectWarps) select_kernel(const __grid_constant__ RouteArgs a,
                                                                    const float *logits)
 {
     extern __shared__ float s_keys[];   // [kSelectWarps][E], with groups only
+    pdl_wait();
+    pdl_trigger();
     const int T = token_count(a.d_num_tokens, a.T_max);
     const int warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kSelectWarps + warp;
     if (t < T)
-        select_any(a, t, logits + static_cast<size_t>(t) * a.E, s_keys + warp * a.E);
+        select_body<kPer>(a, t, logits + static_cast<size_t>(t) * a.E, s_keys + warp * a.E);
 }
 
 // ------------------------------------------------------------- few tokens
@@ -569,12 +551,15 @@ cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t stream, b
         }
     }
     float *logits = a.logits ? a.logits : a.part;
-    cudaError_t e = launch_k(logits_kernel, dim3((a.T_max + 63) / 64, (a.E + 63) / 64), dim3(256), 0, stream, false, a,
-                             logits);
+    const cudaError_t e = launch_route_gemm(a, logits, stream, pdl);
     if (e != cudaSuccess)
         return e;
-    return launch_k(select_kernel, dim3((a.T_max + kSelectWarps - 1) / kSelectWarps), dim3(32 * kSelectWarps),
-                    a.n_group > 1 ? sizeof(float) * kSelectWarps * a.E : 0, stream, false, a, logits);
+    auto kern = a.E <= 128   ? select_kernel<4>
+                : a.E <= 256 ? select_kernel<8>
+                : a.E <= 512 ? select_kernel<16>
+                             : select_kernel<32>;
+    return launch_k(kern, dim3((a.T_max + kSelectWarps - 1) / kSelectWarps), dim3(32 * kSelectWarps),
+                    a.n_group > 1 ? sizeof(float) * kSelectWarps * a.E : 0, stream, pdl, a, logits);
 }
 
 }  // namespace moe
