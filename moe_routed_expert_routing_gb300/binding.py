@@ -297,21 +297,30 @@ def _need(t, name: str, dtype, numel: int):
         raise ValueError(f"{name} holds {t.numel()} elements; the problem needs at least {numel}")
 
 
+def _dev(t, name: str, dtype, numel: int) -> int | None:
+    """_need and _ptr in one: the checked pointer."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.is_cuda and t.dtype == dtype and t.numel() >= numel and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, numel)
+    return _ptr(t)
+
+
 def _need_rows(t, name: str, dtype, rows: int, cols: int, stride: int) -> int | None:
     """Pointer of a [rows, cols] tensor whose rows lie ``stride`` elements
     apart (0 = cols, contiguous), checked as _need does."""
     if t is None or isinstance(t, int):
         return t
+    if (stride == 0 or stride == cols) and t.is_contiguous():
+        return _dev(t, name, dtype, rows * cols)
     stride = stride or cols
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (device memory), not on {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.is_contiguous() and stride == cols:
-        if t.numel() < rows * cols:
-            raise ValueError(f"{name} holds {t.numel()} elements; the problem needs at least {rows * cols}")
-    elif (t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols or t.stride(1) != 1 or
-          (rows > 1 and t.stride(0) != stride)):
+    if (t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols or t.stride(1) != 1 or
+            (rows > 1 and t.stride(0) != stride)):
         raise ValueError(f"{name} must be [{rows}, {cols}] with rows {stride} elements apart, not "
                          f"{tuple(t.shape)} with strides {t.stride()}")
     return t.data_ptr()
@@ -330,7 +339,8 @@ def _need_weights(problem, W13, W2):
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: a torch.cuda.Stream object takes 2.6 us to build, as long as a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -484,41 +494,37 @@ def moe_quantize_weights(problem, W13, W2, W13_mx=None, W2_mx=None, stream=None)
 def moe_norm(problem: NormProblem, h, w, x, d_num_tokens=None, stream=None):
     """x = norm(h) * w; see include/moe.h."""
     p = problem
-    h = _need_rows(h, "h", p.h_torch, p.T_max, p.H, p.h_stride)
-    _need(w, "w", p.w_torch, p.H)
-    _need(d_num_tokens, "d_num_tokens", torch.int32, 1)
-    x = _need_rows(x, "x", torch.bfloat16, p.T_max, p.H, p.x_stride)
-    _check(load_library().moe_norm(ctypes.byref(p), h, _ptr(w), _ptr(d_num_tokens), x, _stream(stream)), "moe_norm")
+    T, H = p.T_max, p.H
+    _check(load_library().moe_norm(ctypes.byref(p), _need_rows(h, "h", p.h_torch, T, H, p.h_stride),
+                                   _dev(w, "w", p.w_torch, H), _dev(d_num_tokens, "d_num_tokens", torch.int32, 1),
+                                   _need_rows(x, "x", torch.bfloat16, T, H, p.x_stride), _stream(stream)), "moe_norm")
 
 
 def _need_residual(p: NormProblem, h, w_post, gate, w_next, h_out, x_next):
-    """Checked pointers (h, gate, h_out, x_next) of the way back into the residual stream."""
-    _need(w_post, "w_post", p.w_torch, p.H)
-    _need(w_next, "w_next", p.w_torch, p.H)
-    if p.gate == MOE_GATE_CHANNEL:
-        _need(gate, "gate", p.w_torch, p.H)
-        gate = _ptr(gate)
-    elif p.gate == MOE_GATE_TOKEN:
-        _need(gate, "gate", torch.float32, p.T_max)
-        gate = _ptr(gate)
-    elif p.gate == MOE_GATE_ELEMENT:
-        gate = _need_rows(gate, "gate", torch.bfloat16, p.T_max, p.H, p.gate_stride)
+    """Checked pointers (h, w_post, gate, w_next, h_out, x_next) of the way back into the residual stream."""
+    T, H, ht, wt, kind = p.T_max, p.H, p.h_torch, p.w_torch, p.gate
+    if kind == MOE_GATE_CHANNEL:
+        gate = _dev(gate, "gate", wt, H)
+    elif kind == MOE_GATE_TOKEN:
+        gate = _dev(gate, "gate", torch.float32, T)
+    elif kind == MOE_GATE_ELEMENT:
+        gate = _need_rows(gate, "gate", torch.bfloat16, T, H, p.gate_stride)
     elif gate is not None:
         raise ValueError("gate given, but the problem has none")
-    return (_need_rows(h, "h", p.h_torch, p.T_max, p.H, p.h_stride), gate,
-            _need_rows(h_out, "h_out", p.h_torch, p.T_max, p.H, p.out_stride),
-            _need_rows(x_next, "x_next", torch.bfloat16, p.T_max, p.H, p.x_stride))
+    return (_need_rows(h, "h", ht, T, H, p.h_stride), _dev(w_post, "w_post", wt, H), gate,
+            _dev(w_next, "w_next", wt, H), _need_rows(h_out, "h_out", ht, T, H, p.out_stride),
+            _need_rows(x_next, "x_next", torch.bfloat16, T, H, p.x_stride))
 
 
 def moe_norm_residual(problem: NormProblem, h, y, h_out, w_post=None, gate=None, w_next=None, x_next=None,
                       d_num_tokens=None, stream=None):
     """h_out = h + scale * gate * norm(y) * w_post, and x_next = norm(h_out) * w_next; see include/moe.h."""
     p = problem
-    h, gate, h_out, x_next = _need_residual(p, h, w_post, gate, w_next, h_out, x_next)
+    h, w_post, gate, w_next, h_out, x_next = _need_residual(p, h, w_post, gate, w_next, h_out, x_next)
     y = _need_rows(y, "y", torch.bfloat16, p.T_max, p.H, p.y_stride)
-    _need(d_num_tokens, "d_num_tokens", torch.int32, 1)
-    _check(load_library().moe_norm_residual(ctypes.byref(p), h, y, _ptr(w_post), gate, _ptr(w_next),
-                                            _ptr(d_num_tokens), h_out, x_next, _stream(stream)), "moe_norm_residual")
+    _check(load_library().moe_norm_residual(ctypes.byref(p), h, y, w_post, gate, w_next,
+                                            _dev(d_num_tokens, "d_num_tokens", torch.int32, 1), h_out, x_next,
+                                            _stream(stream)), "moe_norm_residual")
 
 
 def moe_route_workspace_size(problem: RouterProblem) -> int:
@@ -529,23 +535,23 @@ def moe_route_workspace_size(problem: RouterProblem) -> int:
 
 
 def _need_router(p: RouterProblem, w_router, bias, topk_ids, topk_weights, d_num_tokens):
-    _need(w_router, "w_router", torch.bfloat16, p.E * p.H)
-    _need(bias, "bias", torch.float32, p.E)
-    _need(topk_ids, "topk_ids", torch.int32, p.T_max * p.k)
-    _need(topk_weights, "topk_weights", torch.float32, p.T_max * p.k)
-    _need(d_num_tokens, "d_num_tokens", torch.int32, 1)
+    """Checked pointers of the router's arguments, in that order."""
+    slots = p.T_max * p.k
+    return (_dev(w_router, "w_router", torch.bfloat16, p.E * p.H), _dev(bias, "bias", torch.float32, p.E),
+            _dev(topk_ids, "topk_ids", torch.int32, slots), _dev(topk_weights, "topk_weights", torch.float32, slots),
+            _dev(d_num_tokens, "d_num_tokens", torch.int32, 1))
 
 
 def moe_route(problem: RouterProblem, x, w_router, topk_ids, topk_weights, ws, bias=None, logits=None,
               d_num_tokens=None, stream=None):
     """Logits, the k experts of the largest keys and their weights; see include/moe.h."""
     p = problem
-    _need(x, "x", torch.bfloat16, p.T_max * p.H)
-    _need_router(p, w_router, bias, topk_ids, topk_weights, d_num_tokens)
-    _need(logits, "logits", torch.float32, p.T_max * p.E)
+    T = p.T_max
+    x = _dev(x, "x", torch.bfloat16, T * p.H)
+    w_router, bias, ids, weights, n = _need_router(p, w_router, bias, topk_ids, topk_weights, d_num_tokens)
     _need(ws, "ws", None, 0)
-    _check(load_library().moe_route(ctypes.byref(p), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(d_num_tokens),
-                                    _ptr(topk_ids), _ptr(topk_weights), _ptr(logits), _ptr(ws),
+    _check(load_library().moe_route(ctypes.byref(p), x, w_router, bias, n, ids, weights,
+                                    _dev(logits, "logits", torch.float32, T * p.E), _ptr(ws),
                                     ws.numel() * ws.element_size(), _stream(stream)), "moe_route")
 
 
@@ -560,16 +566,16 @@ def moe_layer(problem: LayerProblem, h, w_pre, w_router, W13, W2, topk_ids, topk
               ws, bias=None, w_post=None, gate=None, w_next=None, x_next=None, d_num_tokens=None, stream=None):
     """Norm, router, experts and the way back into the residual stream, for a few tokens; see include/moe.h."""
     p = problem
-    h, gate, h_out, x_next = _need_residual(p.norm, h, w_post, gate, w_next, h_out, x_next)
-    _need(w_pre, "w_pre", p.norm.w_torch, p.norm.H)
-    _need_router(p.router, w_router, bias, topk_ids, topk_weights, d_num_tokens)
-    _need_weights(p.experts, W13, W2)
-    _need(expert_offsets, "expert_offsets", torch.int32, p.experts.E + 1)
-    _need(perm, "perm", torch.int32, p.experts.cap)
+    h, w_post, gate, w_next, h_out, x_next = _need_residual(p.norm, h, w_post, gate, w_next, h_out, x_next)
+    w_pre = _dev(w_pre, "w_pre", p.norm.w_torch, p.norm.H)
+    w_router, bias, ids, weights, n = _need_router(p.router, w_router, bias, topk_ids, topk_weights, d_num_tokens)
+    e = p.experts
+    _need_weights(e, W13, W2)
+    offsets = _dev(expert_offsets, "expert_offsets", torch.int32, e.E + 1)
+    perm = _dev(perm, "perm", torch.int32, e.cap)
     _need(ws, "ws", None, 0)
-    _check(load_library().moe_layer(ctypes.byref(p), h, _ptr(w_pre), _ptr(w_router), _ptr(bias), _ptr(W13), _ptr(W2),
-                                    _ptr(w_post), gate, _ptr(w_next), _ptr(d_num_tokens), _ptr(topk_ids),
-                                    _ptr(topk_weights), _ptr(expert_offsets), _ptr(perm), h_out, x_next, _ptr(ws),
+    _check(load_library().moe_layer(ctypes.byref(p), h, w_pre, w_router, bias, _ptr(W13), _ptr(W2), w_post, gate,
+                                    w_next, n, ids, weights, offsets, perm, h_out, x_next, _ptr(ws),
                                     ws.numel() * ws.element_size(), _stream(stream)), "moe_layer")
 
 

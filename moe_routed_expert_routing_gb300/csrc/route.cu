@@ -70,8 +70,64 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
+__device__ __forceinline__ float score_of(const RouteArgs &a, float l, float mx, float sum)
+{
+    return a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - mx) / sum;
+}
+
 // log of the sigmoid, without overflow or a loss of small values
 __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.f) - log1pf(expf(-fabsf(l))); }
+
+// The chosen experts' weights, by one warp: lane j holds places j and j + 32
+// (id -1: none). mx and sum are the softmax's maximum and denominator, used
+// when the scores are not renormalised.
+__device__ __forceinline__ void store_choice(const RouteArgs &a, int t, const int (&id)[2], const float (&l)[2],
+                                             float mx, float sum)
+{
+    float w[2], norm = 1.f;
+    if (a.renormalize) {
+        // the chosen scores over their sum, from their logarithms (the softmax
+        // over all E cancels), so that scores that underflow keep their ratios
+        float lg[2], top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            lg[q] = id[q] >= 0 ? (a.sigmoid ? log_sigmoid(l[q]) : l[q]) : -INFINITY;
+            top = fmaxf(top, lg[q]);
+        }
+        top = warp_max(top);
+        top = top > -INFINITY ? top : 0.f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            w[q] = expf(lg[q] - top);
+        norm = warp_sum(w[0] + w[1]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            w[q] = id[q] >= 0 ? score_of(a, l[q], mx, sum) : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int j = (threadIdx.x & 31) + 32 * q;
+        if (j < a.k) {
+            a.ids[static_cast<size_t>(t) * a.k + j] = id[q];
+            a.weights[static_cast<size_t>(t) * a.k + j] = id[q] >= 0 ? a.scale * (w[q] / norm) : 0.f;
+        }
+    }
+}
+
+// Which groups stay, from lane g's group value: bit g of the result. One warp.
+__device__ __forceinline__ unsigned keep_groups(const RouteArgs &a, float value)
+{
+    const int lane = threadIdx.x & 31;
+    if (!(value > -INFINITY))   // also the sum of +inf and -inf
+        value = -INFINITY;
+    int rank = 0;
+    for (int g = 0; g < a.n_group; ++g) {
+        const float o = __shfl_sync(kFull, value, g);
+        rank += (o > value || (o == value && g < lane)) ? 1 : 0;
+    }
+    return __ballot_sync(kFull, lane < a.n_group && rank < a.topk_group);
+}
 
 // One warp selects for one token whose logits lie in logits[E]; lane i holds
 // experts i, i + 32, ... s_key[E]: this warp's scratch, used with groups only
@@ -97,8 +153,9 @@ __device__ __forceinline__ void select_body(const RouteArgs &a, int t, const flo
     }
     if (__any_sync(kFull, bad) && lane == 0)
         atomicOr(a.err, MOE_DEVERR_BAD_LOGIT);
+    const bool by_score = a.bias != nullptr || a.group_top > 1;
     float mx = -INFINITY, sum = 1.f;
-    if (!a.sigmoid) {
+    if (!a.sigmoid && (by_score || !a.renormalize)) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             mx = fmaxf(mx, l[i]);
@@ -110,15 +167,13 @@ __device__ __forceinline__ void select_body(const RouteArgs &a, int t, const flo
             sum += expf(l[i] - mx);
         sum = warp_sum(sum);
     }
-    auto score = [&](float v) { return a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - mx) / sum; };
-    const bool by_score = a.bias != nullptr || a.group_top > 1;
     uint32_t key[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = lane + 32 * i;
         float v = l[i];
         if (by_score && e < a.E && v > -INFINITY)
-            v = score(v) + (a.bias ? a.bias[e] : 0.f);
+            v = score_of(a, v, mx, sum) + (a.bias ? a.bias[e] : 0.f);
         key[i] = e < a.E ? order_key(v) : 0u;
         if (a.n_group > 1 && e < a.E)
             s_key[e] = key[i] ? v : -INFINITY;
@@ -139,15 +194,8 @@ __device__ __forceinline__ void select_body(const RouteArgs &a, int t, const flo
                 }
             }
             value = a.group_top > 1 ? first + second : first;
-            if (!(value > -INFINITY))   // also inf - inf
-                value = -INFINITY;
         }
-        int rank = 0;
-        for (int g = 0; g < a.n_group; ++g) {
-            const float o = __shfl_sync(kFull, value, g);
-            rank += (o > value || (o == value && g < lane)) ? 1 : 0;
-        }
-        const unsigned kept = __ballot_sync(kFull, lane < a.n_group && rank < a.topk_group);
+        const unsigned kept = keep_groups(a, value);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = lane + 32 * i;
@@ -187,56 +235,7 @@ __device__ __forceinline__ void select_body(const RouteArgs &a, int t, const flo
             my_l[j >> 5] = val;
         }
     }
-    // weights
-    float w[2], norm = 1.f;
-    if (a.renormalize) {
-        // the chosen scores over their sum, from their logarithms (the softmax
-        // over all E cancels), so that scores that underflow keep their ratios
-        float lg[2], m2 = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            lg[q] = my_id[q] >= 0 ? (a.sigmoid ? log_sigmoid(my_l[q]) : my_l[q]) : -INFINITY;
-            m2 = fmaxf(m2, lg[q]);
-        }
-        m2 = warp_max(m2);
-        m2 = m2 > -INFINITY ? m2 : 0.f;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-            w[q] = expf(lg[q] - m2);
-        norm = warp_sum(w[0] + w[1]);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-            w[q] = my_id[q] >= 0 ? score(my_l[q]) : 0.f;
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int j = lane + 32 * q;
-        if (j < a.k) {
-            a.ids[static_cast<size_t>(t) * a.k + j] = my_id[q];
-            a.weights[static_cast<size_t>(t) * a.k + j] = my_id[q] >= 0 ? a.scale * (w[q] / norm) : 0.f;
-        }
-    }
-}
-
-// The four sizes of the few-token kernel, as calls: inlined, each of its twelve
-// instances would hold four copies.
-template <int kPer>
-__device__ __noinline__ void select_experts(const RouteArgs &a, int t, const float *logits, float *s_key)
-{
-    select_body<kPer>(a, t, logits, s_key);
-}
-
-__device__ __forceinline__ void select_any(const RouteArgs &a, int t, const float *logits, float *s_key)
-{
-    if (a.E <= 128)
-        select_experts<4>(a, t, logits, s_key);
-    else if (a.E <= 256)
-        select_experts<8>(a, t, logits, s_key);
-    else if (a.E <= 512)
-        select_experts<16>(a, t, logits, s_key);
-    else
-        select_experts<32>(a, t, logits, s_key);
+    store_choice(a, t, my_id, my_l, mx, sum);
 }
 
 // ------------------------------------------------------------ many tokens
@@ -320,6 +319,157 @@ __device__ __forceinline__ void load_weight8(const RouteArgs &a, int m, float (&
             w[i] = 1.f + w[i];
 }
 
+// Float of an order_key (which is not 0).
+__device__ __forceinline__ float key_value(uint32_t u)
+{
+    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
+// Shared memory of one selection by a whole block.
+struct SelectScratch {
+    float logits[kMaxExperts];
+    uint32_t key[kMaxExperts];
+    uint64_t found[kFewWarps * kMaxTopK];   // each warp's best, key and ~expert
+    float warp[kFewWarps];
+    float group[32];
+    unsigned kept;
+    int id[kMaxTopK];
+};
+
+// All eight warps select for one token, logits in s.logits: each warp takes
+// the k best of an eighth of the experts, then every one of those 8 k counts
+// the ones that beat it. Called with a cold instruction cache between a
+// model's other kernels, so its loops stay rolled: the version that one warp
+// ran on unrolled registers took 13 us there.
+__device__ void select_block(const RouteArgs &a, int t, SelectScratch &s)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int E = a.E, k = a.k;
+    const bool by_score = a.bias != nullptr || a.group_top > 1;
+    bool bad = false;
+    float mx = -INFINITY, sum = 1.f;
+    for (int e = tid; e < E; e += kFewThreads) {
+        float v = s.logits[e];
+        if (!(v < INFINITY)) {   // NaN or +inf
+            bad = true;
+            s.logits[e] = v = -INFINITY;
+        }
+        mx = fmaxf(mx, v);
+    }
+    if (bad)
+        atomicOr(a.err, MOE_DEVERR_BAD_LOGIT);
+    if (!a.sigmoid && (by_score || !a.renormalize)) {
+        mx = warp_max(mx);
+        if (lane == 0)
+            s.warp[warp] = mx;
+        __syncthreads();
+        for (int i = 0; i < kFewWarps; ++i)
+            mx = fmaxf(mx, s.warp[i]);
+        mx = mx > -INFINITY ? mx : 0.f;
+        sum = 0.f;
+        for (int e = tid; e < E; e += kFewThreads)
+            sum += expf(s.logits[e] - mx);
+        sum = warp_sum(sum);
+        __syncthreads();
+        if (lane == 0)
+            s.warp[warp] = sum;
+        __syncthreads();
+        sum = 0.f;
+        for (int i = 0; i < kFewWarps; ++i)
+            sum += s.warp[i];
+    }
+    for (int e = tid; e < E; e += kFewThreads) {
+        float v = s.logits[e];
+        if (by_score && v > -INFINITY)
+            v = score_of(a, v, mx, sum) + (a.bias ? a.bias[e] : 0.f);
+        s.key[e] = order_key(v);
+    }
+    if (a.n_group > 1) {
+        const int gs = E / a.n_group;
+        __syncthreads();
+        for (int g = warp; g < a.n_group; g += kFewWarps) {
+            uint32_t first = 0u, second = 0u;
+            for (int i = lane; i < gs; i += 32) {
+                const uint32_t u = s.key[g * gs + i];
+                second = u > first ? first : (u > second ? u : second);
+                first = u > first ? u : first;
+            }
+            const uint32_t top = __reduce_max_sync(kFull, first);
+            const int holder = __ffs(__ballot_sync(kFull, first == top)) - 1;
+            const uint32_t next = __reduce_max_sync(kFull, lane == holder ? second : first);
+            if (lane == 0)
+                s.group[g] = top == 0u                            ? -INFINITY
+                             : a.group_top == 1                   ? key_value(top)
+                             : next == 0u                         ? -INFINITY
+                                                                  : key_value(top) + key_value(next);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const unsigned kept = keep_groups(a, lane < a.n_group ? s.group[lane] : -INFINITY);
+            if (lane == 0)
+                s.kept = kept;
+        }
+        __syncthreads();
+        for (int e = tid; e < E; e += kFewThreads)
+            if (!((s.kept >> (e / gs)) & 1u))
+                s.key[e] = 0u;
+    }
+    if (tid < kMaxTopK)
+        s.id[tid] = -1;
+    // this warp's best, over its own threads' experts (tid, tid + 256, ...)
+    uint32_t key[kMaxExperts / kFewThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / kFewThreads; ++i)
+        key[i] = tid + i * kFewThreads < E ? s.key[tid + i * kFewThreads] : 0u;
+    int n = 0;
+#pragma unroll 1
+    for (; n < k; ++n) {
+        uint32_t best = 0u;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxExperts / kFewThreads; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = tid + i * kFewThreads;
+            }
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        if (top == 0u)
+            break;
+        const int e = __reduce_min_sync(kFull, best == top ? at : 1 << 30);
+#pragma unroll
+        for (int i = 0; i < kMaxExperts / kFewThreads; ++i)
+            if (tid + i * kFewThreads == e)
+                key[i] = 0u;
+        if (lane == 0)
+            s.found[warp * k + n] = static_cast<uint64_t>(top) << 32 | static_cast<uint32_t>(~e);
+    }
+    for (int i = lane; i < k; i += 32)
+        if (i >= n)
+            s.found[warp * k + i] = 0u;
+    __syncthreads();
+    for (int c = tid; c < kFewWarps * k; c += kFewThreads) {
+        const uint64_t mine = s.found[c];
+        int rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < kFewWarps * k; ++i)
+            rank += s.found[i] > mine ? 1 : 0;
+        if (mine != 0u && rank < k)
+            s.id[rank] = static_cast<int>(~static_cast<uint32_t>(mine));
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int id[2];
+        float l[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            id[q] = s.id[lane + 32 * q];
+            l[q] = id[q] >= 0 ? s.logits[id[q]] : -INFINITY;
+        }
+        store_choice(a, t, id, l, mx, sum);
+    }
+    __syncthreads();
+}
+
 // kTiles: 8-token tiles of a unit. kParts: bf16 parts of the token operand;
 // 1: x as it is (moe_route), 2 or 3: u = h * w_pre (moe_layer).
 template <int kTiles, int kParts>
@@ -329,7 +479,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
     constexpr int kTok = 8 * kTiles;
     __shared__ float s_acc[kFewWarps][16][kTok + 1];
     __shared__ float s_sq[kFewWarps][kTok];
-    __shared__ float s_logits[kMaxExperts];
+    __shared__ SelectScratch s_sel;
     __shared__ int s_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
@@ -461,13 +611,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
     }
 
     // all units' partial sums are in the workspace once every CTA has counted
-    // itself; only the CTAs that select for a token wait (bounded)
+    // itself; only the CTAs with a job after that wait (bounded): one per token
+    // that selects and, in moe_layer, one that writes its rounded row
+    const int jobs = kParts > 1 ? 2 * T : T;
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
         s_flag = 0;
         atom_add_acq_rel_gpu(a.counters, 1);
-        if (static_cast<int>(blockIdx.x) < T) {
+        if (static_cast<int>(blockIdx.x) < jobs) {
             const uint64_t since = global_timer_ns();
             while (ld_acquire_gpu(a.counters) < static_cast<int>(gridDim.x))
                 if (global_timer_ns() - since > wait_limit_ns) {
@@ -485,29 +637,41 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
     __syncthreads();
     if (s_flag)
         return;
-    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const int t = job < T ? job : job - T;
         float r = 1.f;
         if (kParts > 1) {
+            const float *sq = a.part + static_cast<size_t>(sp.slices) * a.T_max * E + t;
             float v = 0.f;
+#pragma unroll 8
             for (int s = 0; s < sp.slices; ++s)
-                v += __ldcg(a.part + static_cast<size_t>(sp.slices) * a.T_max * E + static_cast<size_t>(s) * a.T_max + t);
+                v += __ldcg(sq + static_cast<size_t>(s) * a.T_max);
             r = 1.f / sqrtf(v / H + a.eps);
         }
-        for (int e = threadIdx.x; e < E; e += kFewThreads) {
-            float v = 0.f;
+        if (job < T) {
+            float v[kMaxExperts / kFewThreads] = {};
+#pragma unroll 4
             for (int s = 0; s < sp.slices; ++s)
-                v += __ldcg(a.part + (static_cast<size_t>(s) * a.T_max + t) * E + e);
-            v *= r;
-            s_logits[e] = v;
-            if (a.logits)
-                a.logits[static_cast<size_t>(t) * E + e] = v;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            select_any(a, t, s_logits, s_logits);
+#pragma unroll
+                for (int i = 0; i < kMaxExperts / kFewThreads; ++i)
+                    if (threadIdx.x + i * kFewThreads < E)
+                        v[i] += __ldcg(a.part + (static_cast<size_t>(s) * a.T_max + t) * E + threadIdx.x +
+                                       i * kFewThreads);
+#pragma unroll
+            for (int i = 0; i < kMaxExperts / kFewThreads; ++i) {
+                const int e = threadIdx.x + i * kFewThreads;
+                if (e < E) {
+                    s_sel.logits[e] = v[i] * r;
+                    if (a.logits)
+                        a.logits[static_cast<size_t>(t) * E + e] = v[i] * r;
+                }
+            }
+            __syncthreads();
+            select_block(a, t, s_sel);
         } else if (kParts > 1) {
             // the normalised row for the experts, rounded to bf16 (their MMAs' operand type)
-            for (int m = 8 * (threadIdx.x - 32); m < H; m += 8 * (kFewThreads - 32)) {
+#pragma unroll 2
+            for (int m = 8 * threadIdx.x; m < H; m += 8 * kFewThreads) {
                 float f[8], wp[8];
                 load8(a.x, a.x_f32, t * a.x_stride + m, f);
                 load_weight8(a, m, wp);
@@ -519,7 +683,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) + static_cast<size_t>(t) * H + m) = o;
             }
         }
-        __syncthreads();
     }
 }
 
