@@ -75,14 +75,21 @@ __device__ __forceinline__ float score_of(const RouteArgs &a, float l, float mx,
     return a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - mx) / sum;
 }
 
+// Float of an order_key (which is not 0).
+__device__ __forceinline__ float key_value(uint32_t u)
+{
+    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
 // log of the sigmoid, without overflow or a loss of small values
 __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.f) - log1pf(expf(-fabsf(l))); }
 
-// The chosen experts' weights, by one warp: lane j holds places j and j + 32
-// (id -1: none). mx and sum are the softmax's maximum and denominator, used
-// when the scores are not renormalised.
-__device__ __forceinline__ void store_choice(const RouteArgs &a, int t, const int (&id)[2], const float (&l)[2],
-                                             float mx, float sum)
+// The chosen experts' ids and weights, by one warp: a lane holds up to two of
+// them (id -1: none) with their places; mx and sum are the softmax's maximum
+// and denominator, used when the scores are not renormalised. n: how many were
+// found; places from n on get id -1 and weight 0.
+__device__ __forceinline__ void store_choice(const RouteArgs &a, int t, const int (&id)[2], const int (&place)[2],
+                                             const float (&l)[2], int n, float mx, float sum)
 {
     float w[2], norm = 1.f;
     if (a.renormalize) {
@@ -105,13 +112,17 @@ __device__ __forceinline__ void store_choice(const RouteArgs &a, int t, const in
         for (int q = 0; q < 2; ++q)
             w[q] = id[q] >= 0 ? score_of(a, l[q], mx, sum) : 0.f;
     }
+    int32_t *ids = a.ids + static_cast<size_t>(t) * a.k;
+    float *weights = a.weights + static_cast<size_t>(t) * a.k;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int j = (threadIdx.x & 31) + 32 * q;
-        if (j < a.k) {
-            a.ids[static_cast<size_t>(t) * a.k + j] = id[q];
-            a.weights[static_cast<size_t>(t) * a.k + j] = id[q] >= 0 ? a.scale * (w[q] / norm) : 0.f;
+    for (int q = 0; q < 2; ++q)
+        if (id[q] >= 0) {
+            ids[place[q]] = id[q];
+            weights[place[q]] = a.scale * (w[q] / norm);
         }
+    for (int j = n + (threadIdx.x & 31); j < a.k; j += 32) {
+        ids[j] = -1;
+        weights[j] = 0.f;
     }
 }
 
@@ -130,10 +141,17 @@ __device__ __forceinline__ unsigned keep_groups(const RouteArgs &a, float value)
 }
 
 // One warp selects for one token whose logits lie in logits[E]; lane i holds
-// experts i, i + 32, ... s_key[E]: this warp's scratch, used with groups only
-// (it may be logits itself).
+// experts i, i + 32, ... s_key[E]: this warp's scratch, used with groups only.
+// s_found: 32 words of scratch.
+//
+// k rounds of a warp-wide maximum over all keys would cost k passes over the
+// lane's registers. The k-th largest of the lanes' own maxima is a lower bound
+// of the k-th largest key, and few keys reach it (9 or 10 of 128 or 384 at
+// k = 6 to 8): those are gathered, and each counts the ones that beat it. More
+// than 32 of them (many equal keys), or k > 32, take the rounds.
 template <int kPer>
-__device__ __forceinline__ void select_body(const RouteArgs &a, int t, const float *logits, float *s_key)
+__device__ __forceinline__ void select_body(const RouteArgs &a, int t, const float *logits, float *s_key,
+                                            uint64_t *s_found)
 {
     const int lane = threadIdx.x & 31;
     float l[kPer];
@@ -204,38 +222,73 @@ __device__ __forceinline__ void select_body(const RouteArgs &a, int t, const flo
         }
         __syncwarp();
     }
-    // k rounds: the largest key, the lowest expert among equals
-    int my_id[2] = {-1, -1};       // lane j holds places j and j + 32
+    int my_id[2] = {-1, -1}, place[2] = {lane, lane + 32};
     float my_l[2] = {-INFINITY, -INFINITY};
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0;
-        int at = 1 << 30;
-        float val = 0.f;
+    int n = 0;
+    uint32_t own = 0u;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = lane + 32 * i;
-                val = l[i];
+    for (int i = 0; i < kPer; ++i)
+        own = max(own, key[i]);
+    uint32_t least = 0u;
+    if (a.k <= 32)
+#pragma unroll 1
+        for (int j = 0; j < a.k; ++j) {
+            least = __reduce_max_sync(kFull, own);
+            if (least == 0u)
+                break;
+            if (lane == __ffs(__ballot_sync(kFull, own == least)) - 1)
+                own = 0u;
+        }
+    least = max(least, 1u);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const unsigned b = __ballot_sync(kFull, key[i] >= least);
+        const int slot = n + __popc(b & ((1u << lane) - 1u));
+        if (key[i] >= least && slot < 32)
+            s_found[slot] = static_cast<uint64_t>(key[i]) << 32 | static_cast<uint32_t>(~(lane + 32 * i));
+        n += __popc(b);
+    }
+    if (n <= 32 && a.k <= 32) {
+        __syncwarp();
+        const uint64_t mine = lane < n ? s_found[lane] : 0u;
+        int rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i)
+            rank += s_found[i] > mine ? 1 : 0;
+        if (lane < n && rank < a.k) {
+            my_id[0] = static_cast<int>(~static_cast<uint32_t>(mine));
+            place[0] = rank;
+            my_l[0] = by_score ? logits[my_id[0]] : key_value(static_cast<uint32_t>(mine >> 32));
+        }
+        n = min(n, a.k);
+    } else {
+        // k rounds: the largest key, the lowest expert among equals
+        n = 0;
+#pragma unroll 1
+        for (; n < a.k; ++n) {
+            uint32_t best = 0u;
+            int at = 1 << 30;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    at = lane + 32 * i;
+                }
+            const uint32_t top = __reduce_max_sync(kFull, best);
+            if (top == 0u)
+                break;
+            const int e = __reduce_min_sync(kFull, best == top ? at : 1 << 30);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (lane + 32 * i == e)
+                    key[i] = 0u;
+            if (lane == (n & 31)) {
+                my_id[n >> 5] = e;
+                my_l[n >> 5] = logits[e];
             }
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        if (top == 0u)
-            break;
-        const unsigned holders = __ballot_sync(kFull, best == top);
-        int e = __shfl_sync(kFull, at, __ffs(holders) - 1);
-        if (holders & (holders - 1))    // a tie between lanes
-            e = __reduce_min_sync(kFull, best == top ? at : 1 << 30);
-        val = __shfl_sync(kFull, val, e & 31);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i == e)
-                key[i] = 0u;
-        if (lane == (j & 31)) {
-            my_id[j >> 5] = e;
-            my_l[j >> 5] = val;
         }
     }
-    store_choice(a, t, my_id, my_l, mx, sum);
+    store_choice(a, t, my_id, place, my_l, n, mx, sum);
 }
 
 // ------------------------------------------------------------ many tokens
@@ -250,13 +303,15 @@ __global__ void __launch_bounds__(32 * kSelectWarps) select_kernel(const __grid_
                                                                    const float *logits)
 {
     extern __shared__ float s_keys[];   // [kSelectWarps][E], with groups only
+    __shared__ uint64_t s_found[kSelectWarps][32];
     pdl_wait();
     pdl_trigger();
     const int T = token_count(a.d_num_tokens, a.T_max);
     const int warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kSelectWarps + warp;
     if (t < T)
-        select_body<kPer>(a, t, logits + static_cast<size_t>(t) * a.E, s_keys + warp * a.E);
+        select_body<kPer>(a, t, logits + static_cast<size_t>(t) * a.E, s_keys + warp * a.E,
+                          s_found[warp]);
 }
 
 // ------------------------------------------------------------- few tokens
@@ -317,12 +372,6 @@ __device__ __forceinline__ void load_weight8(const RouteArgs &a, int m, float (&
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             w[i] = 1.f + w[i];
-}
-
-// Float of an order_key (which is not 0).
-__device__ __forceinline__ float key_value(uint32_t u)
-{
-    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
 
 // Shared memory of one selection by a whole block.
@@ -459,13 +508,15 @@ __device__ void select_block(const RouteArgs &a, int t, SelectScratch &s)
     __syncthreads();
     if (warp == 0) {
         int id[2];
+        const int place[2] = {lane, lane + 32};
         float l[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             id[q] = s.id[lane + 32 * q];
             l[q] = id[q] >= 0 ? s.logits[id[q]] : -INFINITY;
         }
-        store_choice(a, t, id, l, mx, sum);
+        const int n = __popc(__ballot_sync(kFull, id[0] >= 0)) + __popc(__ballot_sync(kFull, id[1] >= 0));
+        store_choice(a, t, id, place, l, n, mx, sum);
     }
     __syncthreads();
 }

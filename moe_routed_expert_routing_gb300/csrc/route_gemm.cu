@@ -149,37 +149,54 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int own = kTokens / slices;
         const uint32_t dst = map_to_cta(
             smem_u32(smem) + static_cast<uint32_t>((rank * own + row % own) * C::kRowFloats * 4), row / own);
+        const int accs = min(C::kAccs, kb1 - kb0);
 #pragma unroll 1
         for (int c = (warp >> 2) * (kBN / 2); c < ((warp >> 2) + 1) * (kBN / 2); c += 32) {
             const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c;
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(at, r);
-            tmem_wait_ld();
-            for (int q = 1; q < C::kAccs && q < kb1 - kb0; ++q) {
-                uint32_t more[32];
-                tmem_ld_32x32b_x32(at + q * kBN, more);
-                tmem_wait_ld();
+            uint32_t r[C::kAccs][32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(more[i]));
-            }
+            for (int q = 0; q < C::kAccs; ++q)
+                if (q < accs)
+                    tmem_ld_32x32b_x32(at + q * kBN, r[q]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 1; q < C::kAccs; ++q)
+                if (q < accs)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) + __uint_as_float(r[q][i]));
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-                st_cluster_v4(dst + (c + i) * 4, r + i);
+                st_cluster_v4(dst + (c + i) * 4, r[0] + i);
         }
         cluster_sync();
-        const float *buf = reinterpret_cast<const float *>(smem);
-        if (!s_abort)
-            for (int i = threadIdx.x; i < own * kBN; i += kGemmThreads) {
-                const int r = i / kBN, c = i % kBN;
-                const int t = t0 + rank * own + r;
-                if (t < T && e0 + c < E) {
-                    float v = buf[r * C::kRowFloats + c];
-                    for (int s = 1; s < slices; ++s)
-                        v += buf[(s * own + r) * C::kRowFloats + c];
-                    logits[static_cast<size_t>(t) * E + e0 + c] = v;
+        if (!s_abort) {
+            const float *buf = reinterpret_cast<const float *>(smem);
+            const bool whole = E % 4 == 0;   // rows of logits 16-byte aligned
+            const int t_own = t0 + rank * own;
+#pragma unroll 4
+            for (int i = threadIdx.x; i < own * (kBN / 4); i += kGemmThreads) {
+                const int r = i / (kBN / 4), c = 4 * (i % (kBN / 4));
+                const float *src = buf + r * C::kRowFloats + c;
+                float4 v = *reinterpret_cast<const float4 *>(src);
+                for (int s = 1; s < slices; ++s) {
+                    const float4 p = *reinterpret_cast<const float4 *>(src + s * own * C::kRowFloats);
+                    v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+                }
+                if (t_own + r >= T)
+                    continue;
+                float *out = logits + static_cast<size_t>(t_own + r) * E + e0 + c;
+                if (whole && e0 + c < E) {
+                    *reinterpret_cast<float4 *>(out) = v;
+                } else if (!whole) {
+                    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (e0 + c + j < E)
+                            out[j] = f[j];
                 }
             }
+        }
         tc_fence_before();
     }
     __syncthreads();
