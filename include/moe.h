@@ -360,7 +360,7 @@ typedef enum moe_gate {
 } moe_gate_t;
 
 typedef struct moe_norm_problem {
-    int32_t T_max;          /* maximum tokens, >= 1 */
+    int32_t T_max;          /* maximum tokens, 1..2^30 */
     int32_t H;              /* hidden size, a multiple of 64, at most 32768 */
     int32_t h_dtype;        /* moe_dtype_t of the residual stream (h and h_out) */
     int32_t w_dtype;        /* moe_dtype_t of the norm weights and of the channel gate */

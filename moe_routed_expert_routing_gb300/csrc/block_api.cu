@@ -26,7 +26,8 @@ moe_status_t check_norm(const moe_norm_problem_t *p)
 {
     if (!p)
         return MOE_ERR_NULL;
-    if (p->T_max < 1 || p->H < 1 || p->H > kNormMaxHidden || (p->h_dtype != MOE_DTYPE_BF16 && p->h_dtype != MOE_DTYPE_FP32) ||
+    if (p->T_max < 1 || p->T_max > (1 << 30) || p->H < 1 || p->H > kNormMaxHidden ||
+        (p->h_dtype != MOE_DTYPE_BF16 && p->h_dtype != MOE_DTYPE_FP32) ||
         (p->w_dtype != MOE_DTYPE_BF16 && p->w_dtype != MOE_DTYPE_FP32) || !is_flag(p->unit_offset) ||
         !is_flag(p->norm_block) || p->gate < MOE_GATE_NONE || p->gate > MOE_GATE_ELEMENT)
         return MOE_ERR_SHAPE;

@@ -11,7 +11,13 @@
 // of 32..512 threads that keeps it in registers from the load to the store,
 // so the row sums cost no second read. Blocks are persistent and load their
 // next row before the sums of this one, so loads are in flight through the
-// barriers; the weights stay in L1 (the streams are loaded past it).
+// barriers; the weights stay in L1 (the streams are loaded past it). The
+// arithmetic runs on packed pairs (fma.rn.f32x2): at HBM's pace an SM has
+// about 12 issue slots for 32 elements of bf16, and scalar arithmetic with a
+// division and a square root per thread and row took 74% of all issue slots
+// (T=8192, H=4096, bf16: 25.0 us; with the residual in fp32 87 us). Now, of
+// the measured copy rate: 22.5 us, 0.88; 72.8 us, 0.82 (T=8191, fp32 stream,
+// channel gate, next norm). One row of 7168: 2.5 us, the launch.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -21,8 +27,6 @@
 namespace moe {
 
 namespace {
-
-constexpr int kMaxBlock = 512;
 
 __device__ __forceinline__ uint4 ld_stream(const void *p)
 {
@@ -40,22 +44,62 @@ __device__ __forceinline__ uint2 ld_stream2(const void *p)
     return v;
 }
 
-__device__ __forceinline__ void widen(uint32_t u, float &lo, float &hi)
+// ---- packed pairs of fp32 ----
+
+using Pair = unsigned long long;
+
+__device__ __forceinline__ Pair pair(float lo, float hi)
 {
-    lo = __uint_as_float(u << 16);
-    hi = __uint_as_float(u & 0xffff0000u);
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
 }
 
-__device__ __forceinline__ uint32_t pack(float lo, float hi)
+__device__ __forceinline__ float2 halves(Pair p)
 {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&p);
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
+{
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ Pair widen(uint32_t u)   // two bf16
+{
+    return pair(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t narrow(Pair p)
+{
+    const float2 f = halves(p);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
 }
 
 // A thread's unit is 16 bytes of the residual stream: 8 columns of bf16 or 4 of fp32.
 template <bool kF32>
 struct Unit {
     static constexpr int kCols = kF32 ? 4 : 8;
+    static constexpr int kPairs = kCols / 2;
     using Half = typename std::conditional<kF32, uint2, uint4>::type;   // the same columns in bf16
 
     static __device__ __forceinline__ Half load_half(const __nv_bfloat16 *p)
@@ -66,113 +110,129 @@ struct Unit {
             return ld_stream(p);
     }
 
-    static __device__ __forceinline__ void floats(const uint4 &u, float (&f)[kCols])
+    static __device__ __forceinline__ void pairs(const uint4 &u, Pair (&f)[kPairs])
     {
         if constexpr (kF32) {
-            f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-            f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+            f[0] = pair(__uint_as_float(u.x), __uint_as_float(u.y));
+            f[1] = pair(__uint_as_float(u.z), __uint_as_float(u.w));
         } else {
-            widen(u.x, f[0], f[1]); widen(u.y, f[2], f[3]);
-            widen(u.z, f[4], f[5]); widen(u.w, f[6], f[7]);
+            f[0] = widen(u.x); f[1] = widen(u.y); f[2] = widen(u.z); f[3] = widen(u.w);
         }
     }
 
-    static __device__ __forceinline__ void half_floats(const Half &u, float (&f)[kCols])
+    static __device__ __forceinline__ void half_pairs(const Half &u, Pair (&f)[kPairs])
     {
-        widen(u.x, f[0], f[1]);
-        widen(u.y, f[2], f[3]);
+        f[0] = widen(u.x);
+        f[1] = widen(u.y);
         if constexpr (!kF32) {
-            widen(u.z, f[4], f[5]);
-            widen(u.w, f[6], f[7]);
+            f[2] = widen(u.z);
+            f[3] = widen(u.w);
         }
     }
 
-    static __device__ __forceinline__ void store_half(__nv_bfloat16 *p, const float (&f)[kCols])
+    static __device__ __forceinline__ void store_half(__nv_bfloat16 *p, const Pair (&f)[kPairs])
     {
         if constexpr (kF32)
-            *reinterpret_cast<uint2 *>(p) = make_uint2(pack(f[0], f[1]), pack(f[2], f[3]));
+            *reinterpret_cast<uint2 *>(p) = make_uint2(narrow(f[0]), narrow(f[1]));
         else
-            *reinterpret_cast<uint4 *>(p) =
-                make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+            *reinterpret_cast<uint4 *>(p) = make_uint4(narrow(f[0]), narrow(f[1]), narrow(f[2]), narrow(f[3]));
     }
 
-    static __device__ __forceinline__ void store(void *p, const float (&f)[kCols])
+    static __device__ __forceinline__ void store(void *p, const Pair (&f)[kPairs])
     {
-        if constexpr (kF32)
-            *static_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-        else
+        if constexpr (kF32) {
+            const float2 a = halves(f[0]), b = halves(f[1]);
+            *static_cast<float4 *>(p) = make_float4(a.x, a.y, b.x, b.y);
+        } else {
             store_half(static_cast<__nv_bfloat16 *>(p), f);
+        }
     }
 
     // kCols values of a per-channel vector of either type
-    static __device__ __forceinline__ void channel(const void *p, bool f32, int m, float (&f)[kCols])
+    static __device__ __forceinline__ void channel(const void *p, bool f32, int m, Pair (&f)[kPairs])
     {
         if (f32) {
 #pragma unroll
-            for (int i = 0; i < kCols; i += 4) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + m + i));
-                f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
+            for (int i = 0; i < kPairs; i += 2) {
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + m + 2 * i));
+                f[i] = pair(v.x, v.y);
+                f[i + 1] = pair(v.z, v.w);
             }
         } else {
-            half_floats(__ldg(reinterpret_cast<const Half *>(static_cast<const __nv_bfloat16 *>(p) + m)), f);
+            half_pairs(__ldg(reinterpret_cast<const Half *>(static_cast<const __nv_bfloat16 *>(p) + m)), f);
         }
+    }
+
+    // f *= s * (norm weight of the columns from m on)
+    static __device__ __forceinline__ void apply_norm(const NormArgs &a, const void *w, int m, float s,
+                                                      Pair (&f)[kPairs])
+    {
+        const Pair s2 = pair(s, s);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            f[i] = mul2(f[i], s2);
+        if (!w)
+            return;
+        Pair c[kPairs];
+        channel(w, a.w_f32, m, c);
+        if (a.unit_offset) {
+            const Pair one = pair(1.f, 1.f);
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                c[i] = add2(c[i], one);
+        }
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            f[i] = mul2(f[i], c[i]);
     }
 };
 
-template <bool kF32>
-__device__ __forceinline__ void norm_weight(const NormArgs &a, const void *w, int m, float (&f)[Unit<kF32>::kCols])
-{
-    if (!w) {
-#pragma unroll
-        for (int i = 0; i < Unit<kF32>::kCols; ++i)
-            f[i] = 1.f;
-        return;
-    }
-    Unit<kF32>::channel(w, a.w_f32, m, f);
-    if (a.unit_offset)
-#pragma unroll
-        for (int i = 0; i < Unit<kF32>::kCols; ++i)
-            f[i] += 1.f;
-}
-
 // Sum over the tpr threads of a row group (whole warps); every thread of the
 // block calls it. s: this sum's words, one per warp of the block.
-__device__ __forceinline__ float row_sum(float v, int tpr, float *s)
+__device__ __forceinline__ float row_sum(Pair q, int tpr, float *s)
 {
+    const float2 f = halves(q);
+    float v = f.x + f.y;
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         v += __shfl_xor_sync(0xffffffffu, v, o);
     if (tpr == 32)
         return v;
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
         s[warp] = v;
     __syncthreads();
-    const int n = tpr >> 5, first = warp / n * n;
-    v = 0.f;
-    for (int i = 0; i < n; ++i)
-        v += s[first + i];
-    return v;
+    const int n = tpr >> 5;      // at most 16
+    v = lane < n ? s[warp / n * n + lane] : 0.f;
+#pragma unroll
+    for (int o = 8; o; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// Whether an instance fits 64 registers with its next row in them: two blocks
-// of 512 threads on an SM then. The wider rows run one block and load late.
-template <bool kF32, int kV, bool kRes>
-constexpr bool kLean = kV <= 2 || (kV == 4 && (kF32 || !kRes));
+// Blocks of kBlock threads that share an SM, by the columns a thread holds: a
+// row's values and the next row's raw bytes take 50 to 128 registers.
+template <bool kF32, int kV, bool kRes, int kBlock>
+struct Plan {
+    static constexpr int kHeld = kV * Unit<kF32>::kCols;
+    static constexpr bool kAhead = kHeld <= 32;   // the next row in registers too
+    static constexpr int kPerSm = kBlock == 256 ? (kHeld <= 16 ? (kRes ? 3 : 4) : 2) : (kHeld <= 16 && !kRes ? 2 : 1);
+};
 
 // kV units per thread; kRes: moe_norm_residual. tpr threads per row.
-template <bool kF32, int kV, bool kRes>
-__global__ void __launch_bounds__(kMaxBlock, kLean<kF32, kV, kRes> ? 2 : 1) norm_kernel(const __grid_constant__ NormArgs a, int tpr)
+template <bool kF32, int kV, bool kRes, int kBlock>
+__global__ void __launch_bounds__(kBlock, Plan<kF32, kV, kRes, kBlock>::kPerSm)
+    norm_kernel(const __grid_constant__ NormArgs a, int tpr, float inv_H)
 {
     using U = Unit<kF32>;
-    constexpr int kCols = U::kCols;
-    constexpr bool kAhead = kLean<kF32, kV, kRes>;   // the next row in registers too
+    constexpr int kCols = U::kCols, kPairs = U::kPairs;
+    constexpr int kBytes = kF32 ? 4 : 2;
+    constexpr bool kAhead = Plan<kF32, kV, kRes, kBlock>::kAhead;
     // two buffers: a row's words are not written again before every thread
     // has passed the barrier of the other sum
-    __shared__ float s_sum[2][kMaxBlock / 32];
+    __shared__ float s_sum[2][kBlock / 32];
     const int group = threadIdx.x / tpr, lane = threadIdx.x % tpr;
     const int rows = blockDim.x / tpr;
-    const int units = a.H / kCols;
     pdl_wait();
     pdl_trigger();
     int T = a.T_max;
@@ -180,71 +240,87 @@ __global__ void __launch_bounds__(kMaxBlock, kLean<kF32, kV, kRes> ? 2 : 1) norm
         T = *a.d_num_tokens;
         T = T < 0 ? 0 : (T > a.T_max ? a.T_max : T);
     }
+    const int step = gridDim.x * rows;
+    int t = blockIdx.x * rows + group;
+    // this thread's first column of its next row in each tensor
+    const int col0 = lane * kCols;
+    const char *h_at = static_cast<const char *>(a.h) + (t * a.h_stride + col0) * kBytes;
+    const __nv_bfloat16 *y_at = static_cast<const __nv_bfloat16 *>(a.y) + t * a.y_stride + col0;
+    bool on[kV];      // columns past H: never loaded, zero
     uint4 h[kV];
     typename U::Half y[kRes ? kV : 1];
-    auto load = [&](long long t) {
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            const int u = lane + v * tpr;
-            if (t < T && u < units) {
-                h[v] = ld_stream(static_cast<const char *>(a.h) + (t * a.h_stride + u * kCols) * (kF32 ? 4 : 2));
+    for (int v = 0; v < kV; ++v) {
+        on[v] = col0 + v * tpr * kCols < a.H;
+        h[v] = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kRes)
+            y[v] = typename U::Half{};
+    }
+    auto load = [&]() {
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+            if (on[v]) {
+                h[v] = ld_stream(h_at + v * tpr * kCols * kBytes);
                 if constexpr (kRes)
-                    y[v] = U::load_half(static_cast<const __nv_bfloat16 *>(a.y) + t * a.y_stride + u * kCols);
+                    y[v] = U::load_half(y_at + v * tpr * kCols);
             }
-        }
+        h_at += step * a.h_stride * kBytes;
+        if constexpr (kRes)
+            y_at += step * a.y_stride;
     };
-    const long long step = static_cast<long long>(gridDim.x) * rows;
-    long long base = static_cast<long long>(blockIdx.x) * rows;
-    if (kAhead)
-        load(base + group);
-    for (; base < T; base += step) {
-        const long long t = base + group;
-        if (!kAhead)
-            load(t);
+    if (kAhead && t < T)
+        load();
+    for (int base = blockIdx.x * rows; base < T; base += step, t += step) {
         const bool row = t < T;
-        float f[kV][kCols];
+        if (!kAhead && row)
+            load();
+        Pair f[kV][kPairs];
         if constexpr (kRes) {
-            float n[kV][kCols];
-            float q = 0.f;
+            Pair n[kV][kPairs];
+            Pair q = 0ull;
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
-                U::floats(h[v], f[v]);
-                U::half_floats(y[v], n[v]);
-                if (row && lane + v * tpr < units)
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        q = fmaf(n[v][i], n[v][i], q);
+                U::pairs(h[v], f[v]);
+                U::half_pairs(y[v], n[v]);
             }
-            if (kAhead)
-                load(t + step);
-            const float r = a.norm_block ? 1.f / sqrtf(row_sum(q, tpr, s_sum[0]) / a.H + a.eps) : 1.f;
-            const float s = (row && a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float *>(a.gate)[t] : 1.f) * a.scale;
+            if (kAhead && t + step < T)
+                load();
+            if (a.norm_block) {
 #pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                const int u = lane + v * tpr;
-                if (!row || u >= units)
-                    continue;
-                float c[kCols];
-                if (a.norm_block) {
-                    norm_weight<kF32>(a, a.w_post, u * kCols, c);
+                for (int v = 0; v < kV; ++v)
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        n[v][i] *= r * c[i];
+                    for (int i = 0; i < kPairs; ++i)
+                        q = fma2(n[v][i], n[v][i], q);
+                const float r = rsqrtf(fmaf(row_sum(q, tpr, s_sum[0]), inv_H, a.eps));
+#pragma unroll
+                for (int v = 0; v < kV; ++v)
+                    if (on[v])
+                        U::apply_norm(a, a.w_post, col0 + v * tpr * kCols, r, n[v]);
+            }
+            if (row) {
+                const float s = (a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float *>(a.gate)[t] : 1.f) * a.scale;
+                const Pair s2 = pair(s, s);
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    const int m = col0 + v * tpr * kCols;
+                    if (!on[v])
+                        continue;
+                    if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_ELEMENT) {
+                        Pair c[kPairs];
+                        if (a.gate_kind == MOE_GATE_CHANNEL)
+                            U::channel(a.gate, a.w_f32, m, c);
+                        else
+                            U::half_pairs(U::load_half(static_cast<const __nv_bfloat16 *>(a.gate) + t * a.gate_stride + m),
+                                          c);
+#pragma unroll
+                        for (int i = 0; i < kPairs; ++i)
+                            n[v][i] = mul2(n[v][i], c[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i)
+                        f[v][i] = fma2(s2, n[v][i], f[v][i]);
+                    U::store(static_cast<char *>(a.h_out) + (t * a.out_stride + m) * kBytes, f[v]);
                 }
-                if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_ELEMENT) {
-                    if (a.gate_kind == MOE_GATE_CHANNEL)
-                        U::channel(a.gate, a.w_f32, u * kCols, c);
-                    else
-                        U::half_floats(U::load_half(static_cast<const __nv_bfloat16 *>(a.gate) + t * a.gate_stride +
-                                                    u * kCols), c);
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        n[v][i] *= c[i];
-                }
-#pragma unroll
-                for (int i = 0; i < kCols; ++i)
-                    f[v][i] = fmaf(s, n[v][i], f[v][i]);
-                U::store(static_cast<char *>(a.h_out) + (t * a.out_stride + u * kCols) * (kF32 ? 4 : 2), f[v]);
             }
             if (!a.x) {
                 if (tpr != 32)
@@ -254,78 +330,76 @@ __global__ void __launch_bounds__(kMaxBlock, kLean<kF32, kV, kRes> ? 2 : 1) norm
         } else {
 #pragma unroll
             for (int v = 0; v < kV; ++v)
-                U::floats(h[v], f[v]);
-            if (kAhead)
-                load(t + step);
+                U::pairs(h[v], f[v]);
+            if (kAhead && t + step < T)
+                load();
         }
-        float q = 0.f;
+        Pair q = 0ull;
 #pragma unroll
         for (int v = 0; v < kV; ++v)
-            if (row && lane + v * tpr < units)
 #pragma unroll
-                for (int i = 0; i < kCols; ++i)
-                    q = fmaf(f[v][i], f[v][i], q);
-        const float r = 1.f / sqrtf(row_sum(q, tpr, s_sum[1]) / a.H + a.eps);
+            for (int i = 0; i < kPairs; ++i)
+                q = fma2(f[v][i], f[v][i], q);
+        const float r = rsqrtf(fmaf(row_sum(q, tpr, s_sum[1]), inv_H, a.eps));
+        if (row) {
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            const int u = lane + v * tpr;
-            if (!row || u >= units)
-                continue;
-            float c[kCols];
-            norm_weight<kF32>(a, a.w_next, u * kCols, c);
-#pragma unroll
-            for (int i = 0; i < kCols; ++i)
-                f[v][i] *= r * c[i];
-            U::store_half(static_cast<__nv_bfloat16 *>(a.x) + t * a.x_stride + u * kCols, f[v]);
+            for (int v = 0; v < kV; ++v) {
+                const int m = col0 + v * tpr * kCols;
+                if (!on[v])
+                    continue;
+                U::apply_norm(a, a.w_next, m, r, f[v]);
+                U::store_half(static_cast<__nv_bfloat16 *>(a.x) + t * a.x_stride + m, f[v]);
+            }
         }
         if ((!kRes || !a.norm_block) && tpr != 32)
             __syncthreads();   // one sum per row: s_sum[1] is free for the next row
     }
 }
 
-template <bool kF32, int kV>
+template <bool kF32, int kV, bool kRes, int kBlock>
 cudaError_t launch(const NormArgs &a, int tpr, int num_sms, cudaStream_t stream, bool pdl)
 {
-    const int rows = tpr < 256 ? 256 / tpr : 1;
-    const int threads = rows * tpr;
+    const int rows = kBlock == 256 ? 256 / tpr : 1;
     const long long need = (static_cast<long long>(a.T_max) + rows - 1) / rows;
-    const long long most = static_cast<long long>(num_sms) * (1024 / threads);
-    const dim3 grid(static_cast<unsigned>(need < most ? need : most));
-    return a.y ? launch_k(norm_kernel<kF32, kV, true>, grid, dim3(threads), 0, stream, pdl, a, tpr)
-               : launch_k(norm_kernel<kF32, kV, false>, grid, dim3(threads), 0, stream, pdl, a, tpr);
+    const long long most = static_cast<long long>(num_sms) * Plan<kF32, kV, kRes, kBlock>::kPerSm;
+    return launch_k(norm_kernel<kF32, kV, kRes, kBlock>, dim3(static_cast<unsigned>(need < most ? need : most)),
+                    dim3(rows * tpr), 0, stream, pdl, a, tpr, 1.f / a.H);
 }
 
-template <bool kF32>
+template <bool kF32, bool kRes>
 cudaError_t launch_units(const NormArgs &a, int num_sms, cudaStream_t stream, bool pdl)
 {
-    // 32 bytes (bf16) or 64 bytes (fp32) of the stream per thread, fewer where
-    // a row would not fill a warp, more where it would need over 512 threads
+    // 16 columns a thread, fewer where a row would not fill a warp, up to 32
+    // to keep its group within 256 threads (several blocks per SM), then 512
     const int units = a.H / Unit<kF32>::kCols;
-    int v = kF32 ? 4 : 2;
+    constexpr int kFew = kF32 ? 4 : 2;
+    int v = kFew;
     while (v > 1 && units / v < 32)
         v /= 2;
-    while ((units + v - 1) / v > kMaxBlock)
+    if (units > 256 * v)
+        v = 2 * kFew;
+    while (units > 512 * v)
         v *= 2;
     const int tpr = ((units + v - 1) / v + 31) / 32 * 32;
-    switch (v) {
-    case 1:
-        return launch<kF32, 1>(a, tpr, num_sms, stream, pdl);
-    case 2:
-        return launch<kF32, 2>(a, tpr, num_sms, stream, pdl);
-    case 4:
-        return launch<kF32, 4>(a, tpr, num_sms, stream, pdl);
-    case 8:
-        return launch<kF32, 8>(a, tpr, num_sms, stream, pdl);
-    default:
-        return launch<kF32, 16>(a, tpr, num_sms, stream, pdl);
-    }
+    if (v == 1)
+        return launch<kF32, 1, kRes, 256>(a, tpr, num_sms, stream, pdl);
+    if (v == 2)
+        return launch<kF32, 2, kRes, 256>(a, tpr, num_sms, stream, pdl);
+    if (kF32 && v == 4)
+        return launch<true, 4, kRes, 256>(a, tpr, num_sms, stream, pdl);
+    if (v == 2 * kFew)
+        return tpr <= 256 ? launch<kF32, 2 * kFew, kRes, 256>(a, tpr, num_sms, stream, pdl)
+                          : launch<kF32, 2 * kFew, kRes, 512>(a, tpr, num_sms, stream, pdl);
+    return launch<kF32, 4 * kFew, kRes, 512>(a, tpr, num_sms, stream, pdl);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t stream, bool pdl)
 {
-    return a.h_f32 ? launch_units<true>(a, num_sms, stream, pdl) : launch_units<false>(a, num_sms, stream, pdl);
+    if (a.h_f32)
+        return a.y ? launch_units<true, true>(a, num_sms, stream, pdl) : launch_units<true, false>(a, num_sms, stream, pdl);
+    return a.y ? launch_units<false, true>(a, num_sms, stream, pdl) : launch_units<false, false>(a, num_sms, stream, pdl);
 }
 
 }  // namespace moe
