@@ -282,6 +282,51 @@ inline RouteSplit route_split(int T_max, int E, int H)
     return r;
 }
 
+// The tensor-core logits' tile (route_gemm.cu): experts of a tile and the CTAs
+// of a cluster that share one 128-token tile's K.
+struct RouteTile {
+    int experts, slices;
+};
+
+// TMEM accumulators that a tile's K blocks go round
+constexpr int route_accumulators(int experts) { return experts <= 128 ? 4 : 2; }
+
+// The pair with the shortest estimate in cycles: waves of clusters over the
+// GPU, each CTA its K blocks at their operand bytes at 64 a cycle (above the
+// MMAs' cycles at these widths), the exchange of the partial rows and a fixed
+// start and end. kHeld[s]: clusters of s one-per-SM CTAs that a GB300 holds at
+// once, as its occupancy query reports; the 16 clusters of eight of T=1024,
+// E=256, H=4096 run in two waves, 22.1 us against 14.3 in clusters of six.
+// Measured otherwise (graph replays): T=2048, E=384, H=7168, 192 x 4 slices
+// 22.5 us, 192 x 3 25.1, 256 x 4 24.1, 128 x 4 35.7; T=256, E=256, H=7168,
+// 64 x 8 12.5, 128 x 8 14.3; T=8192, E=128, H=4096, 128 x 2 23.0, 64 x 1 30.2.
+// Tiles whose chains of MMAs are longer than 80 are taken only if all are: the
+// tensor cores truncate as they add (route_gemm.cu).
+inline RouteTile route_tile(int T_max, int E, int H)
+{
+    constexpr int kHeld[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+    RouteTile best = {64, 1};
+    double best_cycles = 1e30;
+    for (int n = 64; n <= 256; n += 64) {
+        if (n > 64 && n - 64 >= E)
+            break;
+        for (int s = 1; s <= 8 && s <= H / 64; ++s) {
+            const int blocks = (H / 64 + s - 1) / s;
+            const int chain = 4 * ((blocks + route_accumulators(n) - 1) / route_accumulators(n));
+            const long long clusters = ((static_cast<long long>(T_max) + 127) / 128) * ((E + n - 1) / n);
+            const double waves = static_cast<double>((clusters + kHeld[s] - 1) / kHeld[s]);
+            double cycles = waves * (3000.0 + blocks * 2.0 * (128 + n) + (s > 1 ? 128.0 * n * 4 / 32 : 0));
+            if (chain > 80)
+                cycles += 1e9 * chain;
+            if (cycles < best_cycles) {
+                best_cycles = cycles;
+                best = {n, s};
+            }
+        }
+    }
+    return best;
+}
+
 // Floats of scratch: the slices' partial logits and sums of squares (few
 // tokens), or the logits.
 inline size_t route_scratch_floats(int T_max, int E, int H)
@@ -290,36 +335,6 @@ inline size_t route_scratch_floats(int T_max, int E, int H)
     if (T_max > kRouteFewTokens)
         return T * E;
     return static_cast<size_t>(route_split(T_max, E, H).slices) * T * (E + 1);
-}
-
-// The tensor-core logits' tile (route_gemm.cu): experts of a tile and the CTAs
-// of a cluster that share one 128-token tile's K.
-struct RouteTile {
-    int experts, slices;
-};
-
-// The pair with the shortest estimate: waves of CTAs over 152 SMs, each its K
-// blocks at the larger of their MMA cycles and their operand bytes at 64 a
-// cycle, plus the exchange of the partial rows and a fixed start and end.
-inline RouteTile route_tile(int T_max, int E, int H)
-{
-    RouteTile best = {64, 1};
-    double best_cycles = 1e30;
-    for (int n = 64; n <= 256; n += 64) {
-        if (n > 64 && n - 64 >= E)
-            break;
-        for (int s = 1; s <= 8 && s <= H / 64; s *= 2) {
-            const double ctas = static_cast<double>((T_max + 127) / 128) * ((E + n - 1) / n) * s;
-            const double waves = static_cast<double>(static_cast<long long>((ctas + 151) / 152));
-            const double block = 2.0 * n > 2.0 * (128 + n) ? 2.0 * n : 2.0 * (128 + n);
-            const double cycles = waves * (3000.0 + (H / 64 + s - 1) / s * block + (s > 1 ? 128.0 * n * 4 / 32 : 0));
-            if (cycles < best_cycles) {
-                best_cycles = cycles;
-                best = {n, s};
-            }
-        }
-    }
-    return best;
 }
 
 // logits[t, e] for the rows t < T (T_max > kRouteFewTokens)

@@ -16,7 +16,9 @@
 // bytes and nothing is permuted.
 //
 // More tokens: logits on the tensor cores (route_gemm.cu), then a warp per
-// token selects.
+// token selects. (Selecting inside that kernel, a warp per token from the rows
+// in shared memory, measured no better: T=8192, E=128 24.0 against 23.0 us,
+// since there only 16 warps per SM are left to hide its latency.)
 //
 // In moe_layer the token operand is u = h * w_pre without r(h), which the sum
 // does not need before its end: logits = r * sum u w. u is split exactly into
@@ -27,291 +29,38 @@
 
 #include "moe_internal.h"
 #include "ptx.cuh"
+#include "route_select.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
-
-__device__ __forceinline__ int token_count(const int32_t *d_num_tokens, int T_max)
-{
-    int T = T_max;
-    if (d_num_tokens) {
-        T = *d_num_tokens;
-        T = T < 0 ? 0 : (T > T_max ? T_max : T);
-    }
-    return T;
-}
-
-// A float as an unsigned integer of the same order; 0 for what may not be
-// chosen (-inf and NaN). -0 and +0 give the same number.
-__device__ __forceinline__ uint32_t order_key(float f)
-{
-    f = f + 0.f;
-    const uint32_t b = __float_as_uint(f);
-    const uint32_t u = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-    return f > -INFINITY ? u : 0u;   // false for NaN too
-}
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        v += __shfl_xor_sync(kFull, v, o);
-    return v;
-}
-
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-    return v;
-}
-
-__device__ __forceinline__ float score_of(const RouteArgs &a, float l, float mx, float sum)
-{
-    return a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - mx) / sum;
-}
-
-// Float of an order_key (which is not 0).
-__device__ __forceinline__ float key_value(uint32_t u)
-{
-    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
-}
-
-// log of the sigmoid, without overflow or a loss of small values
-__device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.f) - log1pf(expf(-fabsf(l))); }
-
-// The chosen experts' ids and weights, by one warp: a lane holds up to two of
-// them (id -1: none) with their places; mx and sum are the softmax's maximum
-// and denominator, used when the scores are not renormalised. n: how many were
-// found; places from n on get id -1 and weight 0.
-__device__ __forceinline__ void store_choice(const RouteArgs &a, int t, const int (&id)[2], const int (&place)[2],
-                                             const float (&l)[2], int n, float mx, float sum)
-{
-    float w[2], norm = 1.f;
-    if (a.renormalize) {
-        // the chosen scores over their sum, from their logarithms (the softmax
-        // over all E cancels), so that scores that underflow keep their ratios
-        float lg[2], top = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            lg[q] = id[q] >= 0 ? (a.sigmoid ? log_sigmoid(l[q]) : l[q]) : -INFINITY;
-            top = fmaxf(top, lg[q]);
-        }
-        top = warp_max(top);
-        top = top > -INFINITY ? top : 0.f;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-            w[q] = expf(lg[q] - top);
-        norm = warp_sum(w[0] + w[1]);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-            w[q] = id[q] >= 0 ? score_of(a, l[q], mx, sum) : 0.f;
-    }
-    int32_t *ids = a.ids + static_cast<size_t>(t) * a.k;
-    float *weights = a.weights + static_cast<size_t>(t) * a.k;
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-        if (id[q] >= 0) {
-            ids[place[q]] = id[q];
-            weights[place[q]] = a.scale * (w[q] / norm);
-        }
-    for (int j = n + (threadIdx.x & 31); j < a.k; j += 32) {
-        ids[j] = -1;
-        weights[j] = 0.f;
-    }
-}
-
-// Which groups stay, from lane g's group value: bit g of the result. One warp.
-__device__ __forceinline__ unsigned keep_groups(const RouteArgs &a, float value)
-{
-    const int lane = threadIdx.x & 31;
-    if (!(value > -INFINITY))   // also the sum of +inf and -inf
-        value = -INFINITY;
-    int rank = 0;
-    for (int g = 0; g < a.n_group; ++g) {
-        const float o = __shfl_sync(kFull, value, g);
-        rank += (o > value || (o == value && g < lane)) ? 1 : 0;
-    }
-    return __ballot_sync(kFull, lane < a.n_group && rank < a.topk_group);
-}
-
-// One warp selects for one token whose logits lie in logits[E]; lane i holds
-// experts i, i + 32, ... s_key[E]: this warp's scratch, used with groups only.
-// s_found: 32 words of scratch.
-//
-// k rounds of a warp-wide maximum over all keys would cost k passes over the
-// lane's registers. The k-th largest of the lanes' own maxima is a lower bound
-// of the k-th largest key, and few keys reach it (9 or 10 of 128 or 384 at
-// k = 6 to 8): those are gathered, and each counts the ones that beat it. More
-// than 32 of them (many equal keys), or k > 32, take the rounds.
-template <int kPer>
-__device__ __forceinline__ void select_body(const RouteArgs &a, int t, const float *logits, float *s_key,
-                                            uint64_t *s_found)
-{
-    const int lane = threadIdx.x & 31;
-    float l[kPer];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        l[i] = lane + 32 * i < a.E ? logits[lane + 32 * i] : 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const bool real = lane + 32 * i < a.E;
-        if (real && !(l[i] < INFINITY)) {   // NaN or +inf
-            bad = true;
-            l[i] = -INFINITY;
-        }
-        if (!real)
-            l[i] = -INFINITY;
-    }
-    if (__any_sync(kFull, bad) && lane == 0)
-        atomicOr(a.err, MOE_DEVERR_BAD_LOGIT);
-    const bool by_score = a.bias != nullptr || a.group_top > 1;
-    float mx = -INFINITY, sum = 1.f;
-    if (!a.sigmoid && (by_score || !a.renormalize)) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            mx = fmaxf(mx, l[i]);
-        mx = warp_max(mx);
-        mx = mx > -INFINITY ? mx : 0.f;
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            sum += expf(l[i] - mx);
-        sum = warp_sum(sum);
-    }
-    uint32_t key[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        float v = l[i];
-        if (by_score && e < a.E && v > -INFINITY)
-            v = score_of(a, v, mx, sum) + (a.bias ? a.bias[e] : 0.f);
-        key[i] = e < a.E ? order_key(v) : 0u;
-        if (a.n_group > 1 && e < a.E)
-            s_key[e] = key[i] ? v : -INFINITY;
-    }
-    if (a.n_group > 1) {
-        __syncwarp();
-        const int gs = a.E / a.n_group;
-        float value = -INFINITY;
-        if (lane < a.n_group) {
-            float first = -INFINITY, second = -INFINITY;
-            for (int i = 0; i < gs; ++i) {
-                const float v = s_key[lane * gs + i];
-                if (v > first) {
-                    second = first;
-                    first = v;
-                } else if (v > second) {
-                    second = v;
-                }
-            }
-            value = a.group_top > 1 ? first + second : first;
-        }
-        const unsigned kept = keep_groups(a, value);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E && !((kept >> (e / gs)) & 1u))
-                key[i] = 0u;
-        }
-        __syncwarp();
-    }
-    int my_id[2] = {-1, -1}, place[2] = {lane, lane + 32};
-    float my_l[2] = {-INFINITY, -INFINITY};
-    int n = 0;
-    uint32_t own = 0u;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        own = max(own, key[i]);
-    uint32_t least = 0u;
-    if (a.k <= 32)
-#pragma unroll 1
-        for (int j = 0; j < a.k; ++j) {
-            least = __reduce_max_sync(kFull, own);
-            if (least == 0u)
-                break;
-            if (lane == __ffs(__ballot_sync(kFull, own == least)) - 1)
-                own = 0u;
-        }
-    least = max(least, 1u);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const unsigned b = __ballot_sync(kFull, key[i] >= least);
-        const int slot = n + __popc(b & ((1u << lane) - 1u));
-        if (key[i] >= least && slot < 32)
-            s_found[slot] = static_cast<uint64_t>(key[i]) << 32 | static_cast<uint32_t>(~(lane + 32 * i));
-        n += __popc(b);
-    }
-    if (n <= 32 && a.k <= 32) {
-        __syncwarp();
-        const uint64_t mine = lane < n ? s_found[lane] : 0u;
-        int rank = 0;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i)
-            rank += s_found[i] > mine ? 1 : 0;
-        if (lane < n && rank < a.k) {
-            my_id[0] = static_cast<int>(~static_cast<uint32_t>(mine));
-            place[0] = rank;
-            my_l[0] = by_score ? logits[my_id[0]] : key_value(static_cast<uint32_t>(mine >> 32));
-        }
-        n = min(n, a.k);
-    } else {
-        // k rounds: the largest key, the lowest expert among equals
-        n = 0;
-#pragma unroll 1
-        for (; n < a.k; ++n) {
-            uint32_t best = 0u;
-            int at = 1 << 30;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = lane + 32 * i;
-                }
-            const uint32_t top = __reduce_max_sync(kFull, best);
-            if (top == 0u)
-                break;
-            const int e = __reduce_min_sync(kFull, best == top ? at : 1 << 30);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (lane + 32 * i == e)
-                    key[i] = 0u;
-            if (lane == (n & 31)) {
-                my_id[n >> 5] = e;
-                my_l[n >> 5] = logits[e];
-            }
-        }
-    }
-    store_choice(a, t, my_id, place, my_l, n, mx, sum);
-}
-
 // ------------------------------------------------------------ many tokens
 
 constexpr int kSelectWarps = 4;
 
-// A warp per token, one instance per 128, 256, 512 or 1024 experts: with the
-// registers of the largest (128) only 16 warps fit on an SM, and the chain of
-// warp-wide reductions is latency.
+// One instance per 128, 256, 512 or 1024 experts: with the registers of the
+// largest only a few warps fit on an SM.
 template <int kPer>
 __global__ void __launch_bounds__(32 * kSelectWarps) select_kernel(const __grid_constant__ RouteArgs a,
                                                                    const float *logits)
 {
     extern __shared__ float s_keys[];   // [kSelectWarps][E], with groups only
-    __shared__ uint64_t s_found[kSelectWarps][32];
+    __shared__ SelectWarp s_warp[kSelectWarps];
     pdl_wait();
     pdl_trigger();
     const int T = token_count(a.d_num_tokens, a.T_max);
     const int warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kSelectWarps + warp;
     if (t < T)
-        select_body<kPer>(a, t, logits + static_cast<size_t>(t) * a.E, s_keys + warp * a.E,
-                          s_found[warp]);
+        select_token<kPer>(a, t, logits + static_cast<size_t>(t) * a.E, s_keys + warp * a.E, s_warp[warp]);
+}
+
+template <int kPer>
+cudaError_t launch_select(const RouteArgs &a, const float *logits, cudaStream_t stream, bool pdl)
+{
+    return launch_k(select_kernel<kPer>, dim3((a.T_max + kSelectWarps - 1) / kSelectWarps), dim3(32 * kSelectWarps),
+                    a.n_group > 1 ? sizeof(float) * kSelectWarps * a.E : 0, stream, pdl, a, logits);
 }
 
 // ------------------------------------------------------------- few tokens
@@ -394,7 +143,6 @@ __device__ void select_block(const RouteArgs &a, int t, SelectScratch &s)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = a.E, k = a.k;
-    const bool by_score = a.bias != nullptr || a.group_top > 1;
     bool bad = false;
     float mx = -INFINITY, sum = 1.f;
     for (int e = tid; e < E; e += kFewThreads) {
@@ -407,7 +155,7 @@ __device__ void select_block(const RouteArgs &a, int t, SelectScratch &s)
     }
     if (bad)
         atomicOr(a.err, MOE_DEVERR_BAD_LOGIT);
-    if (!a.sigmoid && (by_score || !a.renormalize)) {
+    if (needs_softmax(a)) {
         mx = warp_max(mx);
         if (lane == 0)
             s.warp[warp] = mx;
@@ -427,12 +175,8 @@ __device__ void select_block(const RouteArgs &a, int t, SelectScratch &s)
         for (int i = 0; i < kFewWarps; ++i)
             sum += s.warp[i];
     }
-    for (int e = tid; e < E; e += kFewThreads) {
-        float v = s.logits[e];
-        if (by_score && v > -INFINITY)
-            v = score_of(a, v, mx, sum) + (a.bias ? a.bias[e] : 0.f);
-        s.key[e] = order_key(v);
-    }
+    for (int e = tid; e < E; e += kFewThreads)
+        s.key[e] = order_key(key_float(a, e, s.logits[e], mx, sum));
     if (a.n_group > 1) {
         const int gs = E / a.n_group;
         __syncthreads();
@@ -768,12 +512,13 @@ cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t stream, b
     const cudaError_t e = launch_route_gemm(a, logits, stream, pdl);
     if (e != cudaSuccess)
         return e;
-    auto kern = a.E <= 128   ? select_kernel<4>
-                : a.E <= 256 ? select_kernel<8>
-                : a.E <= 512 ? select_kernel<16>
-                             : select_kernel<32>;
-    return launch_k(kern, dim3((a.T_max + kSelectWarps - 1) / kSelectWarps), dim3(32 * kSelectWarps),
-                    a.n_group > 1 ? sizeof(float) * kSelectWarps * a.E : 0, stream, pdl, a, logits);
+    if (a.E <= 128)
+        return launch_select<4>(a, logits, stream, pdl);
+    if (a.E <= 256)
+        return launch_select<8>(a, logits, stream, pdl);
+    if (a.E <= 512)
+        return launch_select<16>(a, logits, stream, pdl);
+    return launch_select<32>(a, logits, stream, pdl);
 }
 
 }  // namespace moe

@@ -6,26 +6,27 @@
 // most SMs idle (64 tiles at T=8192, E=128); a cluster of `slices` CTAs
 // shares one tile instead, each over its slice of H, and the partial
 // accumulators meet through distributed shared memory: every CTA sends each
-// peer the 128 / slices rows that peer owns, and the owner adds the slices
+// peer the ceil(128 / slices) rows that peer owns, and the owner adds the slices
 // in rank order (the same bits whatever the timing) and stores its rows.
 //
 // Per CTA: warp 0 feeds a ring of TMA stages (128-byte swizzled 64-wide K
-// blocks of x and w), warp 1 issues tcgen05.mma, then all eight warps move the
+// blocks of x and w), warp 1 issues tcgen05.mma, then all 16 warps move the
 // accumulators out. The tensor cores truncate as they accumulate, so one long
 // chain of MMAs drifts (2.1e-6 of the logits' norm after 128 of them, at
 // H=4096 in two slices); the K blocks go round over as many TMEM accumulators
-// as fit (four of 64 or 128 experts, two of 192 or 256), added in fp32 on the
-// way out.
+// as fit (four of 64 or 128 experts, two of 192 or 256; 4.7e-7 then), added in
+// fp32 on the way out.
 #include <cuda_bf16.h>
 
 #include "moe_internal.h"
 #include "ptx.cuh"
+#include "route_select.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kGemmThreads = 256;
+constexpr int kGemmThreads = 512;
 constexpr int kTokens = 128;
 
 template <int kBN>
@@ -34,12 +35,14 @@ struct RouteCfg {
     static constexpr int kStageBytes = kXBytes + kBN * 128;
     static constexpr int kStages = 196608 / kStageBytes;   // 4 at 256 experts to 8 at 64
     static constexpr int kRowFloats = kBN + 4;             // rows of the exchange buffer, 16 bytes apart in banks
-    static constexpr int kExchangeBytes = kTokens * kRowFloats * 4;
+    // slices * ceil(128 / slices) rows: at most 133 (seven slices)
+    static constexpr int kExchangeBytes = 133 * kRowFloats * 4;
     static constexpr int kDynSmem =
         1024 + (kStages * kStageBytes > kExchangeBytes ? kStages * kStageBytes : kExchangeBytes);
-    static constexpr int kAccs = kBN <= 128 ? 4 : 2;
+    static constexpr int kAccs = route_accumulators(kBN);
     static constexpr int kTmemCols = kBN <= 64 ? 256 : 512;
     static constexpr uint32_t kIdesc = idesc_bf16_f32(kTokens, kBN);
+    static_assert(kAccs * kBN <= kTmemCols, "accumulators");
     static_assert(kBN % 64 == 0 && kBN <= 256, "expert tile");
 };
 
@@ -53,8 +56,8 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t *v)
 template <int kBN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     route_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                      const int32_t *d_num_tokens, int T_max, int E, int H, int slices, float *__restrict__ logits,
-                      int32_t *err, uint64_t wait_limit_ns)
+                      const __grid_constant__ RouteArgs a, int slices, float *__restrict__ logits,
+                      uint64_t wait_limit_ns)
 {
     using C = RouteCfg<kBN>;
     extern __shared__ uint8_t smem_raw[];
@@ -87,17 +90,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t tmem = s_tmem_base;
     pdl_wait();
     pdl_trigger();
-    int T = T_max;
-    if (d_num_tokens) {
-        T = *d_num_tokens;
-        T = T < 0 ? 0 : (T > T_max ? T_max : T);
-    }
+    const int T = token_count(a.d_num_tokens, a.T_max);
+    const int E = a.E;
     const int rank = static_cast<int>(cluster_ctarank());
     const int n_tiles = (E + kBN - 1) / kBN;
     const int tile = blockIdx.x / slices;
     const int e0 = (tile % n_tiles) * kBN;
     const int t0 = (tile / n_tiles) * kTokens;
-    const int blocks = H / 64;
+    const int blocks = a.H / 64;
     const int kb0 = rank * blocks / slices, kb1 = (rank + 1) * blocks / slices;
     const bool active = t0 < T;     // the same in every CTA of the cluster
 
@@ -144,36 +144,36 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tc_fence_after();
         __syncthreads();
         cluster_sync();   // every peer's stages are free: they become the exchange buffers
-        // row = TMEM lane; warps w and w + 4 take half of its columns each
+        // row = TMEM lane; the four warps of a lane quarter take a quarter of its columns each
         const int row = (warp & 3) * 32 + lane;
-        const int own = kTokens / slices;
+        const int own = (kTokens + slices - 1) / slices;
         const uint32_t dst = map_to_cta(
             smem_u32(smem) + static_cast<uint32_t>((rank * own + row % own) * C::kRowFloats * 4), row / own);
         const int accs = min(C::kAccs, kb1 - kb0);
 #pragma unroll 1
-        for (int c = (warp >> 2) * (kBN / 2); c < ((warp >> 2) + 1) * (kBN / 2); c += 32) {
+        for (int c = (warp >> 2) * (kBN / 4); c < ((warp >> 2) + 1) * (kBN / 4); c += 16) {
             const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c;
-            uint32_t r[C::kAccs][32];
+            uint32_t r[C::kAccs][16];
 #pragma unroll
             for (int q = 0; q < C::kAccs; ++q)
                 if (q < accs)
-                    tmem_ld_32x32b_x32(at + q * kBN, r[q]);
+                    tmem_ld_32x32b_x16(at + q * kBN, r[q]);
             tmem_wait_ld();
 #pragma unroll
             for (int q = 1; q < C::kAccs; ++q)
                 if (q < accs)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
+                    for (int i = 0; i < 16; ++i)
                         r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) + __uint_as_float(r[q][i]));
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
+            for (int i = 0; i < 16; i += 4)
                 st_cluster_v4(dst + (c + i) * 4, r[0] + i);
         }
         cluster_sync();
+        const float *const buf = reinterpret_cast<const float *>(smem);
+        const int t_own = t0 + rank * own;
         if (!s_abort) {
-            const float *buf = reinterpret_cast<const float *>(smem);
             const bool whole = E % 4 == 0;   // rows of logits 16-byte aligned
-            const int t_own = t0 + rank * own;
 #pragma unroll 4
             for (int i = threadIdx.x; i < own * (kBN / 4); i += kGemmThreads) {
                 const int r = i / (kBN / 4), c = 4 * (i % (kBN / 4));
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     const float4 p = *reinterpret_cast<const float4 *>(src + s * own * C::kRowFloats);
                     v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
                 }
-                if (t_own + r >= T)
+                if (t_own + r >= T || rank * own + r >= kTokens)
                     continue;
                 float *out = logits + static_cast<size_t>(t_own + r) * E + e0 + c;
                 if (whole && e0 + c < E) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tmem_dealloc(tmem, C::kTmemCols);
     }
     if (threadIdx.x == 0 && s_abort)
-        atomicOr(err, MOE_DEVERR_WAIT_TIMEOUT);
+        atomicOr(a.err, MOE_DEVERR_WAIT_TIMEOUT);
 }
 
 template <int kBN>
@@ -242,8 +242,7 @@ cudaError_t run(const RouteArgs &a, int slices, float *logits, cudaStream_t stre
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, a.d_num_tokens, a.T_max, a.E, a.H, slices, logits, a.err,
-                              kWaitLimitNs);
+    return cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, a, slices, logits, kWaitLimitNs);
 }
 
 }  // namespace

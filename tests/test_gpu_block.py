@@ -191,7 +191,7 @@ def run_route(B, p, x, w, bias=None, logits=None, T_dev=None, ws=None):
 
 ROUTE_SHAPES = [(1, 1, 1, 64), (1, 384, 6, 7168), (2, 7, 7, 128), (9, 33, 4, 192), (31, 130, 8, 2880), (64, 256, 8, 1024),
                 (65, 128, 64, 512), (100, 1000, 10, 448), (129, 384, 6, 1536), (300, 512, 8, 512), (513, 96, 2, 4096),
-                (1025, 1024, 16, 256), (2500, 64, 8, 320)]
+                (300, 128, 64, 128), (200, 200, 33, 64),                 (1025, 1024, 16, 256), (2500, 64, 8, 320)]
 
 
 @pytest.mark.parametrize("T,E,k,H", ROUTE_SHAPES)
@@ -210,6 +210,24 @@ def test_route_exact_logits_and_ties(B, T, E, k, H, score, renorm):
     assert B.moe_last_device_error(ws) == 0
     again, wt2, _ = run_route(B, p, x, w, ws=ws)      # no logits asked for, the same workspace again
     assert torch.equal(again, ids) and torch.equal(wt2, wt)
+
+
+@pytest.mark.parametrize("T", [2, 200])
+@pytest.mark.parametrize("E,k", [(100, 8), (70, 40)])
+def test_route_equal_logits(B, T, E, k):
+    """All experts equal: the lowest k, in order; and rows where only a few differ."""
+    H = 64
+    x = torch.ones((T, H), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((E, H), dtype=torch.bfloat16, device="cuda")
+    w[50:53, 0] = 1.0
+    x[0] = 0
+    x[-1] = -1
+    for score in (0, 1):
+        p = B.RouterProblem.make(T, E, k, H, score=score)
+        ids, wt, _ = run_route(B, p, x, w)
+        want_ids, want_w, _ = ref.route(ref.f64(x) @ ref.f64(w).T, k, ("softmax", "sigmoid")[score])
+        assert np.array_equal(ids.cpu().numpy(), want_ids)
+        check(wt, want_w, np.abs(want_w) * 4e-6, "weights")
 
 
 @pytest.mark.parametrize("T,E,k,H", [(1, 384, 6, 7168), (40, 256, 8, 2880), (515, 384, 6, 7168), (2048, 128, 8, 4096),
