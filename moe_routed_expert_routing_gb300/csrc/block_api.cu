@@ -98,7 +98,7 @@ RouteLayout route_layout(const moe_router_problem_t &p)
 {
     RouteLayout L;
     L.part = workspace_header_bytes();
-    L.total = align_up(L.part + sizeof(float) * route_scratch_floats(p.T_max, p.E, p.H));
+    L.total = align_up(L.part + sizeof(float) * route_scratch_floats(p.T_max, p.E, p.H, false));
     return L;
 }
 
@@ -149,7 +149,7 @@ moe_status_t layer_layout(const moe_layer_problem_t &p, LayerLayout *L)
     L->x = o;
     o = align_up(o + 2 * T * H);
     L->part = o;
-    o = align_up(o + sizeof(float) * route_scratch_floats(p.experts.T_max, p.experts.E, p.experts.H));
+    o = align_up(o + sizeof(float) * route_scratch_floats(p.experts.T_max, p.experts.E, p.experts.H, true));
     L->y = o;
     o = align_up(o + 2 * T * H);
     L->total = o;
@@ -273,7 +273,7 @@ moe_status_t moe_route(const moe_router_problem_t *problem, const void *x, const
     a.err = at<int32_t>(ws, 0);
     a.counters = at<int32_t>(ws, route_counters_offset());
     a.part = at<float>(ws, L.part);
-    return cuda_status(launch_route(a, device_sm_count(), static_cast<cudaStream_t>(stream), true));
+    return cuda_status(launch_route(a, static_cast<cudaStream_t>(stream), true));
 }
 
 moe_status_t moe_layer_workspace_size(const moe_layer_problem_t *problem, size_t *bytes)
@@ -312,7 +312,6 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
         (st = validate_device()) != MOE_OK || (st = check_forward(p.experts)) != MOE_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int sms = device_sm_count();
     void *x = at<void>(ws, L.x);
     NormArgs n = norm_args(p.norm, d_num_tokens);
     n.h = h;
@@ -340,10 +339,19 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
     r.err = at<int32_t>(ws, 0);
     r.counters = at<int32_t>(ws, route_counters_offset());
     r.part = at<float>(ws, L.part);
-    if ((st = cuda_status(launch_route(r, sms, s, true))) != MOE_OK)
+    // a few routed slots: the router's last CTA dispatches them (the one-kernel
+    // form of the experts dispatches by itself)
+    const bool dispatched = p.experts.T_max * p.experts.k <= kRouteDispatchSlots &&
+                            p.experts.forward_form != MOE_FORWARD_ONE_KERNEL;
+    if (dispatched) {
+        r.expert_offsets = expert_offsets;
+        r.perm = perm;
+        r.inv = forward_inv(p.experts, ws);
+    }
+    if ((st = cuda_status(launch_route(r, s, true))) != MOE_OK)
         return st;
     return enqueue_forward(p.experts, x, topk_ids, topk_weights, d_num_tokens, W13, W2, expert_offsets, perm,
-                           at<void>(ws, L.y), ws, s, nullptr, &n);
+                           at<void>(ws, L.y), ws, s, nullptr, &n, dispatched);
 }
 
 }  // extern "C"

@@ -26,11 +26,11 @@ struct Layout {
 // per-expert readiness counts and its three GPU-wide counters (CTAs through
 // their GEMM units, CTAs at the tail, units handed out), then the separate
 // grouped GEMMs' two (units handed out, CTAs at the tail), then the few-token
-// router's two (CTAs through with their units, CTAs out). The kernels leave
-// the counters at zero after every launch.
+// router's one (CTAs through with their part). The kernels leave the counters
+// at zero after every launch.
 constexpr size_t kReadyOffset = kAlign;
 constexpr size_t kCountersOffset = kReadyOffset + sizeof(int32_t) * kMaxExperts;
-constexpr size_t kHeaderBytes = (kCountersOffset + 7 * sizeof(int32_t) + kAlign - 1) / kAlign * kAlign;
+constexpr size_t kHeaderBytes = (kCountersOffset + 6 * sizeof(int32_t) + kAlign - 1) / kAlign * kAlign;
 
 void resolve(const moe_problem_t &p, int *path, int *tile_rows);
 
@@ -415,6 +415,8 @@ moe_status_t validate_device() { return check_device(); }
 
 size_t workspace_header_bytes() { return kHeaderBytes; }
 
+int32_t *forward_inv(const moe_problem_t &p, void *ws) { return at<int32_t>(ws, layout_of(p).inv); }
+
 size_t route_counters_offset() { return kCountersOffset + 5 * sizeof(int32_t); }
 
 bool use_pdl(const moe_problem_t &problem)
@@ -433,7 +435,7 @@ moe_status_t check_forward(const moe_problem_t &p)
 moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_t *topk_ids,
                              const float *topk_weights, const int32_t *d_num_tokens, const void *W13, const void *W2,
                              int32_t *expert_offsets, int32_t *perm, void *out, void *ws, cudaStream_t s,
-                             void *const *stage_events, const NormArgs *tail)
+                             void *const *stage_events, const NormArgs *tail, bool dispatched)
 {
     moe_status_t st = MOE_OK;
     const Layout L = layout_of(p);
@@ -481,9 +483,10 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
     const bool fused_mlp = fused_mlp_of(p, path, tile_rows);
     if ((st = mark(0)) != MOE_OK)
         return st;
-    st = cuda_status(launch_dispatch(topk_ids, d_num_tokens, p.T_max, p.k, p.E, at<int32_t>(ws, L.block_counts),
-                                     at<int32_t>(ws, L.block_base), expert_offsets, perm, inv,
-                                     at<int32_t>(ws, L.err), s, use_pdl(p)));
+    if (!dispatched)
+        st = cuda_status(launch_dispatch(topk_ids, d_num_tokens, p.T_max, p.k, p.E, at<int32_t>(ws, L.block_counts),
+                                         at<int32_t>(ws, L.block_base), expert_offsets, perm, inv,
+                                         at<int32_t>(ws, L.err), s, use_pdl(p)));
     if (st != MOE_OK || (st = mark(1)) != MOE_OK)
         return st;
     // On the M-small path the gate-up GEMM gathers its few rows per tile from x
@@ -509,7 +512,7 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
     // and the combine's inv. Measured at one token, E=384, H=7168, I=3072, in
     // one process, outputs bit-identical: 126.6 vs 127.5 us per call; at
     // eight tokens (full grid) +1.9 us, so those keep the plain form.
-    const bool dispatch_beside = fused_mlp && megakernel_possible(p) && p.weight_layout != MOE_WEIGHTS_MXFP8 &&
+    const bool dispatch_beside = !dispatched && fused_mlp && megakernel_possible(p) && p.weight_layout != MOE_WEIGHTS_MXFP8 &&
                                  fused_grid_sms(false, false, capacity_of(p), p.E, p.I, tile_rows, sms) < sms;
     if (dispatch_beside) {
         MegaParams mp;
@@ -686,7 +689,7 @@ static moe_status_t forward_impl(const moe_problem_t *problem, const void *x, co
     if ((st = check_forward(p)) != MOE_OK)
         return st;
     return enqueue_forward(p, x, topk_ids, topk_weights, d_num_tokens, W13, W2, expert_offsets, perm, out, ws,
-                           static_cast<cudaStream_t>(stream), stage_events, nullptr);
+                           static_cast<cudaStream_t>(stream), stage_events, nullptr, false);
 }
 
 moe_status_t moe_forward(const moe_problem_t *problem, const void *x, const int32_t *topk_ids,

@@ -247,7 +247,7 @@ struct RouteArgs {
     float *weights;
     float *logits;             // [T_max, E], or null: not wanted
     int32_t *err;
-    int32_t *counters;         // two, zero at launch and at exit (few tokens)
+    int32_t *counters;         // one, zero at launch and at exit (few tokens)
     float *part;               // workspace, route_scratch_floats() of them
     int T_max, E, k, H;
     int sigmoid, renormalize, n_group, topk_group, group_top;
@@ -257,28 +257,41 @@ struct RouteArgs {
     int normed, x_f32, w_f32, unit_offset;
     const void *w_pre;         // null: no weight
     void *x_out;               // [T_max, H] bf16
+    // moe_layer, at most kRouteDispatchSlots slots: moe_dispatch's tables, or null
+    int32_t *expert_offsets, *perm, *inv;
     long long x_stride;
     float eps;
 };
 
 // The few-token kernel's split of [T_max, E, H]: units of 16 experts x one
-// slice of H x up to 64 tokens, about one per SM.
+// slice of H x up to 32 tokens, about one per SM. Narrow units: the layer of 13
+// tokens of E=64, H=2048 took 81.8 us with two units of 8 tokens and 83.2 with
+// one of 16, the one of 64 tokens of E=128, H=4096 676 us in units of 16 or 32
+// and 681 in one of 64.
 struct RouteSplit {
-    int tiles;                 // 8-token tiles of a unit: 1, 2, 4 or 8
+    int tiles;                 // 8-token tiles of a unit: 1, 2 or 4
     int chunks, groups, slices;
+    bool join;                 // one kernel: its last CTA selects
 };
 
-constexpr int kRouteFewTokens = 128;
+// moe_route takes the few-token kernels up to here, then the tensor-core ones
+// (route_gemm.cu): 7.8 us against 12.2 at 16 tokens (E=256, H=7168), 10.8
+// against 9.9 at 32 (E=128, H=4096). moe_layer, whose router reads unrounded
+// rows, takes them always.
+constexpr int kRouteFewTokens = 16;
+constexpr int kRouteJoinTokens = 2;
+constexpr int kRouteDispatchSlots = 128;
 
 inline RouteSplit route_split(int T_max, int E, int H)
 {
     RouteSplit r;
-    r.tiles = T_max <= 8 ? 1 : (T_max <= 16 ? 2 : (T_max <= 32 ? 4 : 8));
+    r.tiles = T_max <= 16 ? 1 : (T_max <= 64 ? 2 : 4);
     r.chunks = (T_max + 8 * r.tiles - 1) / (8 * r.tiles);
     r.groups = (E + 15) / 16;
     const int blocks = H / 64;
     const int want = 152 / (r.groups * r.chunks);
     r.slices = want < 1 ? 1 : (want < blocks ? want : blocks);
+    r.join = T_max <= kRouteJoinTokens;
     return r;
 }
 
@@ -329,10 +342,10 @@ inline RouteTile route_tile(int T_max, int E, int H)
 
 // Floats of scratch: the slices' partial logits and sums of squares (few
 // tokens), or the logits.
-inline size_t route_scratch_floats(int T_max, int E, int H)
+inline size_t route_scratch_floats(int T_max, int E, int H, bool normed)
 {
     const size_t T = static_cast<size_t>(T_max);
-    if (T_max > kRouteFewTokens)
+    if (!normed && T_max > kRouteFewTokens)
         return T * E;
     return static_cast<size_t>(route_split(T_max, E, H).slices) * T * (E + 1);
 }
@@ -340,7 +353,7 @@ inline size_t route_scratch_floats(int T_max, int E, int H)
 // logits[t, e] for the rows t < T (T_max > kRouteFewTokens)
 cudaError_t launch_route_gemm(const RouteArgs &a, float *logits, cudaStream_t stream, bool pdl);
 
-cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl);
 
 // 2-D bf16 tensor map [rows, cols] (cols contiguous), box of 64 columns x
 // box_rows rows, 128-byte swizzle (grouped_gemm.cu).
@@ -361,15 +374,17 @@ moe_status_t validate_device();
 moe_status_t check_forward(const moe_problem_t &problem);
 // moe_forward after its checks. With `tail`, the combine's place is taken by
 // launch_combine_residual: `out` is scratch, and the block's output goes into
-// the residual stream as `tail` says.
+// the residual stream as `tail` says. With `dispatched`, expert_offsets, perm
+// and inv (forward_inv) are already written by the kernel before.
 moe_status_t enqueue_forward(const moe_problem_t &problem, const void *x, const int32_t *topk_ids,
                              const float *topk_weights, const int32_t *d_num_tokens, const void *W13, const void *W2,
                              int32_t *expert_offsets, int32_t *perm, void *out, void *ws, cudaStream_t stream,
-                             void *const *stage_events, const NormArgs *tail);
+                             void *const *stage_events, const NormArgs *tail, bool dispatched);
+int32_t *forward_inv(const moe_problem_t &problem, void *ws);
 // bytes at the start of every workspace: the device error word and the
 // counters that kernels leave at zero (moe_clear_device_error clears them)
 size_t workspace_header_bytes();
-// byte offset in that header of the router's two counters
+// byte offset in that header of the router's counter
 size_t route_counters_offset();
 // whether launches for this problem use programmatic dependent launch (M-small path)
 bool use_pdl(const moe_problem_t &problem);

@@ -3,11 +3,17 @@
 //
 //   logits[t, e] = sum_m x[t, m] w[e, m]        (x = h * r(h) * w_pre in moe_layer)
 //
-// Few tokens (T_max <= 128): one cooperative kernel. The router's weights are
-// the bytes that matter (5.5 MB at E=384, H=7168) and must come from every
-// SM at once, so a unit is 16 experts x a slice of H, about one unit per SM;
-// the slices' partial logits meet in the workspace behind one grid-wide
-// count, and then one CTA per token sums them in slice order and selects.
+// Few tokens (moe_route up to 16, moe_layer): the router's weights are the bytes that matter
+// (5.5 MB at E=384, H=7168) and must come from every SM at once, so a unit is
+// 16 experts x a slice of H, about one unit per SM, and the slices' partial
+// logits meet in the workspace. For one or two tokens the last CTA to get
+// there (a count, nobody waits) sums them in slice order and selects, in the
+// same kernel; for more a second kernel does, one CTA per token, launched
+// early behind the first. (One cooperative kernel whose CTAs waited for all
+// others at a grid-wide count took 8.1 us for one token and 2.3 us more when
+// not in a graph: 2 us of it at the count, the rest the cooperative launch.)
+// For moe_layer these kernels also write the rounded rows and, for up to 128
+// routed slots, dispatch them, so that the expert kernel comes next.
 // Products run on mma.sync m16n8k16 with the experts on M and 8 tokens on N:
 // at these sizes the tensor work is nothing, and fragments taken straight
 // from global memory need no staging. A dot product may take its terms in any
@@ -265,26 +271,100 @@ __device__ void select_block(const RouteArgs &a, int t, SelectScratch &s)
     __syncthreads();
 }
 
+// Sum of one token's partial logits in slice order into s.logits (times r),
+// and its scale r(h) when the rows are to be normalised.
+template <bool kNormed>
+__device__ __forceinline__ float gather_logits(const RouteArgs &a, const RouteSplit &sp, int t, SelectScratch &s)
+{
+    const int E = a.E;
+    float r = 1.f;
+    if (kNormed) {
+        const float *sq = a.part + static_cast<size_t>(sp.slices) * a.T_max * E + t;
+        float v = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < sp.slices; ++i)
+            v += __ldcg(sq + static_cast<size_t>(i) * a.T_max);
+        r = 1.f / sqrtf(v / a.H + a.eps);
+    }
+    float v[kMaxExperts / kFewThreads] = {};
+#pragma unroll 4
+    for (int i = 0; i < sp.slices; ++i)
+#pragma unroll
+        for (int j = 0; j < kMaxExperts / kFewThreads; ++j)
+            if (threadIdx.x + j * kFewThreads < E)
+                v[j] += __ldcg(a.part + (static_cast<size_t>(i) * a.T_max + t) * E + threadIdx.x + j * kFewThreads);
+#pragma unroll
+    for (int j = 0; j < kMaxExperts / kFewThreads; ++j) {
+        const int e = threadIdx.x + j * kFewThreads;
+        if (e < E) {
+            s.logits[e] = v[j] * r;
+            if (a.logits)
+                a.logits[static_cast<size_t>(t) * E + e] = v[j] * r;
+        }
+    }
+    __syncthreads();
+    return r;
+}
+
+// The normalised row for the experts, rounded to bf16 (their MMAs' operand type).
+__device__ __forceinline__ void write_row(const RouteArgs &a, int t, float r)
+{
+#pragma unroll 2
+    for (int m = 8 * threadIdx.x; m < a.H; m += 8 * kFewThreads) {
+        float f[8], wp[8];
+        load8(a.x, a.x_f32, t * a.x_stride + m, f);
+        load_weight8(a, m, wp);
+        uint4 o;
+        o.x = pack_bf16(f[0] * r * wp[0], f[1] * r * wp[1]);
+        o.y = pack_bf16(f[2] * r * wp[2], f[3] * r * wp[3]);
+        o.z = pack_bf16(f[4] * r * wp[4], f[5] * r * wp[5]);
+        o.w = pack_bf16(f[6] * r * wp[6], f[7] * r * wp[7]);
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) + static_cast<size_t>(t) * a.H + m) = o;
+    }
+}
+
+// The tables of moe_dispatch for R <= kRouteDispatchSlots slots, by one block:
+// a slot's row is the count of the slots before it in (expert, slot) order.
+__device__ void dispatch_slots(const RouteArgs &a, const int *s_ids, int R)
+{
+    for (int s = threadIdx.x; s < R; s += kFewThreads) {
+        const int e = s_ids[s];
+        int row = 0;
+        for (int j = 0; j < R; ++j) {
+            const int o = s_ids[j];
+            row += o >= 0 && (o < e || (o == e && j < s)) ? 1 : 0;
+        }
+        a.inv[s] = e >= 0 ? row : -1;
+        if (e >= 0)
+            a.perm[row] = s;
+    }
+    for (int e = threadIdx.x; e <= a.E; e += kFewThreads) {
+        int before = 0;
+        for (int j = 0; j < R; ++j)
+            before += s_ids[j] >= 0 && s_ids[j] < e ? 1 : 0;
+        a.expert_offsets[e] = before;
+    }
+}
+
 // kTiles: 8-token tiles of a unit. kParts: bf16 parts of the token operand;
 // 1: x as it is (moe_route), 2 or 3: u = h * w_pre (moe_layer).
 template <int kTiles, int kParts>
 __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_constant__ RouteArgs a,
-                                                                   const RouteSplit sp, uint64_t wait_limit_ns)
+                                                                   const RouteSplit sp)
 {
     constexpr int kTok = 8 * kTiles;
+    constexpr bool kJoin = kTiles == 1;    // the last CTA may select here (sp.join)
     __shared__ float s_acc[kFewWarps][16][kTok + 1];
     __shared__ float s_sq[kFewWarps][kTok];
-    __shared__ SelectScratch s_sel;
-    __shared__ int s_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
     const int E = a.E, H = a.H;
     const int units = sp.groups * sp.slices * sp.chunks;
     const int blocks64 = H / 64;
     const __nv_bfloat16 *w = static_cast<const __nv_bfloat16 *>(a.w);
-    // this CTA's first weights on their way into L2 before the wait for the
+    // this CTA's weights on their way into L2 before the wait for the
     // previous kernel (a prefetch reads nothing that kernel could still write)
-    if (static_cast<int>(blockIdx.x) < units) {
+    {
         const int u = blockIdx.x;
         const int e0 = (u % sp.groups) * 16, s = (u / sp.groups) % sp.slices;
         const int m0 = 64 * (s * blocks64 / sp.slices), m1 = 64 * ((s + 1) * blocks64 / sp.slices);
@@ -298,11 +378,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
     pdl_trigger();
     const int T = token_count(a.d_num_tokens, a.T_max);
 
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int t0 = static_cast<int>(blockIdx.x) / sp.groups / sp.slices * kTok;
+    if (t0 < T) {
+        const int u = blockIdx.x;
         const int e0 = (u % sp.groups) * 16, s = (u / sp.groups) % sp.slices;
-        const int t0 = (u / sp.groups / sp.slices) * kTok;
-        if (t0 >= T)
-            break;
         const int b0 = 2 * (s * blocks64 / sp.slices), b1 = 2 * ((s + 1) * blocks64 / sp.slices);   // 32-wide blocks
         float acc[kTiles][4] = {};
         float sq[kTiles] = {};
@@ -405,107 +484,119 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
         __syncthreads();
     }
 
-    // all units' partial sums are in the workspace once every CTA has counted
-    // itself; only the CTAs with a job after that wait (bounded): one per token
-    // that selects and, in moe_layer, one that writes its rounded row
-    const int jobs = kParts > 1 ? 2 * T : T;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        s_flag = 0;
-        atom_add_acq_rel_gpu(a.counters, 1);
-        if (static_cast<int>(blockIdx.x) < jobs) {
-            const uint64_t since = global_timer_ns();
-            while (ld_acquire_gpu(a.counters) < static_cast<int>(gridDim.x))
-                if (global_timer_ns() - since > wait_limit_ns) {
-                    s_flag = 1;
-                    atomicOr(a.err, MOE_DEVERR_WAIT_TIMEOUT);
-                    break;
-                }
-        }
-        // the last CTA past its wait returns the counters to zero
-        if (atom_add_acq_rel_gpu(a.counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
-            a.counters[0] = 0;
-            a.counters[1] = 0;
-        }
-    }
-    __syncthreads();
-    if (s_flag)
-        return;
-    for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const int t = job < T ? job : job - T;
-        float r = 1.f;
-        if (kParts > 1) {
-            const float *sq = a.part + static_cast<size_t>(sp.slices) * a.T_max * E + t;
-            float v = 0.f;
-#pragma unroll 8
-            for (int s = 0; s < sp.slices; ++s)
-                v += __ldcg(sq + static_cast<size_t>(s) * a.T_max);
-            r = 1.f / sqrtf(v / H + a.eps);
-        }
-        if (job < T) {
-            float v[kMaxExperts / kFewThreads] = {};
-#pragma unroll 4
-            for (int s = 0; s < sp.slices; ++s)
-#pragma unroll
-                for (int i = 0; i < kMaxExperts / kFewThreads; ++i)
-                    if (threadIdx.x + i * kFewThreads < E)
-                        v[i] += __ldcg(a.part + (static_cast<size_t>(s) * a.T_max + t) * E + threadIdx.x +
-                                       i * kFewThreads);
-#pragma unroll
-            for (int i = 0; i < kMaxExperts / kFewThreads; ++i) {
-                const int e = threadIdx.x + i * kFewThreads;
-                if (e < E) {
-                    s_sel.logits[e] = v[i] * r;
-                    if (a.logits)
-                        a.logits[static_cast<size_t>(t) * E + e] = v[i] * r;
-                }
-            }
-            __syncthreads();
+    if constexpr (kJoin) {
+        if (!sp.join)
+            return;
+        __shared__ SelectScratch s_sel;
+        __shared__ int s_ids[kRouteDispatchSlots];
+        __shared__ int s_last;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0)
+            s_last = atom_add_acq_rel_gpu(a.counters, 1) == units - 1;
+        __syncthreads();
+        if (!s_last)
+            return;
+        if (threadIdx.x == 0)
+            *a.counters = 0;
+        for (int t = 0; t < T; ++t) {
+            const float r = gather_logits<(kParts > 1)>(a, sp, t, s_sel);
+            if (kParts > 1)
+                write_row(a, t, r);
             select_block(a, t, s_sel);
-        } else if (kParts > 1) {
-            // the normalised row for the experts, rounded to bf16 (their MMAs' operand type)
-#pragma unroll 2
-            for (int m = 8 * threadIdx.x; m < H; m += 8 * kFewThreads) {
-                float f[8], wp[8];
-                load8(a.x, a.x_f32, t * a.x_stride + m, f);
-                load_weight8(a, m, wp);
-                uint4 o;
-                o.x = pack_bf16(f[0] * r * wp[0], f[1] * r * wp[1]);
-                o.y = pack_bf16(f[2] * r * wp[2], f[3] * r * wp[3]);
-                o.z = pack_bf16(f[4] * r * wp[4], f[5] * r * wp[5]);
-                o.w = pack_bf16(f[6] * r * wp[6], f[7] * r * wp[7]);
-                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) + static_cast<size_t>(t) * H + m) = o;
-            }
+            if (a.perm)
+                for (int j = threadIdx.x; j < a.k; j += kFewThreads)
+                    s_ids[t * a.k + j] = s_sel.id[j];
+            __syncthreads();
         }
+        if (a.perm)
+            dispatch_slots(a, s_ids, T * a.k);
     }
 }
 
+// What follows the partial logits of more than two tokens: CTA t selects for
+// token t, CTA T_max + t writes its rounded row (moe_layer), and the last CTA
+// that selected dispatches (moe_layer, up to kRouteDispatchSlots slots).
+template <bool kNormed>
+__global__ void __launch_bounds__(kFewThreads) route_finish_kernel(const __grid_constant__ RouteArgs a,
+                                                                   const RouteSplit sp)
+{
+    __shared__ SelectScratch s_sel;
+    __shared__ int s_ids[kRouteDispatchSlots];
+    __shared__ int s_last;
+    pdl_wait();
+    pdl_trigger();
+    const int T = token_count(a.d_num_tokens, a.T_max);
+    const int job = blockIdx.x;
+    if (job >= a.T_max) {
+        const int t = job - a.T_max;
+        if (kNormed && t < T) {
+            const float *sq = a.part + static_cast<size_t>(sp.slices) * a.T_max * a.E + t;
+            float v = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < sp.slices; ++i)
+                v += __ldcg(sq + static_cast<size_t>(i) * a.T_max);
+            write_row(a, t, 1.f / sqrtf(v / a.H + a.eps));
+        }
+        return;
+    }
+    if (job < T) {
+        gather_logits<kNormed>(a, sp, job, s_sel);
+        select_block(a, job, s_sel);
+    }
+    if (!a.perm)
+        return;
+    if (T == 0) {
+        if (job == 0)
+            dispatch_slots(a, s_ids, 0);
+        return;
+    }
+    if (job >= T)
+        return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = atom_add_acq_rel_gpu(a.counters, 1) == T - 1;
+    __syncthreads();
+    if (!s_last)
+        return;
+    if (threadIdx.x == 0)
+        *a.counters = 0;
+    for (int i = threadIdx.x; i < T * a.k; i += kFewThreads)
+        s_ids[i] = __ldcg(a.ids + i);
+    __syncthreads();
+    dispatch_slots(a, s_ids, T * a.k);
+}
+
 template <int kTiles>
-cudaError_t launch_few(const RouteArgs &a, const RouteSplit &sp, int num_sms, cudaStream_t stream, bool pdl)
+cudaError_t launch_few(const RouteArgs &a, const RouteSplit &sp, cudaStream_t stream, bool pdl)
 {
     const bool exact16 = !a.x_f32 && !a.unit_offset && (!a.w_pre || !a.w_f32);
-    auto kern = !a.normed ? route_few_kernel<kTiles, 1>
-                          : (exact16 ? route_few_kernel<kTiles, 2> : route_few_kernel<kTiles, 3>);
-    return launch_k_coresident(kern, static_cast<long long>(sp.groups) * sp.slices * sp.chunks, dim3(kFewThreads), 0,
-                               stream, pdl, num_sms, a, sp, kWaitLimitNs);
+    auto kern = exact16 ? route_few_kernel<kTiles, 2> : route_few_kernel<kTiles, 3>;
+    if constexpr (kTiles == 1)    // moe_route: at most 16 tokens
+        if (!a.normed)
+            kern = route_few_kernel<kTiles, 1>;
+    const cudaError_t e =
+        launch_k(kern, dim3(sp.groups * sp.slices * sp.chunks), dim3(kFewThreads), 0, stream, pdl, a, sp);
+    if (e != cudaSuccess || sp.join)
+        return e;
+    return a.normed ? launch_k(route_finish_kernel<true>, dim3(2 * a.T_max), dim3(kFewThreads), 0, stream, pdl, a, sp)
+                    : launch_k(route_finish_kernel<false>, dim3(a.T_max), dim3(kFewThreads), 0, stream, pdl, a, sp);
 }
 
 }  // namespace
 
-cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t stream, bool pdl)
+cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl)
 {
-    if (a.T_max <= kRouteFewTokens) {
+    if (a.normed || a.T_max <= kRouteFewTokens) {
         const RouteSplit sp = route_split(a.T_max, a.E, a.H);
         switch (sp.tiles) {
         case 1:
-            return launch_few<1>(a, sp, num_sms, stream, pdl);
+            return launch_few<1>(a, sp, stream, pdl);
         case 2:
-            return launch_few<2>(a, sp, num_sms, stream, pdl);
-        case 4:
-            return launch_few<4>(a, sp, num_sms, stream, pdl);
+            return launch_few<2>(a, sp, stream, pdl);
         default:
-            return launch_few<8>(a, sp, num_sms, stream, pdl);
+            return launch_few<4>(a, sp, stream, pdl);
         }
     }
     float *logits = a.logits ? a.logits : a.part;

@@ -135,18 +135,27 @@ __device__ __forceinline__ unsigned keep_groups(const RouteArgs &a, float value)
     return __ballot_sync(kFull, lane < a.n_group && rank < a.topk_group);
 }
 
-// The groups that stay, from one token's keys in shared memory (-inf: none). One warp.
+// The groups that stay, from one token's keys in shared memory (-inf: none).
+// One warp: 32 / n_group lanes take a group.
 __device__ __noinline__ unsigned kept_groups(const RouteArgs &a, const float *s_key)
 {
-    const int lane = threadIdx.x & 31, gs = a.E / a.n_group;
+    const int lane = threadIdx.x & 31, gs = a.E / a.n_group, per = 32 / a.n_group;
+    const int g = lane / per, part = lane % per;
     float first = -INFINITY, second = -INFINITY;
-    if (lane < a.n_group)
-        for (int i = 0; i < gs; ++i) {
-            const float v = s_key[lane * gs + i];
-            second = v > first ? first : fmaxf(second, v);
+    if (g < a.n_group)
+        for (int i = part; i < gs; i += per) {
+            const float v = s_key[g * gs + i];
+            second = fmaxf(second, fminf(first, v));
             first = fmaxf(first, v);
         }
-    return keep_groups(a, a.group_top > 1 ? first + second : first);
+    float top1 = first, top2 = second;       // of the group's first lane
+    for (int j = 1; j < per; ++j) {
+        const float f = __shfl_down_sync(kFull, first, j), s = __shfl_down_sync(kFull, second, j);
+        top2 = fmaxf(fmaxf(top2, s), fminf(top1, f));
+        top1 = fmaxf(top1, f);
+    }
+    const float value = a.group_top > 1 ? top1 + top2 : top1;
+    return keep_groups(a, __shfl_sync(kFull, value, lane * per));
 }
 
 // k rounds of a warp-wide maximum, each below the last: for k > 32, and for
