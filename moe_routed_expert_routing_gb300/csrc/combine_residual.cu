@@ -93,12 +93,47 @@ __device__ __forceinline__ void weight4(const NormArgs &a, const void *w, int m,
 // Y: fp32, or fp16 (the tiled paths' intermediate). kParts: K parts of fp32 y,
 // part_stride elements apart, summed in part order as in combine.cu.
 template <typename Y, int kParts>
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThreads)
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThreads, kParts == 1 ? 2 : 1)
     combine_residual_kernel(const Y *y_sorted, const int32_t *inv, const float *w, const __grid_constant__ NormArgs a,
                             int k, size_t part_stride)
 {
     __shared__ float s_warp[2][kTailThreads / 32];
     __shared__ float s_slot[2];
+    const int t = blockIdx.x / kClusterCtas;
+    const int cols = a.H / kClusterCtas;             // a multiple of 8
+    const int m0 = static_cast<int>(cluster_ctarank()) * cols;
+    // Ahead of the wait for y: the routing, h, the weights and the gate are
+    // inputs of the call or were written two launches back or more, which is
+    // complete (see launch_k), and of a token past the count nothing is used.
+    constexpr int kRows = kParts == 1 ? 4 : 8;       // routed rows in flight
+    int row[kRows];
+    float wj[kRows];
+    auto routing = [&](int j0) {
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            row[q] = j0 + q < k ? inv[t * k + j0 + q] : -1;
+            wj[q] = j0 + q < k ? w[t * k + j0 + q] : 0.f;
+        }
+    };
+    routing(0);
+    float h[kTailVecs][4], wp[kTailVecs][4], wn[kTailVecs][4], g[kTailVecs][4];
+#pragma unroll
+    for (int v = 0; v < kTailVecs; ++v) {
+        const int c = 4 * (threadIdx.x + v * kTailThreads);
+        if (c >= cols)
+            continue;
+        const int m = m0 + c;
+        load4(a.h, a.h_f32, t * a.h_stride + m, h[v]);
+        weight4(a, a.norm_block ? a.w_post : nullptr, m, wp[v]);
+        weight4(a, a.x ? a.w_next : nullptr, m, wn[v]);
+        g[v][0] = g[v][1] = g[v][2] = g[v][3] = 1.f;
+        if (a.gate_kind == MOE_GATE_CHANNEL)
+            load4(a.gate, a.w_f32, m, g[v]);
+        else if (a.gate_kind == MOE_GATE_TOKEN)
+            g[v][0] = g[v][1] = g[v][2] = g[v][3] = static_cast<const float *>(a.gate)[t];
+        else if (a.gate_kind == MOE_GATE_ELEMENT)
+            load4(a.gate, false, t * a.gate_stride + m, g[v]);
+    }
     pdl_wait();
     pdl_trigger();
     int T = a.T_max;
@@ -106,30 +141,24 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
         T = *a.d_num_tokens;
         T = T < 0 ? 0 : (T > a.T_max ? a.T_max : T);
     }
-    const int t = blockIdx.x / kClusterCtas;
     if (t >= T)      // the whole cluster
         return;
-    const int cols = a.H / kClusterCtas;             // a multiple of 8
-    const int m0 = static_cast<int>(cluster_ctarank()) * cols;
     float y[kTailVecs][4];
     float sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < kTailVecs; ++v) {
-        const int c = 4 * (threadIdx.x + v * kTailThreads);
+    for (int v = 0; v < kTailVecs; ++v)
         y[v][0] = y[v][1] = y[v][2] = y[v][3] = 0.f;
-        if (c >= cols)
-            continue;
-        for (int j0 = 0; j0 < k; j0 += 4) {
-            float f[4][kParts][4];
-            int row[4];
-            float wj[4];
+    for (int j0 = 0; j0 < k; j0 += kRows) {
+        if (j0 > 0)
+            routing(j0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                row[q] = j0 + q < k ? inv[t * k + j0 + q] : -1;
-                wj[q] = j0 + q < k ? w[t * k + j0 + q] : 0.f;
-            }
+        for (int v = 0; v < kTailVecs; ++v) {
+            const int c = 4 * (threadIdx.x + v * kTailThreads);
+            if (c >= cols)
+                continue;
+            float f[kRows][kParts][4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < kRows; ++q)
 #pragma unroll
                 for (int p = 0; p < kParts; ++p)
                     if (row[q] >= 0) {
@@ -145,7 +174,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
                         }
                     }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < kRows; ++q) {
                 if (row[q] < 0)
                     continue;
 #pragma unroll
@@ -158,10 +187,12 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
                 }
             }
         }
+    }
+#pragma unroll
+    for (int v = 0; v < kTailVecs; ++v)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             sum = fmaf(y[v][i], y[v][i], sum);
-    }
     const float r_y = a.norm_block ? 1.f / sqrtf(cluster_sum(sum, s_warp[0], &s_slot[0]) / a.H + a.eps) : 1.f;
     sum = 0.f;
 #pragma unroll
@@ -169,25 +200,12 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
         const int c = 4 * (threadIdx.x + v * kTailThreads);
         if (c >= cols)
             continue;
-        const int m = m0 + c;
-        float h[4], wp[4], g[4] = {1.f, 1.f, 1.f, 1.f};
-        load4(a.h, a.h_f32, t * a.h_stride + m, h);
-        if (a.norm_block)
-            weight4(a, a.w_post, m, wp);
-        else
-            wp[0] = wp[1] = wp[2] = wp[3] = 1.f;
-        if (a.gate_kind == MOE_GATE_CHANNEL)
-            load4(a.gate, a.w_f32, m, g);
-        else if (a.gate_kind == MOE_GATE_TOKEN)
-            g[0] = g[1] = g[2] = g[3] = static_cast<const float *>(a.gate)[t];
-        else if (a.gate_kind == MOE_GATE_ELEMENT)
-            load4(a.gate, false, t * a.gate_stride + m, g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            y[v][i] = h[i] + a.scale * g[i] * (y[v][i] * r_y * wp[i]);
+            y[v][i] = h[v][i] + a.scale * g[v][i] * (y[v][i] * r_y * wp[v][i]);
             sum = fmaf(y[v][i], y[v][i], sum);
         }
-        const size_t o = t * a.out_stride + m;
+        const size_t o = t * a.out_stride + m0 + c;
         if (a.h_f32)
             *reinterpret_cast<float4 *>(static_cast<float *>(a.h_out) + o) =
                 make_float4(y[v][0], y[v][1], y[v][2], y[v][3]);
@@ -201,12 +219,10 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
             const int c = 4 * (threadIdx.x + v * kTailThreads);
             if (c >= cols)
                 continue;
-            float wn[4];
-            weight4(a, a.w_next, m0 + c, wn);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                wn[i] = y[v][i] * r * wn[i];
-            store4_bf16(a.x, t * a.x_stride + m0 + c, wn);
+                wn[v][i] = y[v][i] * r * wn[v][i];
+            store4_bf16(a.x, t * a.x_stride + m0 + c, wn[v]);
         }
     }
     cluster_sync();   // no CTA leaves while another may still read its sums

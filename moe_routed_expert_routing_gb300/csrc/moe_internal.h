@@ -280,6 +280,7 @@ struct RouteSplit {
 // rows, takes them always.
 constexpr int kRouteFewTokens = 16;
 constexpr int kRouteJoinTokens = 2;
+constexpr int kRouteBlockTokens = 152;      // one block per SM
 constexpr int kRouteDispatchSlots = 128;
 
 inline RouteSplit route_split(int T_max, int E, int H)

@@ -94,27 +94,32 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t u)
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// Eight consecutive values of a bf16 or fp32 row.
-__device__ __forceinline__ void load8(const void *p, bool f32, size_t i, float (&f)[8])
+// Eight consecutive values of a bf16 or fp32 row, as loaded.
+struct Raw8 {
+    uint4 a, b;       // b: fp32 only
+};
+
+__device__ __forceinline__ Raw8 load_raw8(const void *p, bool f32, size_t i)
 {
-    if (f32) {
-        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        const float4 x = __ldg(q), y = __ldg(q + 1);
-        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-    } else {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i));
-        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 g = unpack_bf16(v[j]);
-            f[2 * j] = g.x;
-            f[2 * j + 1] = g.y;
-        }
-    }
+    Raw8 r;
+    const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + i * (f32 ? 4 : 2));
+    r.a = __ldg(q);
+    r.b = f32 ? __ldg(q + 1) : make_uint4(0u, 0u, 0u, 0u);
+    return r;
 }
 
-__device__ __forceinline__ void load_weight8(const RouteArgs &a, int m, float (&w)[8])
+__device__ __forceinline__ void widen8(const Raw8 &r, bool f32, float (&f)[8])
+{
+    const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 g = unpack_bf16(u[j]);
+        f[2 * j] = f32 ? __uint_as_float(u[2 * j]) : g.x;
+        f[2 * j + 1] = f32 ? __uint_as_float(u[2 * j + 1]) : g.y;
+    }
+}
+// w' of the norm: 1, w or 1 + w
+__device__ __forceinline__ void weight8(const RouteArgs &a, const Raw8 &r, float (&w)[8])
 {
     if (!a.w_pre) {
 #pragma unroll
@@ -122,11 +127,16 @@ __device__ __forceinline__ void load_weight8(const RouteArgs &a, int m, float (&
             w[i] = 1.f;
         return;
     }
-    load8(a.w_pre, a.w_f32, m, w);
+    widen8(r, a.w_f32, w);
     if (a.unit_offset)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             w[i] = 1.f + w[i];
+}
+
+__device__ __forceinline__ Raw8 load_weight_raw8(const RouteArgs &a, int m)
+{
+    return a.w_pre ? load_raw8(a.w_pre, a.w_f32, m) : Raw8{};
 }
 
 // Shared memory of one selection by a whole block.
@@ -137,6 +147,7 @@ struct SelectScratch {
     float warp[kFewWarps];
     float group[32];
     unsigned kept;
+    float mx, sum;                          // softmax, where it is needed
     int id[kMaxTopK];
 };
 
@@ -145,7 +156,9 @@ struct SelectScratch {
 // the ones that beat it. Called with a cold instruction cache between a
 // model's other kernels, so its loops stay rolled: the version that one warp
 // ran on unrolled registers took 13 us there.
-__device__ void select_block(const RouteArgs &a, int t, SelectScratch &s)
+//
+// Leaves the ids in s.id; store_block then writes ids and weights (one warp).
+__device__ void select_block(const RouteArgs &a, SelectScratch &s)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = a.E, k = a.k;
@@ -255,51 +268,79 @@ __device__ void select_block(const RouteArgs &a, int t, SelectScratch &s)
         if (mine != 0u && rank < k)
             s.id[rank] = static_cast<int>(~static_cast<uint32_t>(mine));
     }
-    __syncthreads();
-    if (warp == 0) {
-        int id[2];
-        const int place[2] = {lane, lane + 32};
-        float l[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            id[q] = s.id[lane + 32 * q];
-            l[q] = id[q] >= 0 ? s.logits[id[q]] : -INFINITY;
-        }
-        const int n = __popc(__ballot_sync(kFull, id[0] >= 0)) + __popc(__ballot_sync(kFull, id[1] >= 0));
-        store_choice(a, t, id, place, l, n, mx, sum);
+    if (tid == 0) {
+        s.mx = mx;
+        s.sum = sum;
     }
     __syncthreads();
 }
 
-// Sum of one token's partial logits in slice order into s.logits (times r),
-// and its scale r(h) when the rows are to be normalised.
+__device__ void store_block(const RouteArgs &a, int t, const SelectScratch &s)
+{
+    const int lane = threadIdx.x & 31;
+    int id[2];
+    const int place[2] = {lane, lane + 32};
+    float l[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        id[q] = s.id[lane + 32 * q];
+        l[q] = id[q] >= 0 ? s.logits[id[q]] : -INFINITY;
+    }
+    const int n = __popc(__ballot_sync(kFull, id[0] >= 0)) + __popc(__ballot_sync(kFull, id[1] >= 0));
+    store_choice(a, t, id, place, l, n, s.mx, s.sum);
+}
+
+// r(h) of a token, from the slices' sums of squares in slice order. The loads
+// go out eight at a time: one after the other they cost 0.4 us each.
+__device__ __forceinline__ float row_scale(const RouteArgs &a, const RouteSplit &sp, int t)
+{
+    const float *sq = a.part + static_cast<size_t>(sp.slices) * a.T_max * a.E + t;
+    float sum = 0.f;
+    for (int i0 = 0; i0 < sp.slices; i0 += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = i0 + i < sp.slices ? __ldcg(sq + static_cast<size_t>(i0 + i) * a.T_max) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sum += v[i];
+    }
+    return 1.f / sqrtf(sum / a.H + a.eps);
+}
+
+// Sum of one token's partial logits in slice order, times r(h) in moe_layer,
+// into s.logits. Returns r.
 template <bool kNormed>
 __device__ __forceinline__ float gather_logits(const RouteArgs &a, const RouteSplit &sp, int t, SelectScratch &s)
 {
     const int E = a.E;
-    float r = 1.f;
-    if (kNormed) {
-        const float *sq = a.part + static_cast<size_t>(sp.slices) * a.T_max * E + t;
-        float v = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < sp.slices; ++i)
-            v += __ldcg(sq + static_cast<size_t>(i) * a.T_max);
-        r = 1.f / sqrtf(v / a.H + a.eps);
+    constexpr int kEach = kMaxExperts / kFewThreads;
+    float sum[kEach] = {};
+    for (int i0 = 0; i0 < sp.slices; i0 += 8) {
+        float v[kEach][8];
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = threadIdx.x + j * kFewThreads;
+                v[j][i] = e < E && i0 + i < sp.slices
+                              ? __ldcg(a.part + (static_cast<size_t>(i0 + i) * a.T_max + t) * E + e)
+                              : 0.f;
+            }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sum[j] += v[j][i];
     }
-    float v[kMaxExperts / kFewThreads] = {};
-#pragma unroll 4
-    for (int i = 0; i < sp.slices; ++i)
+    const float r = kNormed ? row_scale(a, sp, t) : 1.f;
 #pragma unroll
-        for (int j = 0; j < kMaxExperts / kFewThreads; ++j)
-            if (threadIdx.x + j * kFewThreads < E)
-                v[j] += __ldcg(a.part + (static_cast<size_t>(i) * a.T_max + t) * E + threadIdx.x + j * kFewThreads);
-#pragma unroll
-    for (int j = 0; j < kMaxExperts / kFewThreads; ++j) {
+    for (int j = 0; j < kEach; ++j) {
         const int e = threadIdx.x + j * kFewThreads;
         if (e < E) {
-            s.logits[e] = v[j] * r;
+            s.logits[e] = sum[j] * r;
             if (a.logits)
-                a.logits[static_cast<size_t>(t) * E + e] = v[j] * r;
+                a.logits[static_cast<size_t>(t) * E + e] = sum[j] * r;
         }
     }
     __syncthreads();
@@ -309,27 +350,46 @@ __device__ __forceinline__ float gather_logits(const RouteArgs &a, const RouteSp
 // The normalised row for the experts, rounded to bf16 (their MMAs' operand type).
 __device__ __forceinline__ void write_row(const RouteArgs &a, int t, float r)
 {
-#pragma unroll 2
-    for (int m = 8 * threadIdx.x; m < a.H; m += 8 * kFewThreads) {
-        float f[8], wp[8];
-        load8(a.x, a.x_f32, t * a.x_stride + m, f);
-        load_weight8(a, m, wp);
-        uint4 o;
-        o.x = pack_bf16(f[0] * r * wp[0], f[1] * r * wp[1]);
-        o.y = pack_bf16(f[2] * r * wp[2], f[3] * r * wp[3]);
-        o.z = pack_bf16(f[4] * r * wp[4], f[5] * r * wp[5]);
-        o.w = pack_bf16(f[6] * r * wp[6], f[7] * r * wp[7]);
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) + static_cast<size_t>(t) * a.H + m) = o;
+    for (int m0 = 8 * threadIdx.x; m0 < a.H; m0 += 4 * 8 * kFewThreads) {
+        Raw8 x[4], w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = m0 + i * 8 * kFewThreads;
+            if (m < a.H) {
+                x[i] = load_raw8(a.x, a.x_f32, t * a.x_stride + m);
+                w[i] = load_weight_raw8(a, m);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = m0 + i * 8 * kFewThreads;
+            if (m >= a.H)
+                break;
+            float f[8], wp[8];
+            widen8(x[i], a.x_f32, f);
+            weight8(a, w[i], wp);
+            uint4 o;
+            o.x = pack_bf16(f[0] * r * wp[0], f[1] * r * wp[1]);
+            o.y = pack_bf16(f[2] * r * wp[2], f[3] * r * wp[3]);
+            o.z = pack_bf16(f[4] * r * wp[4], f[5] * r * wp[5]);
+            o.w = pack_bf16(f[6] * r * wp[6], f[7] * r * wp[7]);
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) + static_cast<size_t>(t) * a.H + m) = o;
+        }
     }
 }
 
 // The tables of moe_dispatch for R <= kRouteDispatchSlots slots, by one block:
 // a slot's row is the count of the slots before it in (expert, slot) order.
-__device__ void dispatch_slots(const RouteArgs &a, const int *s_ids, int R)
+// Threads first..kFewThreads - 1 of the block take part.
+__device__ void dispatch_slots(const RouteArgs &a, const int *s_ids, int R, int first)
 {
-    for (int s = threadIdx.x; s < R; s += kFewThreads) {
+    const int tid = static_cast<int>(threadIdx.x) - first;
+    if (tid < 0)
+        return;
+    for (int s = tid; s < R; s += kFewThreads - first) {
         const int e = s_ids[s];
         int row = 0;
+#pragma unroll 4
         for (int j = 0; j < R; ++j) {
             const int o = s_ids[j];
             row += o >= 0 && (o < e || (o == e && j < s)) ? 1 : 0;
@@ -338,8 +398,9 @@ __device__ void dispatch_slots(const RouteArgs &a, const int *s_ids, int R)
         if (e >= 0)
             a.perm[row] = s;
     }
-    for (int e = threadIdx.x; e <= a.E; e += kFewThreads) {
+    for (int e = tid; e <= a.E; e += kFewThreads - first) {
         int before = 0;
+#pragma unroll 4
         for (int j = 0; j < R; ++j)
             before += s_ids[j] >= 0 && s_ids[j] < e ? 1 : 0;
         a.expert_offsets[e] = before;
@@ -390,38 +451,41 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
         const uint4 *w_hi = reinterpret_cast<const uint4 *>(w + static_cast<size_t>(e0 + g + 8) * H + 8 * q);
         const bool squares = kParts > 1 && e0 == 0;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        constexpr int kAhead = 4;            // weight blocks in flight per warp
+        // K blocks of a warp in flight, weights and tokens: five cover a slice of
+        // the decode workloads (E=384, H=7168) in one round trip
+        constexpr int kAhead = kTiles == 1 ? 5 : (kTiles == 2 ? 3 : 2);
         for (int bb = b0 + warp; bb < b1; bb += kAhead * kFewWarps) {
             uint4 wl[kAhead], wh[kAhead];
+            Raw8 x[kAhead][kTiles], wr[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int b = bb + i * kFewWarps;
+                const int m = 32 * b + 8 * q;
                 wl[i] = (b < b1 && lo_row) ? __ldg(w_lo + 4 * b) : zero;
                 wh[i] = (b < b1 && hi_row) ? __ldg(w_hi + 4 * b) : zero;
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int b = bb + i * kFewWarps;
-                if (b >= b1)
-                    break;
-                const int m = 32 * b + 8 * q;
-                float wp[8];
-                if (kParts > 1)
-                    load_weight8(a, m, wp);
+                wr[i] = kParts > 1 && b < b1 ? load_weight_raw8(a, m) : Raw8{};
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j) {
                     const int t = t0 + 8 * j + g;
-                    const bool real = t < T;
+                    x[i][j] = b < b1 && t < T ? load_raw8(a.x, kParts > 1 && a.x_f32, t * a.x_stride + m) : Raw8{};
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (bb + i * kFewWarps >= b1)
+                    break;
+                float wp[8];
+                if (kParts > 1)
+                    weight8(a, wr[i], wp);
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
                     if (kParts == 1) {
-                        const uint4 xv = real ? __ldg(reinterpret_cast<const uint4 *>(
-                                                    static_cast<const __nv_bfloat16 *>(a.x) + t * a.x_stride + m))
-                                              : zero;
+                        const uint4 xv = x[i][j].a;
                         mma_bf16(acc[j], wl[i].x, wh[i].x, wl[i].y, wh[i].y, xv.x, xv.y);
                         mma_bf16(acc[j], wl[i].z, wh[i].z, wl[i].w, wh[i].w, xv.z, xv.w);
                     } else {
-                        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                        if (real)
-                            load8(a.x, a.x_f32, t * a.x_stride + m, f);
+                        float f[8];
+                        widen8(x[i][j], a.x_f32, f);
                         if (squares)
 #pragma unroll
                             for (int v = 0; v < 8; ++v)
@@ -490,6 +554,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
         __shared__ SelectScratch s_sel;
         __shared__ int s_ids[kRouteDispatchSlots];
         __shared__ int s_last;
+        if (kParts > 1)       // the rows and w_pre into L1: the last CTA, whichever it is, writes the rows
+            for (int m = 32 * threadIdx.x; m < H; m += 32 * kFewThreads) {
+                for (int t = 0; t < T; ++t)
+                    prefetch_l1(static_cast<const char *>(a.x) + (t * a.x_stride + m) * (a.x_f32 ? 4 : 2));
+                if (a.w_pre)
+                    prefetch_l1(static_cast<const char *>(a.w_pre) + m * (a.w_f32 ? 4 : 2));
+            }
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0)
@@ -503,14 +574,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
             const float r = gather_logits<(kParts > 1)>(a, sp, t, s_sel);
             if (kParts > 1)
                 write_row(a, t, r);
-            select_block(a, t, s_sel);
-            if (a.perm)
+            select_block(a, s_sel);
+            if (a.perm) {
                 for (int j = threadIdx.x; j < a.k; j += kFewThreads)
                     s_ids[t * a.k + j] = s_sel.id[j];
-            __syncthreads();
+                __syncthreads();
+            }
+            if (warp == 0)
+                store_block(a, t, s_sel);
+            else if (a.perm && t == T - 1)
+                dispatch_slots(a, s_ids, T * a.k, 32);
+            if (t < T - 1)
+                __syncthreads();
         }
-        if (a.perm)
-            dispatch_slots(a, s_ids, T * a.k);
+        if (a.perm && T == 0)
+            dispatch_slots(a, s_ids, 0, 0);
     }
 }
 
@@ -530,25 +608,21 @@ __global__ void __launch_bounds__(kFewThreads) route_finish_kernel(const __grid_
     const int job = blockIdx.x;
     if (job >= a.T_max) {
         const int t = job - a.T_max;
-        if (kNormed && t < T) {
-            const float *sq = a.part + static_cast<size_t>(sp.slices) * a.T_max * a.E + t;
-            float v = 0.f;
-#pragma unroll 8
-            for (int i = 0; i < sp.slices; ++i)
-                v += __ldcg(sq + static_cast<size_t>(i) * a.T_max);
-            write_row(a, t, 1.f / sqrtf(v / a.H + a.eps));
-        }
+        if (kNormed && t < T)
+            write_row(a, t, row_scale(a, sp, t));
         return;
     }
     if (job < T) {
         gather_logits<kNormed>(a, sp, job, s_sel);
-        select_block(a, job, s_sel);
+        select_block(a, s_sel);
+        if (threadIdx.x < 32)
+            store_block(a, job, s_sel);
     }
     if (!a.perm)
         return;
     if (T == 0) {
         if (job == 0)
-            dispatch_slots(a, s_ids, 0);
+            dispatch_slots(a, s_ids, 0, 0);
         return;
     }
     if (job >= T)
@@ -565,7 +639,7 @@ __global__ void __launch_bounds__(kFewThreads) route_finish_kernel(const __grid_
     for (int i = threadIdx.x; i < T * a.k; i += kFewThreads)
         s_ids[i] = __ldcg(a.ids + i);
     __syncthreads();
-    dispatch_slots(a, s_ids, T * a.k);
+    dispatch_slots(a, s_ids, T * a.k, 0);
 }
 
 template <int kTiles>
@@ -603,6 +677,17 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl)
     const cudaError_t e = launch_route_gemm(a, logits, stream, pdl);
     if (e != cudaSuccess)
         return e;
+    // few tokens chosen by scores or groups: a block each (a warp would pass
+    // over the scores alone: 61 tokens of E=256 in 8 groups 14.7 against 16.0
+    // us; chosen by logits a warp is faster, 12.3 against 13.6)
+    if (a.T_max <= kRouteBlockTokens && (a.bias || a.n_group > 1)) {
+        RouteArgs b = a;
+        b.part = logits;
+        b.logits = nullptr;
+        RouteSplit one = {};
+        one.slices = 1;
+        return launch_k(route_finish_kernel<false>, dim3(a.T_max), dim3(kFewThreads), 0, stream, pdl, b, one);
+    }
     if (a.E <= 128)
         return launch_select<4>(a, logits, stream, pdl);
     if (a.E <= 256)
