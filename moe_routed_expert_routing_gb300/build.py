@@ -22,7 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["moe_api.cu", "dispatch.cu", "dispatch_noalloc.cu", "combine.cu", "grouped_gemm.cu", "weights_pack.cu",
            "weights_mx.cu", "norm.cu", "route.cu", "route_gemm.cu", "combine_residual.cu", "block_api.cu"]
-HEADERS = ["ptx.cuh", "moe_internal.h", "route_select.cuh"]
+HEADERS = ["ptx.cuh", "moe_internal.h", "route_select.cuh", "row_ops.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -134,9 +134,10 @@ moe_status_t check_layer(const moe_layer_problem_t *p)
 }
 
 // Workspace of moe_layer: the one of moe_forward (header first), then the
-// normalised rows, the logits and the block's output.
+// normalised rows, the router's scratch and, for the one-kernel form of the
+// experts, y and its row sums.
 struct LayerLayout {
-    size_t forward, x, part, y, total;
+    size_t forward, x, part, y, sums, total;
 };
 
 moe_status_t layer_layout(const moe_layer_problem_t &p, LayerLayout *L)
@@ -151,7 +152,9 @@ moe_status_t layer_layout(const moe_layer_problem_t &p, LayerLayout *L)
     L->part = o;
     o = align_up(o + sizeof(float) * route_scratch_floats(p.experts.T_max, p.experts.E, p.experts.H, true));
     L->y = o;
-    o = align_up(o + 2 * T * H);
+    L->sums = align_up(o + sizeof(float) * T * H);
+    if (p.experts.forward_form == MOE_FORWARD_ONE_KERNEL)
+        o = align_up(L->sums + sizeof(float) * tail_sum_floats(p.experts.T_max, p.experts.H));
     L->total = o;
     return MOE_OK;
 }
@@ -341,8 +344,8 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
     r.part = at<float>(ws, L.part);
     // a few routed slots: the router's last CTA dispatches them (the one-kernel
     // form of the experts dispatches by itself)
-    const bool dispatched = p.experts.T_max * p.experts.k <= kRouteDispatchSlots &&
-                            p.experts.forward_form != MOE_FORWARD_ONE_KERNEL;
+    r.one_kernel = p.experts.forward_form == MOE_FORWARD_ONE_KERNEL;
+    const bool dispatched = p.experts.T_max * p.experts.k <= kRouteDispatchSlots && !r.one_kernel;
     if (dispatched) {
         r.expert_offsets = expert_offsets;
         r.perm = perm;
@@ -351,7 +354,7 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
     if ((st = cuda_status(launch_route(r, s, true))) != MOE_OK)
         return st;
     return enqueue_forward(p.experts, x, topk_ids, topk_weights, d_num_tokens, W13, W2, expert_offsets, perm,
-                           at<void>(ws, L.y), ws, s, nullptr, &n, dispatched);
+                           at<void>(ws, L.y), ws, s, nullptr, &n, dispatched, at<float>(ws, L.sums));
 }
 
 }  // extern "C"

@@ -14,6 +14,7 @@
 
 #include "moe_internal.h"
 #include "ptx.cuh"
+#include "row_ops.cuh"
 
 namespace moe {
 
@@ -54,42 +55,6 @@ __device__ __forceinline__ float cluster_sum(float v, float *s_warp, float *slot
     return total;
 }
 
-__device__ __forceinline__ void load4(const void *p, bool f32, size_t i, float (&f)[4])
-{
-    if (f32) {
-        const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-    } else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i);
-        f[0] = __uint_as_float(v.x << 16);
-        f[1] = __uint_as_float(v.x & 0xffff0000u);
-        f[2] = __uint_as_float(v.y << 16);
-        f[3] = __uint_as_float(v.y & 0xffff0000u);
-    }
-}
-
-__device__ __forceinline__ void store4_bf16(void *p, size_t i, const float (&f)[4])
-{
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
-    uint2 o;
-    o.x = *reinterpret_cast<const uint32_t *>(&lo);
-    o.y = *reinterpret_cast<const uint32_t *>(&hi);
-    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + i) = o;
-}
-
-__device__ __forceinline__ void weight4(const NormArgs &a, const void *w, int m, float (&f)[4])
-{
-    if (!w) {
-        f[0] = f[1] = f[2] = f[3] = 1.f;
-        return;
-    }
-    load4(w, a.w_f32, m, f);
-    if (a.unit_offset)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f[i] = 1.f + f[i];
-}
-
 // Y: fp32, or fp16 (the tiled paths' intermediate). kParts: K parts of fp32 y,
 // part_stride elements apart, summed in part order as in combine.cu.
 template <typename Y, int kParts>
@@ -126,13 +91,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
         load4(a.h, a.h_f32, t * a.h_stride + m, h[v]);
         weight4(a, a.norm_block ? a.w_post : nullptr, m, wp[v]);
         weight4(a, a.x ? a.w_next : nullptr, m, wn[v]);
-        g[v][0] = g[v][1] = g[v][2] = g[v][3] = 1.f;
-        if (a.gate_kind == MOE_GATE_CHANNEL)
-            load4(a.gate, a.w_f32, m, g[v]);
-        else if (a.gate_kind == MOE_GATE_TOKEN)
-            g[v][0] = g[v][1] = g[v][2] = g[v][3] = static_cast<const float *>(a.gate)[t];
-        else if (a.gate_kind == MOE_GATE_ELEMENT)
-            load4(a.gate, false, t * a.gate_stride + m, g[v]);
+        gate4(a, t, m, g[v]);
     }
     pdl_wait();
     pdl_trigger();
@@ -206,11 +165,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
             sum = fmaf(y[v][i], y[v][i], sum);
         }
         const size_t o = t * a.out_stride + m0 + c;
-        if (a.h_f32)
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.h_out) + o) =
-                make_float4(y[v][0], y[v][1], y[v][2], y[v][3]);
-        else
-            store4_bf16(a.h_out, o, y[v]);
+        store4(a.h_out, a.h_f32, o, y[v]);
     }
     if (a.x) {
         const float r = 1.f / sqrtf(cluster_sum(sum, s_warp[1], &s_slot[1]) / a.H + a.eps);

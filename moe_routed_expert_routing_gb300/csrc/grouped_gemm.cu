@@ -55,10 +55,12 @@
 // the down GEMM stores y in fp32, so the only rounding between the fp32
 // accumulators and the combine's fp32 sum is the final one to bf16 (on the
 // tiled paths moe_forward asks for fp16 y instead, rounded once, saturating).
+#include <type_traits>
 #include <cuda_bf16.h>
 
 #include "moe_internal.h"
 #include "ptx.cuh"
+#include "row_ops.cuh"
 
 namespace moe {
 
@@ -1021,11 +1023,130 @@ __device__ void cta_combine(const FusedArgs &fa, const int *s_inv, int T)
     }
 }
 
-template <int kTileRows, int kStages, int kSplitDown, bool kMega, bool kFp8>
+// moe_layer's end inside the whole-forward form: in place of the combine, the
+// block's output goes through norm, gate and residual scale into the residual
+// stream, and on to the next norm (as combine_residual.cu). An item is one
+// token x 4 kThreads columns, as in the combine; the row sums need all items
+// of a token, so each phase ends at the GPU-wide count `done` once more.
+struct NoTail {};
+
+struct TailArgs {
+    NormArgs n;
+    float *y;        // [T_max, H]: y, then h' in fp32
+    float *sums;     // [2][T_max * items of a token]: sums of squares of y and of h'
+};
+
+// Sum of v over the block in every thread; s: kThreads / 32 words.
+template <int kThreads>
+__device__ __forceinline__ float cta_sum(float v, float *s)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(kFull, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int i = 0; i < kThreads / 32; ++i)
+        v += s[i];
+    return v;
+}
+
+// r of a row from its items' sums of squares
+__device__ __forceinline__ float row_r(const float *sums, int n, int H, float eps)
+{
+    float v = 0.f;
+    for (int i = 0; i < n; ++i)
+        v += __ldcg(sums + i);
+    return 1.f / sqrtf(v / H + eps);
+}
+
+// phase 0: y and its sums; 1: h' into the residual stream, and its sums; 2: x_next
+template <int kSplitDown, int kThreads>
+__device__ void cta_tail(const FusedArgs &fa, const TailArgs &ta, const int *s_inv, int T, float *s_red, int phase)
+{
+    const NormArgs &n = ta.n;
+    const int k = fa.up.k, H = fa.down.n_out, vec = H / 4;
+    const int groups = (vec + kThreads - 1) / kThreads;
+    const float4 *y0 = static_cast<const float4 *>(fa.down.out);
+    const size_t part = static_cast<size_t>(fa.down.cap) * vec;
+    const int items = T * groups;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int t = item / groups;
+        const int c = item % groups * kThreads + threadIdx.x;
+        const bool mine = c < vec;
+        const size_t at = static_cast<size_t>(t) * H + 4 * c;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (phase == 0) {
+            for (int j = 0; mine && j < k; ++j) {
+                const int row = s_inv[t * k + j];
+                if (row < 0)
+                    continue;
+                const float w = __ldg(fa.topk_w + static_cast<size_t>(t) * k + j);
+                const size_t i = static_cast<size_t>(row) * vec + c;
+                float4 f[kSplitDown];
+#pragma unroll
+                for (int p = 0; p < kSplitDown; ++p)
+                    f[p] = __ldcg(y0 + p * part + i);
+#pragma unroll
+                for (int p = 1; p < kSplitDown; ++p) {
+                    f[0].x = __fadd_rn(f[0].x, f[p].x);
+                    f[0].y = __fadd_rn(f[0].y, f[p].y);
+                    f[0].z = __fadd_rn(f[0].z, f[p].z);
+                    f[0].w = __fadd_rn(f[0].w, f[p].w);
+                }
+                v[0] = __fadd_rn(v[0], __fmul_rn(w, f[0].x));
+                v[1] = __fadd_rn(v[1], __fmul_rn(w, f[0].y));
+                v[2] = __fadd_rn(v[2], __fmul_rn(w, f[0].z));
+                v[3] = __fadd_rn(v[3], __fmul_rn(w, f[0].w));
+            }
+        } else if (mine) {
+            const float4 f = *reinterpret_cast<const float4 *>(ta.y + at);   // this thread's own store
+            v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        }
+        float wt[4];
+        if (phase == 1) {
+            const float r = n.norm_block ? row_r(ta.sums + t * groups, groups, H, n.eps) : 1.f;
+            if (mine) {
+                float h[4], g[4];
+                load4(n.h, n.h_f32, t * n.h_stride + 4 * c, h);
+                weight4(n, n.norm_block ? n.w_post : nullptr, 4 * c, wt);
+                gate4(n, t, 4 * c, g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = h[i] + n.scale * g[i] * (v[i] * r * wt[i]);
+                store4(n.h_out, n.h_f32, t * n.out_stride + 4 * c, v);
+            }
+        } else if (phase == 2) {
+            const float r = row_r(ta.sums + (fa.T_max + t) * groups, groups, H, n.eps);
+            if (mine) {
+                weight4(n, n.w_next, 4 * c, wt);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = v[i] * r * wt[i];
+                store4_bf16(n.x, t * n.x_stride + 4 * c, v);
+            }
+            continue;
+        }
+        if (mine)
+            *reinterpret_cast<float4 *>(ta.y + at) = make_float4(v[0], v[1], v[2], v[3]);
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q = fmaf(v[i], v[i], q);
+        q = cta_sum<kThreads>(q, s_red);
+        if (threadIdx.x == 0)
+            ta.sums[(phase * fa.T_max + t) * groups + item % groups] = q;
+    }
+    __threadfence();
+}
+
+template <int kTileRows, int kStages, int kSplitDown, bool kMega, bool kFp8, class Tail = NoTail>
 __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCta, 1)
     fused_small_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w13,
                        const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_w2,
-                       const FusedArgs fa)
+                       const FusedArgs fa, const __grid_constant__ Tail tail)
 {
     using C = FusedCfg<kTileRows, kStages, kFp8>;
     constexpr int kThreads = C::kThreadsCta;
@@ -1561,8 +1682,31 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
             }
         }
         __syncthreads();
-        if (!s_abort)
-            cta_combine<kSplitDown, kThreads>(fa, s_inv, s_T);
+        if constexpr (std::is_same<Tail, TailArgs>::value) {
+            float *const s_red = reinterpret_cast<float *>(smem);   // the stages are free
+            const int last = tail.n.x ? 2 : 1;
+            for (int phase = 0; phase <= last && !s_abort; ++phase) {
+                cta_tail<kSplitDown, kThreads>(fa, tail, s_inv, s_T, s_red, phase);
+                __syncthreads();
+                if (phase == last)
+                    break;
+                // the other CTAs' sums (their threads fenced their stores)
+                if (threadIdx.x == 0) {
+                    red_release_gpu_add(fa.done, 1);
+                    const uint64_t t0 = global_timer_ns();
+                    while (ld_acquire_gpu(fa.done) < need * (phase + 2)) {
+                        if (global_timer_ns() - t0 > A1.wait_limit_ns) {
+                            s_abort = 1;
+                            break;
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+        } else {
+            if (!s_abort)
+                cta_combine<kSplitDown, kThreads>(fa, s_inv, s_T);
+        }
         __syncthreads();
     }
     // tail clean-up: the last CTA out (every other CTA has passed all its
@@ -2179,12 +2323,12 @@ bool make_map_codes(CUtensorMap *m, const void *base, uint64_t rows, uint64_t K)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kTileRows, int kStages, int kSplitDown, bool kMega, bool kFp8>
+template <int kTileRows, int kStages, int kSplitDown, bool kMega, bool kFp8, class Tail = NoTail>
 cudaError_t run_fused(const GemmProblem &up, const GemmProblem &down, int32_t *ready, int32_t *counters,
-                      int num_sms, cudaStream_t stream, const MegaParams *mega)
+                      int num_sms, cudaStream_t stream, const MegaParams *mega, const Tail &tail = Tail())
 {
     using C = FusedCfg<kTileRows, kStages, kFp8>;
-    auto kern = fused_small_kernel<kTileRows, kStages, kSplitDown, kMega, kFp8>;
+    auto kern = fused_small_kernel<kTileRows, kStages, kSplitDown, kMega, kFp8, Tail>;
     const long long slots = mega ? static_cast<long long>(mega->T_max) * up.k : 0;
     const long long tables = kMega ? mega_table_bytes(up.E, slots) : 0;
     long long budget = 0;
@@ -2252,7 +2396,7 @@ cudaError_t run_fused(const GemmProblem &up, const GemmProblem &down, int32_t *r
     const int grid_sms = fused_grid_sms(whole_forward, kFp8, up.cap, up.E, up.n_out, kTileRows, num_sms);
     const long long want = max_units < grid_sms ? (max_units < 1 ? 1 : max_units) : grid_sms;
     return launch_k_coresident(kern, want, dim3(C::kThreadsCta), dyn_smem, stream, up.pdl, num_sms, tm_x, tm_w13,
-                               tm_h, tm_w2, fa);
+                               tm_h, tm_w2, fa, tail);
 }
 
 }  // namespace
@@ -2304,6 +2448,26 @@ cudaError_t launch_grouped_gemm(const GemmProblem &p, int num_sms, cudaStream_t 
     }
 }
 
+namespace {
+
+// moe_layer's form of the whole-forward kernel: the tail in place of the combine.
+template <int kStages, bool kFp8>
+cudaError_t run_fused_tail(const GemmProblem &up, const GemmProblem &down, int32_t *ready, int32_t *counters,
+                           int num_sms, cudaStream_t stream, const MegaParams *mega)
+{
+    TailArgs ta;
+    ta.n = *mega->tail;
+    ta.y = mega->tail_y;
+    ta.sums = mega->tail_sums;
+    return down.split_k == 4
+               ? run_fused<16, kStages, 4, true, kFp8, TailArgs>(up, down, ready, counters, num_sms, stream, mega, ta)
+           : down.split_k == 2
+               ? run_fused<16, kStages, 2, true, kFp8, TailArgs>(up, down, ready, counters, num_sms, stream, mega, ta)
+               : run_fused<16, kStages, 1, true, kFp8, TailArgs>(up, down, ready, counters, num_sms, stream, mega, ta);
+}
+
+}  // namespace
+
 cudaError_t launch_fused_small(const GemmProblem &up, const GemmProblem &down, int32_t *ready, int32_t *counters,
                                int num_sms, cudaStream_t stream, const MegaParams *mega)
 {
@@ -2326,6 +2490,8 @@ cudaError_t launch_fused_small(const GemmProblem &up, const GemmProblem &down, i
             return cudaErrorInvalidValue;
         switch (up.tile_rows) {
         case 16:
+            if (mega && mega->tail)
+                return run_fused_tail<5, true>(up, down, ready, counters, num_sms, stream, mega);
             if (mega)
                 return down.split_k == 4   ? run_fused<16, 5, 4, true, true>(up, down, ready, counters, num_sms, stream, mega)
                        : down.split_k == 2 ? run_fused<16, 5, 2, true, true>(up, down, ready, counters, num_sms, stream, mega)
@@ -2351,6 +2517,8 @@ cudaError_t launch_fused_small(const GemmProblem &up, const GemmProblem &down, i
         return cudaErrorInvalidValue;
     if ((down.K / kBK) % down.split_k != 0)
         return cudaErrorInvalidValue;
+    if (mega && mega->tail)
+        return run_fused_tail<6, false>(up, down, ready, counters, num_sms, stream, mega);
     if (mega)
         return down.split_k == 4   ? run_fused<16, 6, 4, true, false>(up, down, ready, counters, num_sms, stream, mega)
                : down.split_k == 2 ? run_fused<16, 6, 2, true, false>(up, down, ready, counters, num_sms, stream, mega)

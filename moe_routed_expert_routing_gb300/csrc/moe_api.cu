@@ -435,7 +435,7 @@ moe_status_t check_forward(const moe_problem_t &p)
 moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_t *topk_ids,
                              const float *topk_weights, const int32_t *d_num_tokens, const void *W13, const void *W2,
                              int32_t *expert_offsets, int32_t *perm, void *out, void *ws, cudaStream_t s,
-                             void *const *stage_events, const NormArgs *tail, bool dispatched)
+                             void *const *stage_events, const NormArgs *tail, bool dispatched, float *tail_sums)
 {
     moe_status_t st = MOE_OK;
     const Layout L = layout_of(p);
@@ -459,17 +459,14 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
         mp.expert_offsets_out = expert_offsets;
         mp.perm_out = perm;
         mp.out = out;
+        mp.tail = tail;
+        mp.tail_y = static_cast<float *>(out);
+        mp.tail_sums = tail_sums;
         if ((st = mark(0)) != MOE_OK)
             return st;
         st = enqueue_expert_compute(p, x, nullptr, W13, W2, y_sorted, ws, s, nullptr, nullptr, nullptr, true, &mp);
         for (int i = 1; st == MOE_OK && i < 6; ++i)
             st = mark(i);
-        if (st == MOE_OK && tail) {
-            NormArgs n = *tail;
-            n.y = out;
-            n.y_stride = p.H;
-            st = cuda_status(launch_norm(n, sms, s, true));
-        }
         return st;
     }
     // a down GEMM that splits K leaves its parts in the workspace's y buffers;

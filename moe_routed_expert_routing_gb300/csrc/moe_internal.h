@@ -116,6 +116,22 @@ cudaError_t launch_k_coresident(void (*kernel)(KArgs...), long long want_ctas, d
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The norms around the block (norm.cu, combine_residual.cu, grouped_gemm.cu)
+struct NormArgs {
+    const void *h;             // residual stream, bf16 or fp32
+    const void *y;             // block output, bf16 (null: norm of h only)
+    const void *w_post;        // null: no weight
+    const void *gate;
+    const void *w_next;        // weight of x_next (moe_norm: of x); null: no weight
+    const int32_t *d_num_tokens;
+    void *h_out;
+    void *x;                   // x_next (moe_norm: x), bf16; null: not computed
+    int T_max, H;
+    int h_f32, w_f32, unit_offset, norm_block, gate_kind;
+    float eps, scale;
+    long long h_stride, y_stride, x_stride, out_stride, gate_stride;
+};
+
 // ---- dispatch (dispatch.cu) ----
 cudaError_t launch_dispatch(const int32_t *topk_ids, const int32_t *d_num_tokens, int T_max, int k, int E,
                             int32_t *block_counts, int32_t *block_base, int32_t *expert_offsets,
@@ -196,7 +212,15 @@ struct MegaParams {
     // above and inv) and the combine kernel after it: the fused kernel only
     // dispatches locally for its own units
     bool combine_apart = false;
+    // moe_layer: in place of the combine, the way back into the residual
+    // stream (null: combine into `out`), with fp32 scratch for y [T_max, H]
+    // and for row sums (tail_sum_floats)
+    const NormArgs *tail = nullptr;
+    float *tail_y = nullptr;
+    float *tail_sums = nullptr;
 };
+
+inline size_t tail_sum_floats(int T_max, int H) { return 2 * static_cast<size_t>(T_max) * ((H + 1023) / 1024); }
 
 // Both M-small GEMMs in one persistent launch (gate-up with gathered rows, then
 // down). ready[E] and counters[2] must be zero when the kernel starts; the
@@ -213,21 +237,6 @@ cudaError_t launch_fused_small(const GemmProblem &up, const GemmProblem &down, i
 bool fused_mega_fits(int E, long long slots, bool mxfp8);
 
 // ---- norms around the block (norm.cu) ----
-struct NormArgs {
-    const void *h;             // residual stream, bf16 or fp32
-    const void *y;             // block output, bf16 (null: norm of h only)
-    const void *w_post;        // null: no weight
-    const void *gate;
-    const void *w_next;        // weight of x_next (moe_norm: of x); null: no weight
-    const int32_t *d_num_tokens;
-    void *h_out;
-    void *x;                   // x_next (moe_norm: x), bf16; null: not computed
-    int T_max, H;
-    int h_f32, w_f32, unit_offset, norm_block, gate_kind;
-    float eps, scale;
-    long long h_stride, y_stride, x_stride, out_stride, gate_stride;
-};
-
 // x = norm(h) (y null), or h_out = h + s * g * norm(y) and x = norm(h_out).
 cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t stream, bool pdl);
 
@@ -259,6 +268,7 @@ struct RouteArgs {
     void *x_out;               // [T_max, H] bf16
     // moe_layer, at most kRouteDispatchSlots slots: moe_dispatch's tables, or null
     int32_t *expert_offsets, *perm, *inv;
+    int one_kernel;            // the last CTA selects for up to 16 tokens, in the same kernel
     long long x_stride;
     float eps;
 };
@@ -283,7 +293,7 @@ constexpr int kRouteJoinTokens = 2;
 constexpr int kRouteBlockTokens = 152;      // one block per SM
 constexpr int kRouteDispatchSlots = 128;
 
-inline RouteSplit route_split(int T_max, int E, int H)
+inline RouteSplit route_split(int T_max, int E, int H, bool one_kernel = false)
 {
     RouteSplit r;
     r.tiles = T_max <= 16 ? 1 : (T_max <= 64 ? 2 : 4);
@@ -292,7 +302,7 @@ inline RouteSplit route_split(int T_max, int E, int H)
     const int blocks = H / 64;
     const int want = 152 / (r.groups * r.chunks);
     r.slices = want < 1 ? 1 : (want < blocks ? want : blocks);
-    r.join = T_max <= kRouteJoinTokens;
+    r.join = T_max <= (one_kernel ? 16 : kRouteJoinTokens);
     return r;
 }
 
@@ -374,13 +384,15 @@ moe_status_t validate_device();
 // or weight layout that the shape cannot take.
 moe_status_t check_forward(const moe_problem_t &problem);
 // moe_forward after its checks. With `tail`, the combine's place is taken by
-// launch_combine_residual: `out` is scratch, and the block's output goes into
-// the residual stream as `tail` says. With `dispatched`, expert_offsets, perm
+// launch_combine_residual, or by the end of the one-kernel form (`out` is then
+// fp32 scratch [T_max, H], tail_sums tail_sum_floats of it), and the block's
+// output goes into the residual stream as `tail` says. With `dispatched`, expert_offsets, perm
 // and inv (forward_inv) are already written by the kernel before.
 moe_status_t enqueue_forward(const moe_problem_t &problem, const void *x, const int32_t *topk_ids,
                              const float *topk_weights, const int32_t *d_num_tokens, const void *W13, const void *W2,
                              int32_t *expert_offsets, int32_t *perm, void *out, void *ws, cudaStream_t stream,
-                             void *const *stage_events, const NormArgs *tail, bool dispatched);
+                             void *const *stage_events, const NormArgs *tail, bool dispatched,
+                             float *tail_sums = nullptr);
 int32_t *forward_inv(const moe_problem_t &problem, void *ws);
 // bytes at the start of every workspace: the device error word and the
 // counters that kernels leave at zero (moe_clear_device_error clears them)

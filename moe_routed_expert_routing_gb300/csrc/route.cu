@@ -663,7 +663,7 @@ cudaError_t launch_few(const RouteArgs &a, const RouteSplit &sp, cudaStream_t st
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl)
 {
     if (a.normed || a.T_max <= kRouteFewTokens) {
-        const RouteSplit sp = route_split(a.T_max, a.E, a.H);
+        const RouteSplit sp = route_split(a.T_max, a.E, a.H, a.one_kernel != 0);
         switch (sp.tiles) {
         case 1:
             return launch_few<1>(a, sp, stream, pdl);
