@@ -134,7 +134,7 @@ moe_status_t check_layer(const moe_layer_problem_t *p)
 }
 
 // Workspace of moe_layer: the one of moe_forward (header first), then the
-// normalised rows, the router's scratch and, for the one-kernel form of the
+// normalised rows (paired), the router's scratch and, for the one-kernel form of the
 // experts, y and its row sums.
 struct LayerLayout {
     size_t forward, x, part, y, sums, total;
@@ -142,13 +142,14 @@ struct LayerLayout {
 
 moe_status_t layer_layout(const moe_layer_problem_t &p, LayerLayout *L)
 {
-    const moe_status_t st = moe_workspace_size(&p.experts, &L->forward);
+    const moe_problem_t q = paired_problem(p.experts);
+    const moe_status_t st = moe_workspace_size(&q, &L->forward);
     if (st != MOE_OK)
         return st;
     const size_t T = p.experts.T_max, H = p.experts.H;
     size_t o = align_up(L->forward);
     L->x = o;
-    o = align_up(o + 2 * T * H);
+    o = align_up(o + 2 * 2 * T * H);
     L->part = o;
     o = align_up(o + sizeof(float) * route_scratch_floats(p.experts.T_max, p.experts.E, p.experts.H, true));
     L->y = o;
@@ -312,7 +313,7 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
         return MOE_ERR_ALIGN;
     LayerLayout L = {};
     if ((st = layer_layout(p, &L)) != MOE_OK || (st = check_ws(ws, ws_bytes, L.total)) != MOE_OK ||
-        (st = validate_device()) != MOE_OK || (st = check_forward(p.experts)) != MOE_OK)
+        (st = validate_device()) != MOE_OK || (st = check_forward(paired_problem(p.experts))) != MOE_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *x = at<void>(ws, L.x);
@@ -349,7 +350,7 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
     if (dispatched) {
         r.expert_offsets = expert_offsets;
         r.perm = perm;
-        r.inv = forward_inv(p.experts, ws);
+        r.inv = forward_inv(paired_problem(p.experts), ws);
     }
     if ((st = cuda_status(launch_route(r, s, true))) != MOE_OK)
         return st;

@@ -2,7 +2,8 @@
 // of the experts' rows (as combine.cu), normed, gated and scaled into the
 // residual stream, and the next block's norm, in one pass.
 //
-//   y[t, m] = sum_{j = 0..k-1} w[t, j] * y_sorted[inv[t*k + j], m]      (fp32, kept unrounded)
+//   y[t, m] = sum_{j = 0..k-1} w[t, j] * (y_sorted[2 r, m] + y_sorted[2 r + 1, m]),  r = inv[t*k + j]
+//                                                              (paired rows; fp32, kept unrounded)
 //   h'      = h + s * g * (y * r(y) * w_post),  x_next = h' * r(h') * w_next
 //
 // A token's row goes over a cluster of eight CTAs: at one token a single SM
@@ -10,7 +11,6 @@
 // its own L2 port. The two row sums meet through distributed shared memory;
 // each thread keeps its columns of y and h' in registers between them.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include "moe_internal.h"
 #include "ptx.cuh"
@@ -55,11 +55,11 @@ __device__ __forceinline__ float cluster_sum(float v, float *s_warp, float *slot
     return total;
 }
 
-// Y: fp32, or fp16 (the tiled paths' intermediate). kParts: K parts of fp32 y,
-// part_stride elements apart, summed in part order as in combine.cu.
-template <typename Y, int kParts>
+// kParts: K parts of y, part_stride elements apart, summed in part order as in
+// combine.cu, each part's pair of rows first.
+template <int kParts>
 __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThreads, kParts == 1 ? 2 : 1)
-    combine_residual_kernel(const Y *y_sorted, const int32_t *inv, const float *w, const __grid_constant__ NormArgs a,
+    combine_residual_kernel(const float *y_sorted, const int32_t *inv, const float *w, const __grid_constant__ NormArgs a,
                             int k, size_t part_stride)
 {
     __shared__ float s_warp[2][kTailThreads / 32];
@@ -70,7 +70,8 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
     // Ahead of the wait for y: the routing, h, the weights and the gate are
     // inputs of the call or were written two launches back or more, which is
     // complete (see launch_k), and of a token past the count nothing is used.
-    constexpr int kRows = kParts == 1 ? 4 : 8;       // routed rows in flight
+    constexpr int kRows = kParts == 2 ? 8 : 4;       // routed rows in flight
+    constexpr int kSums = 2 * kParts;                // what a routed row is the sum of: its pair's parts
     int row[kRows];
     float wj[kRows];
     auto routing = [&](int j0) {
@@ -115,22 +116,16 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
             const int c = 4 * (threadIdx.x + v * kTailThreads);
             if (c >= cols)
                 continue;
-            float f[kRows][kParts][4];
+            float f[kRows][kSums][4];
 #pragma unroll
             for (int q = 0; q < kRows; ++q)
 #pragma unroll
-                for (int p = 0; p < kParts; ++p)
+                for (int p = 0; p < kSums; ++p)
                     if (row[q] >= 0) {
-                        const Y *src = y_sorted + p * part_stride + static_cast<size_t>(row[q]) * a.H + m0 + c;
-                        if constexpr (sizeof(Y) == 2) {
-                            const uint2 u = *reinterpret_cast<const uint2 *>(src);
-                            const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
-                            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-                            f[q][p][0] = lo.x; f[q][p][1] = lo.y; f[q][p][2] = hi.x; f[q][p][3] = hi.y;
-                        } else {
-                            const float4 u = *reinterpret_cast<const float4 *>(src);
-                            f[q][p][0] = u.x; f[q][p][1] = u.y; f[q][p][2] = u.z; f[q][p][3] = u.w;
-                        }
+                        const float4 u = *reinterpret_cast<const float4 *>(
+                            y_sorted + (p >> 1) * part_stride + (2 * static_cast<size_t>(row[q]) + (p & 1)) * a.H + m0 +
+                            c);
+                        f[q][p][0] = u.x; f[q][p][1] = u.y; f[q][p][2] = u.z; f[q][p][3] = u.w;
                     }
 #pragma unroll
             for (int q = 0; q < kRows; ++q) {
@@ -140,7 +135,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
                 for (int i = 0; i < 4; ++i) {
                     float s = f[q][0][i];
 #pragma unroll
-                    for (int p = 1; p < kParts; ++p)
+                    for (int p = 1; p < kSums; ++p)
                         s = __fadd_rn(s, f[q][p][i]);
                     y[v][i] = __fadd_rn(y[v][i], __fmul_rn(wj[q], s));
                 }
@@ -185,22 +180,15 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kTailThre
 
 }  // namespace
 
-cudaError_t launch_combine_residual(const void *y_sorted, bool y_f16, const int32_t *inv, const float *topk_weights,
+cudaError_t launch_combine_residual(const float *y_sorted, const int32_t *inv, const float *topk_weights,
                                     const NormArgs &a, int k, int parts, size_t part_stride, cudaStream_t stream,
                                     bool pdl)
 {
-    if ((y_f16 && parts != 1) || a.H > kClusterCtas * kTailThreads * kTailVecs * 4)
+    if (a.H > kClusterCtas * kTailThreads * kTailVecs * 4 || (parts != 1 && parts != 2 && parts != 4))
         return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(a.T_max) * kClusterCtas), block(kTailThreads);
-    if (y_f16)
-        return launch_k(combine_residual_kernel<__half, 1>, grid, block, 0, stream, pdl,
-                        static_cast<const __half *>(y_sorted), inv, topk_weights, a, k, size_t(0));
-    auto kern = parts == 4 ? combine_residual_kernel<float, 4>
-                           : (parts == 2 ? combine_residual_kernel<float, 2> : combine_residual_kernel<float, 1>);
-    if (parts != 1 && parts != 2 && parts != 4)
-        return cudaErrorInvalidValue;
-    return launch_k(kern, grid, block, 0, stream, pdl, static_cast<const float *>(y_sorted), inv, topk_weights, a, k,
-                    part_stride);
+    auto kern = parts == 4 ? combine_residual_kernel<4> : (parts == 2 ? combine_residual_kernel<2> : combine_residual_kernel<1>);
+    return launch_k(kern, dim3(static_cast<unsigned>(a.T_max) * kClusterCtas), dim3(kTailThreads), 0, stream, pdl,
+                    y_sorted, inv, topk_weights, a, k, part_stride);
 }
 
 }  // namespace moe

@@ -271,15 +271,15 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows_kernel(const uint4
                                                                      const int32_t *__restrict__ perm,
                                                                      const int32_t *__restrict__ expert_offsets,
                                                                      int E, int k, int vec_per_row, int cap,
-                                                                     uint4 *__restrict__ x_sorted)
+                                                                     uint4 *__restrict__ x_sorted, int pair)
 {
     pdl_wait();
     pdl_trigger();
-    const int n_rows = min(expert_offsets[E], cap);
+    const int n_rows = min(expert_offsets[E] << pair, cap);
     const int lane = threadIdx.x & 31;
     const int warps = kGatherThreads / 32;
     for (int r = blockIdx.x * warps + (threadIdx.x >> 5); r < n_rows; r += gridDim.x * warps) {
-        const int t = perm[r] / k;
+        const int t = (perm[r >> pair] / k << pair) | (r & pair);   // pair: two rows of x per token
         const uint4 *src = x + static_cast<size_t>(t) * vec_per_row;
         uint4 *dst = x_sorted + static_cast<size_t>(r) * vec_per_row;
         for (int c0 = lane; c0 < vec_per_row; c0 += 32 * kGatherUnroll) {
@@ -326,7 +326,7 @@ cudaError_t launch_dispatch(const int32_t *topk_ids, const int32_t *d_num_tokens
 }
 
 cudaError_t launch_gather_rows(const void *x, const int32_t *perm, const int32_t *expert_offsets, int E, int k, int H,
-                               int cap, void *x_sorted, int num_sms, cudaStream_t stream, bool pdl)
+                               int cap, void *x_sorted, int num_sms, cudaStream_t stream, bool pdl, int pair)
 {
     const int warps = kGatherThreads / 32;
     int blocks = (cap + warps - 1) / warps;
@@ -335,7 +335,7 @@ cudaError_t launch_gather_rows(const void *x, const int32_t *perm, const int32_t
         blocks = 1;
     return launch_k(gather_rows_kernel, dim3(blocks), dim3(kGatherThreads), 0, stream, pdl,
                     static_cast<const uint4 *>(x), perm, expert_offsets, E, k, H / 8, cap,
-                    static_cast<uint4 *>(x_sorted));
+                    static_cast<uint4 *>(x_sorted), pair);
 }
 
 }  // namespace moe

@@ -84,6 +84,14 @@ struct GemmArgs {
     int up_row_offset;
     int w_packed;       // weights in the PACKED layout (see include/moe.h)
     int out_f16;        // tiled down GEMM: y stored as fp16 (saturated at +-65504) instead of fp32
+    // 1: paired rows (moe_layer). Each routed row is two activation rows, 2r
+    // and 2r + 1: a value's leading bf16 part and the rest, so that x and h
+    // count with 16 bits instead of 8. The few-token GEMMs stream weights past
+    // token tiles that are mostly empty, so the second row is free; the
+    // gate-up epilogue adds the pair's two sums before SiLU and splits h
+    // again, and the down GEMM's two rows are added by the combine. Offsets
+    // and perm count routed rows; row counts here, cap and x are doubled.
+    int pair;
     int32_t *sched;     // grouped_gemm_kernel: {units handed out, CTAs at the tail}, zero at launch and at exit;
                         // null: units dealt round-robin
 };
@@ -341,6 +349,66 @@ __device__ __forceinline__ void build_tile_prefix_block(const int *s_off, int *s
     __syncthreads();
 }
 
+// Activation row of x behind row `row` of the batch: its slot's token, or that
+// token's row of the pair.
+__device__ __forceinline__ int token_row(int slot, int k, int row, int pair) { return (slot / k << pair) | (row & pair); }
+
+// The two bf16 parts of v: their sum is v to 16 bits.
+__device__ __forceinline__ void split_bf16(float v, __nv_bfloat16 &hi, __nv_bfloat16 &lo)
+{
+    hi = __float2bfloat16_rn(v);
+    lo = __float2bfloat16_rn(v - __bfloat162float(hi));
+}
+
+// Gate-up epilogue of a 128-row tiled unit with paired rows: lanes 2i and
+// 2i + 1 hold a pair; the even one stores the leading parts, the odd one the rest.
+__device__ __forceinline__ void tiled_pair_epilogue(uint32_t t_row, const GemmArgs &args, int row, bool valid, int n0)
+{
+    const int cols = args.n_out - n0;
+    const bool odd = (row & 1) != 0;
+    uint4 *const orow =
+        reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(args.out) + static_cast<size_t>(row) * args.n_out + n0);
+#pragma unroll 1
+    for (int c = 0; c < 128 && c < cols; c += 16) {
+        uint32_t g[16], v[16];
+        tmem_ld_32x32b_x16(t_row + c, g);
+        tmem_ld_32x32b_x16(t_row + 128 + c, v);
+        tmem_wait_ld();
+        float o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float gs = __uint_as_float(g[i]), us = __uint_as_float(v[i]);
+            const float h = silu_mul(gs + __shfl_xor_sync(kFull, gs, 1), us + __shfl_xor_sync(kFull, us, 1));
+            const float lead = __bfloat162float(__float2bfloat16_rn(h));
+            o[i] = odd ? h - lead : lead;
+        }
+        if (valid) {
+            orow[c / 8] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                     pack_bf16x2(o[6], o[7]));
+            orow[c / 8 + 1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]),
+                                         pack_bf16x2(o[12], o[13]), pack_bf16x2(o[14], o[15]));
+        }
+    }
+}
+
+// Gate-up epilogue of 16 token rows of an M-small unit with paired rows: this
+// lane's weight column col, rows [row, row + 16) with the first n of the batch.
+__device__ __forceinline__ void small_pair_epilogue(const uint32_t (&g)[16], const uint32_t (&w)[16],
+                                                    const GemmArgs &args, int row, int n, int col)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        if (i >= n || row + i + 1 >= args.cap || col >= args.n_out)
+            continue;
+        __nv_bfloat16 hi, lo;
+        split_bf16(silu_mul(__uint_as_float(g[i]) + __uint_as_float(g[i + 1]),
+                            __uint_as_float(w[i]) + __uint_as_float(w[i + 1])), hi, lo);
+        __nv_bfloat16 *const h = static_cast<__nv_bfloat16 *>(args.out) + static_cast<size_t>(row + i) * args.n_out + col;
+        h[0] = hi;
+        h[args.n_out] = lo;
+    }
+}
+
 // Epilogue of a 128-row tiled unit: this thread owns accumulator row `row`
 // (TMEM lane base already in t_row); the warp's 32 rows are consecutive.
 // Gate-up: columns [0,128) gate, [128,256) up -> bf16 SiLU(gate)*up into h.
@@ -510,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // persistent grid and take issue slots from it.
     pdl_wait();
     for (int i = threadIdx.x; i <= E; i += kThreads)
-        s_off[i] = args.expert_offsets[i];
+        s_off[i] = args.expert_offsets[i] << args.pair;
     __syncthreads();
     if (warp == 3)
         build_tile_prefix(s_off, s_tp, E, kTileRows, lane);
@@ -563,7 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kGather) {
                 // token of every activation row of the tile; rows past the expert read token 0 and are never stored
                 for (int i = lane; i < kTileRows; i += 32)
-                    s_rows[i] = i < t.rows ? __ldg(args.perm + t.row0 + i) / args.k : 0;
+                    s_rows[i] = i < t.rows ? token_row(__ldg(args.perm + ((t.row0 + i) >> args.pair)), args.k,
+                                                       t.row0 + i, args.pair)
+                                           : 0;
                 __syncwarp();
             }
             if (lane == 0) {
@@ -699,8 +769,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!kSmallM) {
                 const int r = q * 32 + lane;
                 const int row = t.row0 + r;
-                tiled_epilogue<kGated>(t_row, args, row, r < t.rows && row >= 0 && row < args.cap, t.n0,
-                                       reinterpret_cast<float *>(smem + kStages * C::kStageBytes) + q * 32 * 36);
+                const bool valid = r < t.rows && row >= 0 && row < args.cap;
+                if (kGated && args.pair)
+                    tiled_pair_epilogue(t_row, args, row, valid, t.n0);
+                else
+                    tiled_epilogue<kGated>(t_row, args, row, valid, t.n0,
+                                           reinterpret_cast<float *>(smem + kStages * C::kStageBytes) + q * 32 * 36);
             } else {
                 // lane = weight row = output column t.n0 + 32q + lane; TMEM column = token row of the tile
                 const int col = t.n0 + q * 32 + lane;
@@ -711,6 +785,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kGated)
                         tmem_ld_32x32b_x16(t_row + kTileRows + c, v);
                     tmem_wait_ld();
+                    if (kGated && args.pair) {
+                        small_pair_epilogue(g, v, args, t.row0 + c, t.rows - c, col);
+                        continue;
+                    }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int rr = c + i;
@@ -1080,17 +1158,17 @@ __device__ void cta_tail(const FusedArgs &fa, const TailArgs &ta, const int *s_i
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (phase == 0) {
             for (int j = 0; mine && j < k; ++j) {
-                const int row = s_inv[t * k + j];
+                const int row = 2 * s_inv[t * k + j];   // of the pair
                 if (row < 0)
                     continue;
                 const float w = __ldg(fa.topk_w + static_cast<size_t>(t) * k + j);
                 const size_t i = static_cast<size_t>(row) * vec + c;
-                float4 f[kSplitDown];
+                float4 f[2 * kSplitDown];
 #pragma unroll
-                for (int p = 0; p < kSplitDown; ++p)
-                    f[p] = __ldcg(y0 + p * part + i);
+                for (int p = 0; p < 2 * kSplitDown; ++p)
+                    f[p] = __ldcg(y0 + (p >> 1) * part + (p & 1) * vec + i);
 #pragma unroll
-                for (int p = 1; p < kSplitDown; ++p) {
+                for (int p = 1; p < 2 * kSplitDown; ++p) {
                     f[0].x = __fadd_rn(f[0].x, f[p].x);
                     f[0].y = __fadd_rn(f[0].y, f[p].y);
                     f[0].z = __fadd_rn(f[0].z, f[p].z);
@@ -1229,9 +1307,14 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
             s_T = T;
     } else {
         for (int i = threadIdx.x; i <= E; i += kThreads)
-            s_off[i] = A1.expert_offsets[i];
+            s_off[i] = A1.expert_offsets[i] << A1.pair;
     }
     __syncthreads();
+    if (kMega && A1.pair) {   // the local dispatch counts routed rows
+        for (int i = threadIdx.x; i <= E; i += kThreads)
+            s_off[i] <<= 1;
+        __syncthreads();
+    }
     // bf16: the block-wide prefix. MXFP8: one warp's, as before (measured with
     // the block-wide one: decode T=8 749.4 vs 680.5 us, T=1 127.4 vs 118.4 us;
     // the converter warps' schedule, which sets that kernel's pace, came out
@@ -1287,8 +1370,9 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
             bool pre = false;
             if (!kFp8 && up && !fa.act_sorted) {
                 static_assert(kFp8 || kTileRows <= 32, "one row per lane");
+                const int prow = (t.row0 + lane) >> A1.pair;
                 const int slot = lane < t.rows && lane < kTileRows
-                                     ? (kMega ? s_perm[t.row0 + lane] : __ldg(A1.perm + t.row0 + lane))
+                                     ? (kMega ? s_perm[prow] : __ldg(A1.perm + prow))
                                      : 0;
                 if (lane == 0 && ok && steps > 0) {
                     if (mbar_wait_bounded(smem_u32(&bar_empty[stage]), phase ^ 1u, abort_flag, A1.wait_limit_ns)) {
@@ -1306,11 +1390,14 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
                     }
                 }
                 if (lane < kTileRows)
-                    s_rows[lane] = slot / A1.k;
+                    s_rows[lane] = token_row(slot, A1.k, t.row0 + lane, A1.pair);
                 __syncwarp();
             } else if (up && !fa.act_sorted) {
                 for (int i = lane; i < kTileRows; i += 32)
-                    s_rows[i] = i < t.rows ? (kMega ? s_perm[t.row0 + i] : __ldg(A1.perm + t.row0 + i)) / A1.k : 0;
+                    s_rows[i] = i < t.rows ? token_row(kMega ? s_perm[(t.row0 + i) >> A1.pair]
+                                                             : __ldg(A1.perm + ((t.row0 + i) >> A1.pair)),
+                                                       A1.k, t.row0 + i, A1.pair)
+                                           : 0;
                 __syncwarp();
             }
             if (lane == 0) {
@@ -1626,6 +1713,10 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
                 if (up)
                     tmem_ld_32x32b_x16(t_row + kTileRows + c, w);
                 tmem_wait_ld();
+                if (up && A1.pair) {
+                    small_pair_epilogue(g, w, A1, t.row0 + c, t.rows - c, col);
+                    continue;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int rr = c + i;
@@ -2173,6 +2264,7 @@ cudaError_t run(const GemmProblem &p, int num_sms, cudaStream_t stream)
     a.w_packed = p.w_packed ? 1 : 0;
     a.out_f16 = p.out_f16 ? 1 : 0;
     a.sched = p.sched;
+    a.pair = p.pair;
     // Upper bound of the units any routing can produce; no more CTAs than that.
     const long long max_row_tiles = (static_cast<long long>(p.cap) + kTileRows - 1) / kTileRows + p.E;
     const long long max_units = max_row_tiles * ((p.n_out + C::kOutCols - 1) / C::kOutCols) * kSplitK;
@@ -2245,6 +2337,7 @@ cudaError_t run_pair(const GemmProblem &p, int num_sms, cudaStream_t stream)
     a.w_packed = p.w_packed ? 1 : 0;
     a.out_f16 = p.out_f16 ? 1 : 0;
     a.sched = nullptr;
+    a.pair = 0;   // paired rows run on single CTAs
     const long long max_units =
         ((static_cast<long long>(p.cap) + 255) / 256 + p.E) * ((p.n_out + C::kOutCols - 1) / C::kOutCols);
     long long clusters = max_units < max_clusters ? max_units : max_clusters;
@@ -2273,6 +2366,7 @@ GemmArgs make_args(const GemmProblem &p)
     a.w_packed = p.w_packed ? 1 : 0;
     a.out_f16 = 0;
     a.sched = nullptr;
+    a.pair = p.pair;
     return a;
 }
 
@@ -2393,7 +2487,8 @@ cudaError_t run_fused(const GemmProblem &up, const GemmProblem &down, int32_t *r
     const long long tiles = (static_cast<long long>(up.cap) + kTileRows - 1) / kTileRows + up.E;
     const long long max_units = tiles * ((up.n_out + 127) / 128 + ((down.n_out + 127) / 128) * kSplitDown);
     const bool whole_forward = kMega && !(mega && mega->combine_apart);
-    const int grid_sms = fused_grid_sms(whole_forward, kFp8, up.cap, up.E, up.n_out, kTileRows, num_sms);
+    const int grid_sms = fused_grid_sms(whole_forward, kFp8, up.cap >> up.pair, up.E, up.n_out, kTileRows >> up.pair,
+                                        num_sms);
     const long long want = max_units < grid_sms ? (max_units < 1 ? 1 : max_units) : grid_sms;
     return launch_k_coresident(kern, want, dim3(C::kThreadsCta), dyn_smem, stream, up.pdl, num_sms, tm_x, tm_w13,
                                tm_h, tm_w2, fa, tail);
@@ -2421,6 +2516,8 @@ cudaError_t launch_grouped_gemm(const GemmProblem &p, int num_sms, cudaStream_t 
         if (p.tile_rows != 128)
             return cudaErrorInvalidValue;
         if (p.gather)   // tiled tiles would need 32 gather4 per stage: not built (see moe_forward)
+            return cudaErrorInvalidValue;
+        if (p.cta_pair && p.pair)
             return cudaErrorInvalidValue;
         if (p.cta_pair)
             return p.gated ? run_pair<true, 6>(p, num_sms, stream) : run_pair<false, 6>(p, num_sms, stream);

@@ -231,11 +231,12 @@ moe_status_t enqueue_expert_compute(const moe_problem_t &p, const void *act, con
                                     const void *W13, const void *W2, float *y_sorted, void *ws, cudaStream_t s,
                                     void *const *stage_events = nullptr, float *reduce_into = nullptr,
                                     const int32_t *gather_perm = nullptr, bool fused = false,
-                                    const MegaParams *mega = nullptr, bool y_f16 = false)
+                                    const MegaParams *mega = nullptr, bool y_f16 = false, bool pair = false)
 {
-    const Layout L = layout_of(p);
+    const moe_problem_t q = pair ? paired_problem(p) : p;   // the GEMMs' rows
+    const Layout L = layout_of(q);
     int path = 0, tile_rows = 0;
-    resolve(p, &path, &tile_rows);
+    resolve(q, &path, &tile_rows);
     const int sms = device_sm_count();
     if (sms <= 0)
         return MOE_ERR_CUDA;
@@ -244,7 +245,8 @@ moe_status_t enqueue_expert_compute(const moe_problem_t &p, const void *act, con
     g.expert_offsets = expert_offsets;
     g.err = at<int32_t>(ws, L.err);
     g.E = p.E;
-    g.cap = capacity_of(p);
+    g.cap = capacity_of(q);
+    g.pair = pair ? 1 : 0;
     g.small_m = path == MOE_PATH_SMALL_M;
     g.cta_pair = path == MOE_PATH_TILED;
     g.w_packed = p.weight_layout == MOE_WEIGHTS_PACKED;
@@ -259,7 +261,7 @@ moe_status_t enqueue_expert_compute(const moe_problem_t &p, const void *act, con
     g.gather = gather_perm != nullptr || mega != nullptr;
     g.perm = gather_perm;
     g.k = p.k;
-    g.act_rows = g.gather ? p.T_max : g.cap;
+    g.act_rows = g.gather ? q.T_max : g.cap;
     g.w = W13;
     g.out = at<void>(ws, L.h);
     g.K = p.H;
@@ -417,6 +419,18 @@ size_t workspace_header_bytes() { return kHeaderBytes; }
 
 int32_t *forward_inv(const moe_problem_t &p, void *ws) { return at<int32_t>(ws, layout_of(p).inv); }
 
+moe_problem_t paired_problem(const moe_problem_t &p)
+{
+    moe_problem_t q = p;
+    q.T_max = 2 * p.T_max;
+    q.capacity = 2 * p.capacity;
+    int path = 0, tile_rows = 0;
+    resolve(q, &path, &tile_rows);
+    if (path == MOE_PATH_TILED)   // 256-row tiles, which a few tokens do not fill
+        q.path = MOE_PATH_TILED_1CTA;
+    return q;
+}
+
 size_t route_counters_offset() { return kCountersOffset + 5 * sizeof(int32_t); }
 
 bool use_pdl(const moe_problem_t &problem)
@@ -438,19 +452,21 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
                              void *const *stage_events, const NormArgs *tail, bool dispatched, float *tail_sums)
 {
     moe_status_t st = MOE_OK;
-    const Layout L = layout_of(p);
+    const bool pair = tail != nullptr;
+    const moe_problem_t q = pair ? paired_problem(p) : p;   // p counts routed rows, q the GEMMs' rows
+    const Layout L = layout_of(q);
     const int sms = device_sm_count();
     int32_t *inv = at<int32_t>(ws, L.inv);
     void *x_sorted = at<void>(ws, L.x_sorted);
     float *y_sorted = at<float>(ws, L.y_sorted);
     auto mark = [&](int i) { return record_stage(stage_events, i, s); };
     int path = 0, tile_rows = 0;
-    resolve(p, &path, &tile_rows);
+    resolve(q, &path, &tile_rows);
     // decode-size batches (M-small, 16-row token tiles) whose dispatch tables
     // fit in shared memory: the whole call is one persistent kernel (local
     // dispatch in every CTA, both GEMMs, combine); its stage marks all fall
     // after it.
-    if (use_megakernel(p)) {
+    if (use_megakernel(q)) {
         MegaParams mp;
         mp.ids = topk_ids;
         mp.topk_w = topk_weights;
@@ -464,7 +480,8 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
         mp.tail_sums = tail_sums;
         if ((st = mark(0)) != MOE_OK)
             return st;
-        st = enqueue_expert_compute(p, x, nullptr, W13, W2, y_sorted, ws, s, nullptr, nullptr, nullptr, true, &mp);
+        st = enqueue_expert_compute(p, x, nullptr, W13, W2, y_sorted, ws, s, nullptr, nullptr, nullptr, true, &mp, false,
+                                    pair);
         for (int i = 1; st == MOE_OK && i < 6; ++i)
             st = mark(i);
         return st;
@@ -477,29 +494,30 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
     // every launch: the kernel clears them at its tail). Measured in one
     // process against two launches: -1.3% per decode step; +2% on 32-row
     // tiles, which keep two launches.
-    const bool fused_mlp = fused_mlp_of(p, path, tile_rows);
+    const bool fused_mlp = fused_mlp_of(q, path, tile_rows);
     if ((st = mark(0)) != MOE_OK)
         return st;
     if (!dispatched)
         st = cuda_status(launch_dispatch(topk_ids, d_num_tokens, p.T_max, p.k, p.E, at<int32_t>(ws, L.block_counts),
                                          at<int32_t>(ws, L.block_base), expert_offsets, perm, inv,
-                                         at<int32_t>(ws, L.err), s, use_pdl(p)));
+                                         at<int32_t>(ws, L.err), s, use_pdl(q)));
     if (st != MOE_OK || (st = mark(1)) != MOE_OK)
         return st;
     // On the M-small path the gate-up GEMM gathers its few rows per tile from x
     // itself (tile::gather4, at most 16 per stage). The tiled paths read a
     // materialised x_sorted: at 32 gather4 per 128-row stage the TMA issue rate,
     // not the data, limited the gate-up GEMM (4.5x slower on the large shape).
-    const bool fused_gather = gemm_gathers_rows(p, path, tile_rows);
+    const bool fused_gather = gemm_gathers_rows(q, path, tile_rows);
     if (!fused_gather)
-        st = cuda_status(launch_gather_rows(x, perm, expert_offsets, p.E, p.k, p.H, capacity_of(p), x_sorted, sms, s,
-                                            use_pdl(p)));
+        st = cuda_status(launch_gather_rows(x, perm, expert_offsets, p.E, p.k, p.H, capacity_of(q), x_sorted, sms, s,
+                                            use_pdl(q), pair ? 1 : 0));
     if (st != MOE_OK || (st = mark(2)) != MOE_OK)
         return st;
     // tiled paths: y between the down GEMM and the combine in fp16 (half the
     // bytes of the largest intermediate; within the output tolerance). The
     // M-small path keeps fp32 (its y is small).
-    const bool y_f16 = path != MOE_PATH_SMALL_M;
+    // Paired rows (a few tokens, 16-bit activations) keep fp32 too.
+    const bool y_f16 = path != MOE_PATH_SMALL_M && !pair;
     // A few tokens with bf16 weights, whose dispatch tables fit the fused
     // kernel's shared memory and whose gate-up units fit one wave on one SM
     // fewer (so the fused kernel starts beside the dispatch block): the fused
@@ -509,8 +527,9 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
     // and the combine's inv. Measured at one token, E=384, H=7168, I=3072, in
     // one process, outputs bit-identical: 126.6 vs 127.5 us per call; at
     // eight tokens (full grid) +1.9 us, so those keep the plain form.
-    const bool dispatch_beside = !dispatched && fused_mlp && megakernel_possible(p) && p.weight_layout != MOE_WEIGHTS_MXFP8 &&
-                                 fused_grid_sms(false, false, capacity_of(p), p.E, p.I, tile_rows, sms) < sms;
+    const bool dispatch_beside =
+        !dispatched && fused_mlp && megakernel_possible(q) && p.weight_layout != MOE_WEIGHTS_MXFP8 &&
+        fused_grid_sms(false, false, capacity_of(p), p.E, p.I, pair ? tile_rows / 2 : tile_rows, sms) < sms;
     if (dispatch_beside) {
         MegaParams mp;
         mp.ids = topk_ids;
@@ -522,17 +541,17 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
         mp.out = out;
         mp.combine_apart = true;
         st = enqueue_expert_compute(p, x, nullptr, W13, W2, y_sorted, ws, s, stage_events, nullptr, nullptr, true,
-                                    &mp);
+                                    &mp, false, pair);
     } else {
         st = enqueue_expert_compute(p, fused_gather ? x : x_sorted, expert_offsets, W13, W2, y_sorted, ws, s,
                                     stage_events, nullptr, fused_gather ? perm : nullptr, fused_mlp, nullptr,
-                                    y_f16);
+                                    y_f16, pair);
     }
     if (st != MOE_OK || (st = mark(4)) != MOE_OK)
         return st;
     if (tail)
-        return cuda_status(launch_combine_residual(y_sorted, y_f16, inv, topk_weights, *tail, p.k, parts,
-                                                   static_cast<size_t>(capacity_of(p)) * p.H, s, use_pdl(p)));
+        return cuda_status(launch_combine_residual(y_sorted, inv, topk_weights, *tail, p.k, parts,
+                                                   static_cast<size_t>(capacity_of(q)) * p.H, s, use_pdl(q)));
     st = cuda_status(launch_combine(y_sorted, y_f16, inv, topk_weights, d_num_tokens, p.T_max, p.k, p.H, out, sms,
                                     s, use_pdl(p), parts, static_cast<size_t>(capacity_of(p)) * p.H, true));
     if (st != MOE_OK)

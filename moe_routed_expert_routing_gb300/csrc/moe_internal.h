@@ -138,7 +138,8 @@ cudaError_t launch_dispatch(const int32_t *topk_ids, const int32_t *d_num_tokens
                             int32_t *perm, int32_t *inv, int32_t *err, cudaStream_t stream, bool pdl);
 
 cudaError_t launch_gather_rows(const void *x, const int32_t *perm, const int32_t *expert_offsets, int E, int k,
-                               int H, int cap, void *x_sorted, int num_sms, cudaStream_t stream, bool pdl);
+                               int H, int cap, void *x_sorted, int num_sms, cudaStream_t stream, bool pdl,
+                               int pair = 0);
 
 // ---- combine (combine.cu) ----
 // y_sorted is fp32, or fp16 when y_f16 is set (moe_forward's tiled paths).
@@ -191,6 +192,7 @@ struct GemmProblem {
     bool w_packed;            // `w` is in the access-ordered PACKED layout
     bool w_mxfp8;             // `w` is in the MXFP8 layout (codes, then scale blocks): fused kernel only
     bool out_f16;             // tiled down GEMM: y as fp16 (saturated; MOE_DEVERR_Y_RANGE if clipped)
+    int pair = 0;             // 1: paired rows (moe_layer; see GemmArgs)
     int32_t *sched = nullptr; // single-CTA grouped GEMM (M-small and tiled): two workspace counters (units
                               // handed out, CTAs at the tail), zero before the launch and left zero by it;
                               // null: units dealt round-robin
@@ -241,8 +243,9 @@ bool fused_mega_fits(int E, long long slots, bool mxfp8);
 cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t stream, bool pdl);
 
 // The end of moe_layer (combine_residual.cu): combine into an unrounded y, then
-// as launch_norm with that y; y_sorted, inv, parts as launch_combine takes them.
-cudaError_t launch_combine_residual(const void *y_sorted, bool y_f16, const int32_t *inv, const float *topk_weights,
+// as launch_norm with that y; y_sorted (of paired rows), inv (of routed rows)
+// and parts as launch_combine takes them.
+cudaError_t launch_combine_residual(const float *y_sorted, const int32_t *inv, const float *topk_weights,
                                     const NormArgs &a, int k, int parts, size_t part_stride, cudaStream_t stream,
                                     bool pdl);
 
@@ -265,7 +268,7 @@ struct RouteArgs {
     // writes the rounded rows to x_out
     int normed, x_f32, w_f32, unit_offset;
     const void *w_pre;         // null: no weight
-    void *x_out;               // [T_max, H] bf16
+    void *x_out;               // [2 * T_max, H] bf16: each row's leading part and the rest (paired rows)
     // moe_layer, at most kRouteDispatchSlots slots: moe_dispatch's tables, or null
     int32_t *expert_offsets, *perm, *inv;
     int one_kernel;            // the last CTA selects for up to 16 tokens, in the same kernel
@@ -383,7 +386,11 @@ moe_status_t validate_device();
 // What moe_forward refuses beyond its pointers and workspace: a forward form
 // or weight layout that the shape cannot take.
 moe_status_t check_forward(const moe_problem_t &problem);
-// moe_forward after its checks. With `tail`, the combine's place is taken by
+// The forward's problem when its rows are paired (moe_layer): twice the tokens,
+// on single CTAs where CTA pairs were asked for or would be taken.
+moe_problem_t paired_problem(const moe_problem_t &problem);
+// moe_forward after its checks. With `tail` (moe_layer) rows are paired: x has
+// 2 T_max rows, the workspace is paired_problem's, and the combine's place is taken by
 // launch_combine_residual, or by the end of the one-kernel form (`out` is then
 // fp32 scratch [T_max, H], tail_sums tail_sum_floats of it), and the block's
 // output goes into the residual stream as `tail` says. With `dispatched`, expert_offsets, perm

@@ -347,7 +347,8 @@ __device__ __forceinline__ float gather_logits(const RouteArgs &a, const RouteSp
     return r;
 }
 
-// The normalised row for the experts, rounded to bf16 (their MMAs' operand type).
+// The normalised row for the experts as two bf16 rows (bf16 is their MMAs'
+// operand type): the leading parts and the rest, 16 bits together.
 __device__ __forceinline__ void write_row(const RouteArgs &a, int t, float r)
 {
     for (int m0 = 8 * threadIdx.x; m0 < a.H; m0 += 4 * 8 * kFewThreads) {
@@ -368,12 +369,18 @@ __device__ __forceinline__ void write_row(const RouteArgs &a, int t, float r)
             float f[8], wp[8];
             widen8(x[i], a.x_f32, f);
             weight8(a, w[i], wp);
-            uint4 o;
-            o.x = pack_bf16(f[0] * r * wp[0], f[1] * r * wp[1]);
-            o.y = pack_bf16(f[2] * r * wp[2], f[3] * r * wp[3]);
-            o.z = pack_bf16(f[4] * r * wp[4], f[5] * r * wp[5]);
-            o.w = pack_bf16(f[6] * r * wp[6], f[7] * r * wp[7]);
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) + static_cast<size_t>(t) * a.H + m) = o;
+            uint32_t lead[4], rest[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float lo = f[2 * j] * r * wp[2 * j], hi = f[2 * j + 1] * r * wp[2 * j + 1];
+                lead[j] = pack_bf16(lo, hi);
+                const float2 taken = unpack_bf16(lead[j]);
+                rest[j] = pack_bf16(lo - taken.x, hi - taken.y);
+            }
+            uint4 *const o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) +
+                                                       2 * static_cast<size_t>(t) * a.H + m);
+            o[0] = make_uint4(lead[0], lead[1], lead[2], lead[3]);
+            o[a.H / 8] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
         }
     }
 }

@@ -78,3 +78,16 @@ def route(logits, k, score="softmax", renormalize=True, bias=None, n_group=1, to
         g = g[np.isfinite(g) & (g > 0)]
         margin[t] = g.min() if g.size else np.inf
     return ids, w * scale, margin
+
+
+def experts(v, ids, weights, W13, W2):
+    """y[t] = sum_j w[t, j] * MLP_{ids[t, j]}(v[t]) on unrounded activations; ids -1 are skipped."""
+    I = W2.shape[2]
+    y = np.zeros_like(v)
+    for e in range(W13.shape[0]):
+        t, j = np.nonzero(ids == e)
+        if len(t):
+            gu = v[t] @ W13[e].T
+            g, u = gu[:, :I], gu[:, I:]
+            y[t] += weights[t, j, None] * ((g / (1.0 + np.exp(-g)) * u) @ W2[e].T)
+    return y
