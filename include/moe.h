@@ -464,13 +464,23 @@ moe_status_t moe_layer_workspace_size(const moe_layer_problem_t *problem, size_t
  * The whole block for a few tokens (a decode step):
  *   v = h * r(h) * w_pre            the norm, unrounded
  *   ids, weights = the router on v  (as moe_route, but on v before its rounding)
- *   y = the experts on bf16(v), weighted and summed, unrounded
+ *   y = the experts on v, weighted and summed, unrounded
  *   h_out, x_next                   as moe_norm_residual, from y before its rounding
- * Arguments as in moe_norm, moe_route, moe_forward and moe_norm_residual;
+ * The experts' matrix instructions take bf16 activations; v and h go to them
+ * as two bf16 rows each, leading part and rest, so they count with 16 bits
+ * (a few tokens leave the token tiles mostly empty, so the second row costs
+ * nothing to speak of). experts.path MOE_PATH_TILED runs as
+ * MOE_PATH_TILED_1CTA. With experts.forward_form MOE_FORWARD_ONE_KERNEL the
+ * call is two kernels for up to 16 tokens (three beyond): norm and router,
+ * then all the rest; as in moe_forward its CTAs wait on one another and the
+ * form is refused for problems it does not fit. Otherwise three kernels
+ * for one or two tokens (norm, router and dispatch; the experts' two
+ * products; combine and residual), more for more. Arguments as in moe_norm, moe_route, moe_forward and moe_norm_residual;
  * w_pre, w_post and w_next follow norm.w_dtype. topk_ids, topk_weights,
  * expert_offsets and perm are outputs. More tokens than MOE_LAYER_MAX_TOKENS
  * return MOE_ERR_SHAPE: call moe_norm, moe_route, moe_forward and
- * moe_norm_residual in turn (there the router reads the rounded x).
+ * moe_norm_residual in turn (there the router and the experts read the
+ * rounded x). h_out may be h; no other buffers may overlap.
  */
 moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const void *w_pre, const void *w_router,
                        const float *bias, const void *W13, const void *W2, const void *w_post, const void *gate,

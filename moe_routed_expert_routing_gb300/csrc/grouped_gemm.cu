@@ -1106,7 +1106,8 @@ __device__ void cta_combine(const FusedArgs &fa, const int *s_inv, int T)
 // stream, and on to the next norm (as combine_residual.cu). An item is one
 // token x 4 kThreads columns, as in the combine; the row sums need all items
 // of a token, so each phase ends at the GPU-wide count `done` once more.
-struct NoTail {};
+struct NoTail {};     // moe_forward
+struct PairedRows {};  // moe_layer's kernels before combine_residual.cu: paired rows, no tail
 
 struct TailArgs {
     NormArgs n;
@@ -1228,6 +1229,8 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
 {
     using C = FusedCfg<kTileRows, kStages, kFp8>;
     constexpr int kThreads = C::kThreadsCta;
+    constexpr int kPair = std::is_same<Tail, NoTail>::value ? 0 : 1;   // paired rows (GemmArgs): fixed here, since
+                                                                       // a branch per unit cost moe_forward 0.1%
     constexpr int kASlotsRing = kFp8 ? C::kASlots : 1;
     // the whole-forward form keeps its expert tables (sized by E and T_max * k)
     // in dynamic shared memory after the stages
@@ -1307,10 +1310,10 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
             s_T = T;
     } else {
         for (int i = threadIdx.x; i <= E; i += kThreads)
-            s_off[i] = A1.expert_offsets[i] << A1.pair;
+            s_off[i] = A1.expert_offsets[i] << kPair;
     }
     __syncthreads();
-    if (kMega && A1.pair) {   // the local dispatch counts routed rows
+    if constexpr (kMega && kPair != 0) {   // the local dispatch counts routed rows
         for (int i = threadIdx.x; i <= E; i += kThreads)
             s_off[i] <<= 1;
         __syncthreads();
@@ -1370,7 +1373,7 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
             bool pre = false;
             if (!kFp8 && up && !fa.act_sorted) {
                 static_assert(kFp8 || kTileRows <= 32, "one row per lane");
-                const int prow = (t.row0 + lane) >> A1.pair;
+                const int prow = (t.row0 + lane) >> kPair;
                 const int slot = lane < t.rows && lane < kTileRows
                                      ? (kMega ? s_perm[prow] : __ldg(A1.perm + prow))
                                      : 0;
@@ -1390,13 +1393,13 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
                     }
                 }
                 if (lane < kTileRows)
-                    s_rows[lane] = token_row(slot, A1.k, t.row0 + lane, A1.pair);
+                    s_rows[lane] = token_row(slot, A1.k, t.row0 + lane, kPair);
                 __syncwarp();
             } else if (up && !fa.act_sorted) {
                 for (int i = lane; i < kTileRows; i += 32)
-                    s_rows[i] = i < t.rows ? token_row(kMega ? s_perm[(t.row0 + i) >> A1.pair]
-                                                             : __ldg(A1.perm + ((t.row0 + i) >> A1.pair)),
-                                                       A1.k, t.row0 + i, A1.pair)
+                    s_rows[i] = i < t.rows ? token_row(kMega ? s_perm[(t.row0 + i) >> kPair]
+                                                             : __ldg(A1.perm + ((t.row0 + i) >> kPair)),
+                                                       A1.k, t.row0 + i, kPair)
                                            : 0;
                 __syncwarp();
             }
@@ -1713,7 +1716,7 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
                 if (up)
                     tmem_ld_32x32b_x16(t_row + kTileRows + c, w);
                 tmem_wait_ld();
-                if (up && A1.pair) {
+                if (up && kPair) {
                     small_pair_epilogue(g, w, A1, t.row0 + c, t.rows - c, col);
                     continue;
                 }
@@ -2547,6 +2550,21 @@ cudaError_t launch_grouped_gemm(const GemmProblem &p, int num_sms, cudaStream_t 
 
 namespace {
 
+// moe_layer: the two GEMMs on paired rows.
+template <int kTileRows, int kStages, bool kFp8>
+cudaError_t run_fused_paired(const GemmProblem &up, const GemmProblem &down, int32_t *ready, int32_t *counters,
+                             int num_sms, cudaStream_t stream)
+{
+    return down.split_k == 4
+               ? run_fused<kTileRows, kStages, 4, false, kFp8, PairedRows>(up, down, ready, counters, num_sms, stream,
+                                                                          nullptr)
+           : down.split_k == 2
+               ? run_fused<kTileRows, kStages, 2, false, kFp8, PairedRows>(up, down, ready, counters, num_sms, stream,
+                                                                          nullptr)
+               : run_fused<kTileRows, kStages, 1, false, kFp8, PairedRows>(up, down, ready, counters, num_sms, stream,
+                                                                          nullptr);
+}
+
 // moe_layer's form of the whole-forward kernel: the tail in place of the combine.
 template <int kStages, bool kFp8>
 cudaError_t run_fused_tail(const GemmProblem &up, const GemmProblem &down, int32_t *ready, int32_t *counters,
@@ -2577,7 +2595,7 @@ cudaError_t launch_fused_small(const GemmProblem &up, const GemmProblem &down, i
                 mega->T_max < 1)
              : (up.gather && !up.perm))
         return cudaErrorInvalidValue;
-    if (up.w_mxfp8 != down.w_mxfp8)
+    if (up.w_mxfp8 != down.w_mxfp8 || (mega && (mega->tail != nullptr) != (up.pair != 0)))
         return cudaErrorInvalidValue;
     if (up.w_mxfp8) {
         // MXFP8 weights: every M-small tile height (this kernel is their only GEMM)
@@ -2593,14 +2611,24 @@ cudaError_t launch_fused_small(const GemmProblem &up, const GemmProblem &down, i
                 return down.split_k == 4   ? run_fused<16, 5, 4, true, true>(up, down, ready, counters, num_sms, stream, mega)
                        : down.split_k == 2 ? run_fused<16, 5, 2, true, true>(up, down, ready, counters, num_sms, stream, mega)
                                            : run_fused<16, 5, 1, true, true>(up, down, ready, counters, num_sms, stream, mega);
+            if (up.pair)
+                return run_fused_paired<16, 5, true>(up, down, ready, counters, num_sms, stream);
             return down.split_k == 4   ? run_fused<16, 5, 4, false, true>(up, down, ready, counters, num_sms, stream, nullptr)
                    : down.split_k == 2 ? run_fused<16, 5, 2, false, true>(up, down, ready, counters, num_sms, stream, nullptr)
                                        : run_fused<16, 5, 1, false, true>(up, down, ready, counters, num_sms, stream, nullptr);
         case 32:
+            if (up.pair)
+                return down.split_k == 1
+                           ? run_fused<32, 4, 1, false, true, PairedRows>(up, down, ready, counters, num_sms, stream, nullptr)
+                           : cudaErrorInvalidValue;
             return down.split_k == 1
                        ? run_fused<32, 4, 1, false, true>(up, down, ready, counters, num_sms, stream, nullptr)
                        : cudaErrorInvalidValue;
         case 64:
+            if (up.pair)
+                return down.split_k == 1
+                           ? run_fused<64, 3, 1, false, true, PairedRows>(up, down, ready, counters, num_sms, stream, nullptr)
+                           : cudaErrorInvalidValue;
             return down.split_k == 1
                        ? run_fused<64, 3, 1, false, true>(up, down, ready, counters, num_sms, stream, nullptr)
                        : cudaErrorInvalidValue;
@@ -2620,6 +2648,8 @@ cudaError_t launch_fused_small(const GemmProblem &up, const GemmProblem &down, i
         return down.split_k == 4   ? run_fused<16, 6, 4, true, false>(up, down, ready, counters, num_sms, stream, mega)
                : down.split_k == 2 ? run_fused<16, 6, 2, true, false>(up, down, ready, counters, num_sms, stream, mega)
                                    : run_fused<16, 6, 1, true, false>(up, down, ready, counters, num_sms, stream, mega);
+    if (up.pair)
+        return run_fused_paired<16, 6, false>(up, down, ready, counters, num_sms, stream);
     return down.split_k == 4   ? run_fused<16, 6, 4, false, false>(up, down, ready, counters, num_sms, stream, nullptr)
            : down.split_k == 2 ? run_fused<16, 6, 2, false, false>(up, down, ready, counters, num_sms, stream, nullptr)
                                : run_fused<16, 6, 1, false, false>(up, down, ready, counters, num_sms, stream, nullptr);

@@ -528,8 +528,8 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
     // one process, outputs bit-identical: 126.6 vs 127.5 us per call; at
     // eight tokens (full grid) +1.9 us, so those keep the plain form.
     const bool dispatch_beside =
-        !dispatched && fused_mlp && megakernel_possible(q) && p.weight_layout != MOE_WEIGHTS_MXFP8 &&
-        fused_grid_sms(false, false, capacity_of(p), p.E, p.I, pair ? tile_rows / 2 : tile_rows, sms) < sms;
+        !dispatched && !pair && fused_mlp && megakernel_possible(q) && p.weight_layout != MOE_WEIGHTS_MXFP8 &&
+        fused_grid_sms(false, false, capacity_of(p), p.E, p.I, tile_rows, sms) < sms;
     if (dispatch_beside) {
         MegaParams mp;
         mp.ids = topk_ids;
@@ -541,7 +541,7 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
         mp.out = out;
         mp.combine_apart = true;
         st = enqueue_expert_compute(p, x, nullptr, W13, W2, y_sorted, ws, s, stage_events, nullptr, nullptr, true,
-                                    &mp, false, pair);
+                                    &mp);
     } else {
         st = enqueue_expert_compute(p, fused_gather ? x : x_sorted, expert_offsets, W13, W2, y_sorted, ws, s,
                                     stage_events, nullptr, fused_gather ? perm : nullptr, fused_mlp, nullptr,
