@@ -260,7 +260,7 @@ __device__ __forceinline__ void select_token(const RouteArgs &a, int t, const fl
         kept = kept_groups(a, s_key);
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if (!((kept >> ((lane + 32 * i) / gs)) & 1u))
+            if (lane + 32 * i >= a.E || !((kept >> ((lane + 32 * i) / gs)) & 1u))
                 v[i] = -INFINITY;
     }
     float best = -INFINITY;

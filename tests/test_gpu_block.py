@@ -260,6 +260,8 @@ def test_route_real_logits(B, T, E, k, H):
     (150, 64, 4, 192, "softmax", 1, 1, 1, True),
     (19, 36, 3, 64, "sigmoid", 4, 1, 2, False),
     (700, 384, 8, 256, "sigmoid", 2, 1, 1, True),
+    (160, 32, 5, 64, "softmax", 32, 7, 1, False),
+    (12, 30, 2, 64, "softmax", 10, 3, 2, True),
 ])
 def test_route_groups_and_bias(B, T, E, k, H, score, groups, keep, top, bias):
     g = gen(E * 7 + T)
@@ -478,6 +480,9 @@ LAYERS = [
     dict(T=100, E=24, k=2, H=320, I=256, gate=2),
     dict(T=128, E=8, k=2, H=256, I=512, post=False),
     dict(T=128, E=1024, k=2, H=128, I=64),
+    dict(T=3, E=4, k=2, H=16384, I=64, gate=1),
+    dict(T=9, E=32, k=3, H=8256, I=128, h="fp32", score=1),
+    dict(T=40, E=300, k=64, H=64, I=64),
 ]
 
 
@@ -534,6 +539,36 @@ def test_layer_in_place_and_device_token_count_in_a_graph(B):
     o = c.run(h_out=c.h)               # in place
     assert torch.equal(o["h"], full["h"]) and torch.equal(o["x_next"], full["x_next"])
     assert not torch.equal(h0, c.h)
+
+
+@pytest.mark.parametrize("T,form", [(1, 0), (2, 0), (3, 0), (2, 2)])
+def test_layer_device_token_count_of_the_smallest(B, T, form):
+    c = LayerCase(B, T=T, E=32, k=4, H=256, I=128, form=form)
+    full = c.run()
+    c.verify(full)
+    for n in range(T + 1):
+        o = c.run(T_dev=n)
+        for key, fill in (("h", 7.0), ("x_next", 7.0), ("ids", -9), ("weights", -9.0)):
+            assert torch.equal(o[key][:n], full[key][:n]) and (o[key][n:] == fill).all(), (key, n)
+        off = o["offsets"].cpu().numpy()
+        assert off[0] == 0 and off[-1] == n * 4 and (np.diff(off) >= 0).all()
+    assert B.moe_last_device_error(c.ws) == 0
+
+
+@pytest.mark.parametrize("T,form", [(2, 0), (6, 0), (6, 2), (40, 0)])
+def test_layer_with_a_row_of_nan(B, T, form):
+    """A NaN row is routed nowhere, sets the error bit and leaves the other rows as they are."""
+    c = LayerCase(B, T=T, E=64, k=4, H=256, I=128, form=form)
+    good = c.run()
+    assert B.moe_last_device_error(c.ws) == 0
+    c.h[1] = float("nan")
+    o = c.run()
+    assert B.moe_last_device_error(c.ws) == B.MOE_DEVERR_BAD_LOGIT
+    rest = [t for t in range(T) if t != 1]
+    assert (o["ids"][1] == -1).all() and (o["weights"][1] == 0).all() and torch.isnan(o["h"][1].float()).all()
+    for key in ("ids", "weights", "h", "x_next"):
+        assert torch.equal(o[key][rest], good[key][rest]), key
+    assert int(o["offsets"][-1]) == (T - 1) * 4
 
 
 def test_layer_matches_its_pieces(B):
