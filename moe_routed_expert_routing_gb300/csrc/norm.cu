@@ -163,27 +163,22 @@ struct Unit {
         }
     }
 
-    // f *= s * (norm weight of the columns from m on)
-    static __device__ __forceinline__ void apply_norm(const NormArgs &a, const void *w, int m, float s,
-                                                      Pair (&f)[kPairs])
+    // c *= the norm weight w' of the columns from m on (w null: 1)
+    static __device__ __forceinline__ void times_weight(const NormArgs &a, const void *w, int m, Pair (&c)[kPairs])
     {
-        const Pair s2 = pair(s, s);
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i)
-            f[i] = mul2(f[i], s2);
         if (!w)
             return;
-        Pair c[kPairs];
-        channel(w, a.w_f32, m, c);
+        Pair v[kPairs];
+        channel(w, a.w_f32, m, v);
         if (a.unit_offset) {
             const Pair one = pair(1.f, 1.f);
 #pragma unroll
             for (int i = 0; i < kPairs; ++i)
-                c[i] = add2(c[i], one);
+                v[i] = add2(v[i], one);
         }
 #pragma unroll
         for (int i = 0; i < kPairs; ++i)
-            f[i] = mul2(f[i], c[i]);
+            c[i] = mul2(c[i], v[i]);
     }
 };
 
@@ -210,13 +205,14 @@ __device__ __forceinline__ float row_sum(Pair q, int tpr, float *s)
     return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// Blocks of kBlock threads that share an SM, by the columns a thread holds: a
-// row's values and the next row's raw bytes take 50 to 128 registers.
+// Blocks of kBlock threads that share an SM, by the columns a thread holds.
 template <bool kF32, int kV, bool kRes, int kBlock>
 struct Plan {
     static constexpr int kHeld = kV * Unit<kF32>::kCols;
     static constexpr bool kAhead = kHeld <= 32;   // the next row in registers too
-    static constexpr int kPerSm = kBlock == 256 ? (kHeld <= 16 ? (kRes ? 3 : 4) : 2) : (kHeld <= 16 && !kRes ? 2 : 1);
+    static constexpr bool kKeep = kHeld <= 16;    // and the per-channel factors
+    static constexpr int kPerSm =
+        kBlock == 256 ? (kHeld <= 8 ? (kRes ? 3 : 4) : (kHeld <= 16 ? (kRes ? 2 : 3) : 2)) : (kHeld <= 16 && !kRes ? 2 : 1);
 };
 
 // kV units per thread; kRes: moe_norm_residual. tpr threads per row.
@@ -256,6 +252,40 @@ __global__ void __launch_bounds__(kBlock, Plan<kF32, kV, kRes, kBlock>::kPerSm)
         if constexpr (kRes)
             y[v] = typename U::Half{};
     }
+    // per-channel factors: of y, s * w_post' * channel gate; of the normed row, w_next'
+    auto factors_y = [&](int v, Pair(&c)[kPairs]) {
+        const int m = col0 + v * tpr * kCols;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            c[i] = pair(a.scale, a.scale);
+        if (a.norm_block)
+            U::times_weight(a, a.w_post, m, c);
+        if (a.gate_kind == MOE_GATE_CHANNEL) {
+            Pair g[kPairs];
+            U::channel(a.gate, a.w_f32, m, g);
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                c[i] = mul2(c[i], g[i]);
+        }
+    };
+    auto factors_x = [&](int v, Pair(&c)[kPairs]) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            c[i] = pair(1.f, 1.f);
+        U::times_weight(a, a.w_next, col0 + v * tpr * kCols, c);
+    };
+    constexpr bool kKeep = Plan<kF32, kV, kRes, kBlock>::kKeep;
+    Pair keep_y[kKeep && kRes ? kV : 1][kPairs], keep_x[kKeep ? kV : 1][kPairs];
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+            if (on[v]) {
+                if constexpr (kRes)
+                    factors_y(v, keep_y[v]);
+                if (a.x)
+                    factors_x(v, keep_x[v]);
+            }
+    }
     auto load = [&]() {
 #pragma unroll
         for (int v = 0; v < kV; ++v)
@@ -278,6 +308,7 @@ __global__ void __launch_bounds__(kBlock, Plan<kF32, kV, kRes, kBlock>::kPerSm)
         if constexpr (kRes) {
             Pair n[kV][kPairs];
             Pair q = 0ull;
+            float r = 1.f;       // what a row's y is multiplied by
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
                 U::pairs(h[v], f[v]);
@@ -291,34 +322,35 @@ __global__ void __launch_bounds__(kBlock, Plan<kF32, kV, kRes, kBlock>::kPerSm)
 #pragma unroll
                     for (int i = 0; i < kPairs; ++i)
                         q = fma2(n[v][i], n[v][i], q);
-                const float r = rsqrtf(fmaf(row_sum(q, tpr, s_sum[0]), inv_H, a.eps));
-#pragma unroll
-                for (int v = 0; v < kV; ++v)
-                    if (on[v])
-                        U::apply_norm(a, a.w_post, col0 + v * tpr * kCols, r, n[v]);
+                r = rsqrtf(fmaf(row_sum(q, tpr, s_sum[0]), inv_H, a.eps));
             }
             if (row) {
-                const float s = (a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float *>(a.gate)[t] : 1.f) * a.scale;
-                const Pair s2 = pair(s, s);
+                if (a.gate_kind == MOE_GATE_TOKEN)
+                    r *= static_cast<const float *>(a.gate)[t];
+                const Pair r2 = pair(r, r);
 #pragma unroll
                 for (int v = 0; v < kV; ++v) {
                     const int m = col0 + v * tpr * kCols;
                     if (!on[v])
                         continue;
-                    if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_ELEMENT) {
-                        Pair c[kPairs];
-                        if (a.gate_kind == MOE_GATE_CHANNEL)
-                            U::channel(a.gate, a.w_f32, m, c);
-                        else
-                            U::half_pairs(U::load_half(static_cast<const __nv_bfloat16 *>(a.gate) + t * a.gate_stride + m),
-                                          c);
+                    Pair c[kPairs];
+                    if constexpr (kKeep) {
 #pragma unroll
                         for (int i = 0; i < kPairs; ++i)
-                            n[v][i] = mul2(n[v][i], c[i]);
+                            c[i] = keep_y[v][i];
+                    } else {
+                        factors_y(v, c);
+                    }
+                    if (a.gate_kind == MOE_GATE_ELEMENT) {
+                        Pair g[kPairs];
+                        U::half_pairs(U::load_half(static_cast<const __nv_bfloat16 *>(a.gate) + t * a.gate_stride + m), g);
+#pragma unroll
+                        for (int i = 0; i < kPairs; ++i)
+                            c[i] = mul2(c[i], g[i]);
                     }
 #pragma unroll
                     for (int i = 0; i < kPairs; ++i)
-                        f[v][i] = fma2(s2, n[v][i], f[v][i]);
+                        f[v][i] = fma2(mul2(n[v][i], r2), c[i], f[v][i]);
                     U::store(static_cast<char *>(a.h_out) + (t * a.out_stride + m) * kBytes, f[v]);
                 }
             }
@@ -347,7 +379,18 @@ __global__ void __launch_bounds__(kBlock, Plan<kF32, kV, kRes, kBlock>::kPerSm)
                 const int m = col0 + v * tpr * kCols;
                 if (!on[v])
                     continue;
-                U::apply_norm(a, a.w_next, m, r, f[v]);
+                Pair c[kPairs];
+                if constexpr (kKeep) {
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i)
+                        c[i] = keep_x[v][i];
+                } else {
+                    factors_x(v, c);
+                }
+                const Pair r2 = pair(r, r);
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i)
+                    f[v][i] = mul2(mul2(f[v][i], r2), c[i]);
                 U::store_half(static_cast<__nv_bfloat16 *>(a.x) + t * a.x_stride + m, f[v]);
             }
         }
