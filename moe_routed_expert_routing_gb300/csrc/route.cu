@@ -44,6 +44,7 @@ namespace {
 // ------------------------------------------------------------ many tokens
 
 constexpr int kSelectWarps = 4;
+constexpr int kDryBlocks = 608;
 
 // One instance per 128, 256, 512 or 1024 experts: with the registers of the
 // largest only a few warps fit on an SM.
@@ -53,13 +54,30 @@ __global__ void __launch_bounds__(32 * kSelectWarps) select_kernel(const __grid_
 {
     extern __shared__ float s_keys[];   // [kSelectWarps][E], with groups only
     __shared__ SelectWarp s_warp[kSelectWarps];
-    pdl_wait();
-    pdl_trigger();
-    const int T = token_count(a.d_num_tokens, a.T_max);
+    __shared__ float s_dry[32 * kPer];
     const int warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kSelectWarps + warp;
-    if (t < T)
-        select_token<kPer>(a, t, logits + static_cast<size_t>(t) * a.E, s_keys + warp * a.E, s_warp[warp]);
+    // The first blocks sit on the SMs while the logits are still computed: they
+    // run once over made-up logits (falling, so that few reach the bound) and
+    // store nothing, which brings the code into the instruction caches (T=2048,
+    // E=384 22.9 against 24.2 us; T=8192, E=128, where most blocks come later,
+    // 24.8 against 24.9).
+    const bool early = a.k <= 32 && blockIdx.x < kDryBlocks;
+    for (int i = threadIdx.x; early && i < 32 * kPer; i += 32 * kSelectWarps)
+        s_dry[i] = -0.125f * i;
+    __syncthreads();
+#pragma unroll 1
+    for (int pass = early ? 0 : 1; pass < 2; ++pass) {
+        if (pass == 1) {
+            pdl_wait();
+            pdl_trigger();
+            if (t >= token_count(a.d_num_tokens, a.T_max))
+                break;
+        }
+        const float *l = pass == 0 ? s_dry : logits + static_cast<size_t>(t) * a.E;
+        select_token<kPer>(a, t, l, s_keys + warp * a.E, s_warp[warp], pass == 1);
+        __syncwarp();
+    }
 }
 
 template <int kPer>

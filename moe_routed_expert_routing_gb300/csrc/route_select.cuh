@@ -84,7 +84,7 @@ __device__ __forceinline__ bool needs_softmax(const RouteArgs &a)
 // them (id -1: none) with their places. n: how many were found; places from n
 // on get id -1 and weight 0.
 __device__ __forceinline__ void store_choice(const RouteArgs &a, int t, const int (&id)[2], const int (&place)[2],
-                                             const float (&l)[2], int n, float mx, float sum)
+                                             const float (&l)[2], int n, float mx, float sum, bool store = true)
 {
     float w[2], norm = 1.f;
     if (a.renormalize) {
@@ -107,6 +107,8 @@ __device__ __forceinline__ void store_choice(const RouteArgs &a, int t, const in
         for (int q = 0; q < 2; ++q)
             w[q] = id[q] >= 0 ? score_of(a, l[q], mx, sum) : 0.f;
     }
+    if (!store)
+        return;
     int32_t *ids = a.ids + static_cast<size_t>(t) * a.k;
     float *weights = a.weights + static_cast<size_t>(t) * a.k;
 #pragma unroll
@@ -199,6 +201,7 @@ struct __align__(8) SelectWarp {
 
 // One warp selects for one token whose logits lie in logits[E]; lane i holds
 // experts i, i + 32, ... s_key: E floats of scratch, used with groups only.
+// store: false for a run whose result is not wanted (see select_kernel).
 //
 // k rounds of a warp-wide maximum over all keys would be k passes over the
 // lane's registers. k rounds over the lanes' own maxima give a lower bound of
@@ -208,7 +211,8 @@ struct __align__(8) SelectWarp {
 // other code, and unrolled over four tokens it waited for instruction fetches
 // (12,000 cycles for the four, no faster than one after the other).
 template <int kPer>
-__device__ __forceinline__ void select_token(const RouteArgs &a, int t, const float *logits, float *s_key, SelectWarp &s)
+__device__ __forceinline__ void select_token(const RouteArgs &a, int t, const float *logits, float *s_key, SelectWarp &s,
+                                             bool store = true)
 {
     const int lane = threadIdx.x & 31;
     float v[kPer];
@@ -287,7 +291,8 @@ __device__ __forceinline__ void select_token(const RouteArgs &a, int t, const fl
         n += __popc(b);
     }
     if (n > 32 || a.k > 32) {
-        select_by_rounds(a, t, logits, kept, mx, sum);
+        if (store)
+            select_by_rounds(a, t, logits, kept, mx, sum);
         return;
     }
     __syncwarp();
@@ -303,7 +308,7 @@ __device__ __forceinline__ void select_token(const RouteArgs &a, int t, const fl
         id[0] = static_cast<int>(~static_cast<uint32_t>(mine));
         l[0] = keyed_by_score(a) ? logits[id[0]] : key_value(static_cast<uint32_t>(mine >> 32));
     }
-    store_choice(a, t, id, place, l, min(n, a.k), mx, sum);
+    store_choice(a, t, id, place, l, min(n, a.k), mx, sum, store);
 }
 
 }  // namespace

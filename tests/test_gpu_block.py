@@ -262,6 +262,7 @@ def test_route_real_logits(B, T, E, k, H):
     (700, 384, 8, 256, "sigmoid", 2, 1, 1, True),
     (160, 32, 5, 64, "softmax", 32, 7, 1, False),
     (12, 30, 2, 64, "softmax", 10, 3, 2, True),
+    (260, 512, 12, 128, "sigmoid", 16, 6, 1, True),
 ])
 def test_route_groups_and_bias(B, T, E, k, H, score, groups, keep, top, bias):
     g = gen(E * 7 + T)
@@ -297,6 +298,20 @@ def test_route_masked_experts(B, T):
                 check(wt[torch.from_numpy(sure).cuda()], want_w[sure], np.abs(want_w[sure]) * 1e-5 + 1e-37, "weights")
                 assert (ids.cpu().numpy()[:, min(on, k):] == -1).all() and (wt[:, min(on, k):] == 0).all()
                 assert B.moe_last_device_error(ws) == 0
+
+
+def test_route_bias_that_makes_all_keys_equal_leaves_nothing_behind(B):
+    """Many tokens, keys equal by the bias: the lowest experts, for every token and in every repeat."""
+    T, E, k, H = 300, 200, 8, 64
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((E, H), dtype=torch.bfloat16, device="cuda")
+    bias = torch.full((E,), 3.0, device="cuda")
+    p = B.RouterProblem.make(T, E, k, H, score=1)
+    ws = None
+    for _ in range(3):
+        ids, wt, ws = run_route(B, p, x, w, bias=bias, ws=ws)
+        assert (ids == torch.arange(k, dtype=torch.int32, device="cuda")).all()
+        assert (wt - 1.0 / k).abs().max() < 1e-6
 
 
 @pytest.mark.parametrize("T", [3, 300])
