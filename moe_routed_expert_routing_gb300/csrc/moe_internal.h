@@ -277,10 +277,10 @@ struct RouteArgs {
 };
 
 // The few-token kernel's split of [T_max, E, H]: units of 16 experts x one
-// slice of H x up to 32 tokens, about one per SM. Narrow units: the layer of 13
-// tokens of E=64, H=2048 took 81.8 us with two units of 8 tokens and 83.2 with
-// one of 16, the one of 64 tokens of E=128, H=4096 676 us in units of 16 or 32
-// and 681 in one of 64.
+// slice of H x up to 32 tokens, about one per SM. The narrowest units that
+// leave H in four slices or more, else the widest: 32 tokens of E=128, H=4096
+// 6.4 us in units of 8 tokens, 7.3 in one of 32; 24 tokens of E=384, H=7168
+// 9.3 and 8.2; 61 of E=256, H=7168 11.9 and 9.4.
 struct RouteSplit {
     int tiles;                 // 8-token tiles of a unit: 1, 2 or 4
     int chunks, groups, slices;
@@ -288,24 +288,27 @@ struct RouteSplit {
 };
 
 // moe_route takes the few-token kernels up to here, then the tensor-core ones
-// (route_gemm.cu): 7.8 us against 12.2 at 16 tokens (E=256, H=7168), 10.8
-// against 9.9 at 32 (E=128, H=4096). moe_layer, whose router reads unrounded
-// rows, takes them always.
-constexpr int kRouteFewTokens = 16;
+// (route_gemm.cu). 128 tokens of E=128, H=4096 7.8 us against 10.2, 96 of E=256,
+// H=7168 10.3 against 12.4, 190 of E=128 9.0 against 10.2; 256 of E=256 17.4
+// against 12.5. moe_layer, whose router reads unrounded rows, takes them always.
+constexpr int kRouteFewTokens = 192;
 constexpr int kRouteJoinTokens = 2;
-constexpr int kRouteBlockTokens = 152;      // one block per SM
 constexpr int kRouteDispatchSlots = 128;
 
 inline RouteSplit route_split(int T_max, int E, int H, bool one_kernel = false)
 {
     RouteSplit r;
-    r.tiles = T_max <= 16 ? 1 : (T_max <= 64 ? 2 : 4);
-    r.chunks = (T_max + 8 * r.tiles - 1) / (8 * r.tiles);
     r.groups = (E + 15) / 16;
+    const int eights = (T_max + 7) / 8;
+    r.tiles = 1;
+    while (r.tiles < 4 && r.tiles < eights && !(one_kernel && T_max <= 16) &&
+           r.groups * ((eights + r.tiles - 1) / r.tiles) > 152 / 4)
+        r.tiles *= 2;
+    r.chunks = (eights + r.tiles - 1) / r.tiles;
     const int blocks = H / 64;
     const int want = 152 / (r.groups * r.chunks);
     r.slices = want < 1 ? 1 : (want < blocks ? want : blocks);
-    r.join = T_max <= (one_kernel ? 16 : kRouteJoinTokens);
+    r.join = T_max <= (one_kernel ? 16 : kRouteJoinTokens);   // tiles is 1 then
     return r;
 }
 

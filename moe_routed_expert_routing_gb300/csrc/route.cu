@@ -3,7 +3,7 @@
 //
 //   logits[t, e] = sum_m x[t, m] w[e, m]        (x = h * r(h) * w_pre in moe_layer)
 //
-// Few tokens (moe_route up to 16, moe_layer): the router's weights are the bytes that matter
+// Few tokens (moe_route up to 192, moe_layer): the router's weights are the bytes that matter
 // (5.5 MB at E=384, H=7168) and must come from every SM at once, so a unit is
 // 16 experts x a slice of H, about one unit per SM, and the slices' partial
 // logits meet in the workspace. For one or two tokens the last CTA to get
@@ -672,9 +672,8 @@ cudaError_t launch_few(const RouteArgs &a, const RouteSplit &sp, cudaStream_t st
 {
     const bool exact16 = !a.x_f32 && !a.unit_offset && (!a.w_pre || !a.w_f32);
     auto kern = exact16 ? route_few_kernel<kTiles, 2> : route_few_kernel<kTiles, 3>;
-    if constexpr (kTiles == 1)    // moe_route: at most 16 tokens
-        if (!a.normed)
-            kern = route_few_kernel<kTiles, 1>;
+    if (!a.normed)
+        kern = route_few_kernel<kTiles, 1>;
     const cudaError_t e =
         launch_k(kern, dim3(sp.groups * sp.slices * sp.chunks), dim3(kFewThreads), 0, stream, pdl, a, sp);
     if (e != cudaSuccess || sp.join)
@@ -702,17 +701,6 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl)
     const cudaError_t e = launch_route_gemm(a, logits, stream, pdl);
     if (e != cudaSuccess)
         return e;
-    // few tokens chosen by scores or groups: a block each (a warp would pass
-    // over the scores alone: 61 tokens of E=256 in 8 groups 14.7 against 16.0
-    // us; chosen by logits a warp is faster, 12.3 against 13.6)
-    if (a.T_max <= kRouteBlockTokens && (a.bias || a.n_group > 1)) {
-        RouteArgs b = a;
-        b.part = logits;
-        b.logits = nullptr;
-        RouteSplit one = {};
-        one.slices = 1;
-        return launch_k(route_finish_kernel<false>, dim3(a.T_max), dim3(kFewThreads), 0, stream, pdl, b, one);
-    }
     if (a.E <= 128)
         return launch_select<4>(a, logits, stream, pdl);
     if (a.E <= 256)

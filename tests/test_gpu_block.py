@@ -193,7 +193,8 @@ def run_route(B, p, x, w, bias=None, logits=None, T_dev=None, ws=None):
 
 ROUTE_SHAPES = [(1, 1, 1, 64), (1, 384, 6, 7168), (2, 7, 7, 128), (9, 33, 4, 192), (31, 130, 8, 2880), (64, 256, 8, 1024),
                 (65, 128, 64, 512), (100, 1000, 10, 448), (129, 384, 6, 1536), (300, 512, 8, 512), (513, 96, 2, 4096),
-                (300, 128, 64, 128), (200, 200, 33, 64),                 (1025, 1024, 16, 256), (2500, 64, 8, 320)]
+                (300, 128, 64, 128), (200, 200, 33, 64), (192, 48, 3, 128), (193, 48, 3, 128), (150, 1024, 4, 64),
+                                (1025, 1024, 16, 256), (2500, 64, 8, 320)]
 
 
 @pytest.mark.parametrize("T,E,k,H", ROUTE_SHAPES)
@@ -279,7 +280,7 @@ def test_route_groups_and_bias(B, T, E, k, H, score, groups, keep, top, bias):
     check(wt[torch.from_numpy(sure).cuda()], want_w[sure], np.abs(want_w[sure]) * 1e-5 + 1e-37, "weights")
 
 
-@pytest.mark.parametrize("T", [1, 5, 200])
+@pytest.mark.parametrize("T", [1, 5, 120, 200])
 def test_route_masked_experts(B, T):
     """Experts switched off by a bias of -inf, down to fewer than k, then none."""
     E, k, H = 40, 6, 128
