@@ -199,6 +199,7 @@ class Profile(ctypes.Structure):
 
 _lib = None
 _vp = ctypes.c_void_p
+_Tensor = torch.Tensor
 _P = ctypes.POINTER(Problem)
 
 
@@ -298,11 +299,14 @@ def _need(t, name: str, dtype, numel: int):
 
 
 def _dev(t, name: str, dtype, numel: int) -> int | None:
-    """_need and _ptr in one: the checked pointer."""
-    if t is None or isinstance(t, int):
-        return t
-    if t.is_cuda and t.dtype == dtype and t.numel() >= numel and t.is_contiguous():
+    """_need and _ptr in one: the checked pointer. A decode step's norm is a
+    2.5 us kernel, so the usual tensor passes in one expression."""
+    if t is None:
+        return None
+    if t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.numel() >= numel and t.is_contiguous():
         return t.data_ptr()
+    if isinstance(t, int):
+        return t
     _need(t, name, dtype, numel)
     return _ptr(t)
 
@@ -310,10 +314,15 @@ def _dev(t, name: str, dtype, numel: int) -> int | None:
 def _need_rows(t, name: str, dtype, rows: int, cols: int, stride: int) -> int | None:
     """Pointer of a [rows, cols] tensor whose rows lie ``stride`` elements
     apart (0 = cols, contiguous), checked as _need does."""
-    if t is None or isinstance(t, int):
+    if stride == 0 or stride == cols:
+        if t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.numel() >= rows * cols and t.is_contiguous():
+            return t.data_ptr()
+        if t is None or isinstance(t, int):
+            return t
+        if t.is_contiguous():
+            return _dev(t, name, dtype, rows * cols)
+    elif t is None or isinstance(t, int):
         return t
-    if (stride == 0 or stride == cols) and t.is_contiguous():
-        return _dev(t, name, dtype, rows * cols)
     stride = stride or cols
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (device memory), not on {t.device}")
@@ -337,10 +346,14 @@ def _need_weights(problem, W13, W2):
         _need(W2, "W2", torch.bfloat16, problem.E * problem.H * problem.I)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (   # absent from a CPU-only PyTorch
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         # the handle alone: a torch.cuda.Stream object takes 2.6 us to build, as long as a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -495,9 +508,12 @@ def moe_norm(problem: NormProblem, h, w, x, d_num_tokens=None, stream=None):
     """x = norm(h) * w; see include/moe.h."""
     p = problem
     T, H = p.T_max, p.H
-    _check(load_library().moe_norm(ctypes.byref(p), _need_rows(h, "h", p.h_torch, T, H, p.h_stride),
-                                   _dev(w, "w", p.w_torch, H), _dev(d_num_tokens, "d_num_tokens", torch.int32, 1),
-                                   _need_rows(x, "x", torch.bfloat16, T, H, p.x_stride), _stream(stream)), "moe_norm")
+    status = (_lib or load_library()).moe_norm(
+        ctypes.byref(p), _need_rows(h, "h", p.h_torch, T, H, p.h_stride), _dev(w, "w", p.w_torch, H),
+        _dev(d_num_tokens, "d_num_tokens", torch.int32, 1), _need_rows(x, "x", torch.bfloat16, T, H, p.x_stride),
+        _stream(stream))
+    if status:
+        _check(status, "moe_norm")
 
 
 def _need_residual(p: NormProblem, h, w_post, gate, w_next, h_out, x_next):
