@@ -469,7 +469,8 @@ moe_status_t moe_layer_workspace_size(const moe_layer_problem_t *problem, size_t
  * The experts' matrix instructions take bf16 activations; v and h go to them
  * as two bf16 rows each, leading part and rest, so they count with 16 bits
  * (a few tokens leave the token tiles mostly empty, so the second row costs
- * nothing to speak of). experts.path MOE_PATH_TILED runs as
+ * nothing to speak of). experts.path AUTO picks the token tiles for that
+ * (16 or 32 rows, or the tiled path's 128); MOE_PATH_TILED runs as
  * MOE_PATH_TILED_1CTA. With experts.forward_form MOE_FORWARD_ONE_KERNEL the
  * call is two kernels for up to 16 tokens (three beyond): norm and router,
  * then all the rest; as in moe_forward its CTAs wait on one another and the

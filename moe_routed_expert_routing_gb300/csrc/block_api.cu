@@ -140,24 +140,22 @@ struct LayerLayout {
     size_t forward, x, part, y, sums, total;
 };
 
-moe_status_t layer_layout(const moe_layer_problem_t &p, LayerLayout *L)
+LayerLayout layer_layout(const moe_layer_problem_t &p)
 {
-    const moe_problem_t q = paired_problem(p.experts);
-    const moe_status_t st = moe_workspace_size(&q, &L->forward);
-    if (st != MOE_OK)
-        return st;
+    LayerLayout L = {};
+    L.forward = forward_workspace_bytes(paired_problem(p.experts));
     const size_t T = p.experts.T_max, H = p.experts.H;
-    size_t o = align_up(L->forward);
-    L->x = o;
+    size_t o = align_up(L.forward);
+    L.x = o;
     o = align_up(o + 2 * 2 * T * H);
-    L->part = o;
+    L.part = o;
     o = align_up(o + sizeof(float) * route_scratch_floats(p.experts.T_max, p.experts.E, p.experts.H, true));
-    L->y = o;
-    L->sums = align_up(o + sizeof(float) * T * H);
+    L.y = o;
+    L.sums = align_up(o + sizeof(float) * T * H);
     if (p.experts.forward_form == MOE_FORWARD_ONE_KERNEL)
-        o = align_up(L->sums + sizeof(float) * tail_sum_floats(p.experts.T_max, p.experts.H));
-    L->total = o;
-    return MOE_OK;
+        o = align_up(L.sums + sizeof(float) * tail_sum_floats(p.experts.T_max, p.experts.H));
+    L.total = o;
+    return L;
 }
 
 template <typename T>
@@ -284,13 +282,10 @@ moe_status_t moe_layer_workspace_size(const moe_layer_problem_t *problem, size_t
 {
     if (!bytes)
         return MOE_ERR_NULL;
-    moe_status_t st = check_layer(problem);
+    const moe_status_t st = check_layer(problem);
     if (st != MOE_OK)
         return st;
-    LayerLayout L = {};
-    if ((st = layer_layout(*problem, &L)) != MOE_OK)
-        return st;
-    *bytes = L.total;
+    *bytes = layer_layout(*problem).total;
     return MOE_OK;
 }
 
@@ -311,9 +306,8 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
     if (!aligned(w_pre, 16) || !aligned(w_router, 16) || !aligned(bias, 16) || !aligned(W13, 16) || !aligned(W2, 16) ||
         !aligned(topk_ids, 16) || !aligned(topk_weights, 16))
         return MOE_ERR_ALIGN;
-    LayerLayout L = {};
-    if ((st = layer_layout(p, &L)) != MOE_OK || (st = check_ws(ws, ws_bytes, L.total)) != MOE_OK ||
-        (st = validate_device()) != MOE_OK || (st = check_forward(paired_problem(p.experts))) != MOE_OK)
+    const LayerLayout L = layer_layout(p);
+    if ((st = check_ws(ws, ws_bytes, L.total)) != MOE_OK || (st = validate_device()) != MOE_OK || (st = check_forward(paired_problem(p.experts))) != MOE_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *x = at<void>(ws, L.x);

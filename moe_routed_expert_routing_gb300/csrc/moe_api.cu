@@ -34,6 +34,10 @@ constexpr size_t kHeaderBytes = (kCountersOffset + 6 * sizeof(int32_t) + kAlign 
 
 void resolve(const moe_problem_t &p, int *path, int *tile_rows);
 
+// Internal values of moe_problem_t.path (paired_problem): the M-small path with
+// token tiles of path - kPathPairedSmallM rows.
+constexpr int kPathPairedSmallM = 1000;
+
 // 128-wide K blocks of the down GEMM, the unit its K parts are made of (for
 // every weight layout alike, so that MXFP8 and bf16 weights split the same
 // way and stay bit-identical); 1 when I is not a multiple of 128 (no split).
@@ -136,6 +140,11 @@ void resolve(const moe_problem_t &p, int *path, int *tile_rows)
         chosen = (avg_rows <= 8.0 || p.weight_layout == MOE_WEIGHTS_MXFP8)
                      ? MOE_PATH_SMALL_M
                      : (avg_rows < 128.0 ? MOE_PATH_TILED_1CTA : MOE_PATH_TILED);
+    if (chosen > kPathPairedSmallM) {   // paired_problem's choice
+        *path = MOE_PATH_SMALL_M;
+        *tile_rows = chosen - kPathPairedSmallM;
+        return;
+    }
     *path = chosen;
     if (chosen == MOE_PATH_TILED || chosen == MOE_PATH_TILED_1CTA)
         *tile_rows = 128;
@@ -417,6 +426,8 @@ moe_status_t validate_device() { return check_device(); }
 
 size_t workspace_header_bytes() { return kHeaderBytes; }
 
+size_t forward_workspace_bytes(const moe_problem_t &p) { return layout_of(p).total; }
+
 int32_t *forward_inv(const moe_problem_t &p, void *ws) { return at<int32_t>(ws, layout_of(p).inv); }
 
 moe_problem_t paired_problem(const moe_problem_t &p)
@@ -424,10 +435,29 @@ moe_problem_t paired_problem(const moe_problem_t &p)
     moe_problem_t q = p;
     q.T_max = 2 * p.T_max;
     q.capacity = 2 * p.capacity;
-    int path = 0, tile_rows = 0;
-    resolve(q, &path, &tile_rows);
-    if (path == MOE_PATH_TILED)   // 256-row tiles, which a few tokens do not fill
-        q.path = MOE_PATH_TILED_1CTA;
+    if (p.weight_layout == MOE_WEIGHTS_MXFP8)
+        return q;
+    // Token tiles for a = 2 T_max k / E paired rows per expert on average: the
+    // fused 16-row kernel far longer than for whole batches, since few tokens
+    // leave its tiles mostly empty even in pairs. Measured per layer, us, with
+    // 16-row tiles / 32-row tiles / 128-row tiles (single CTA): E=64, k=8,
+    // H=4096, I=1536 a=4 301 / 339, a=8 352 / 365, a=16 382 / 409 / 443, a=32
+    // 32-row 481, 128-row 458; small experts gain from the wider tiles sooner:
+    // E=16, k=4, H=2048, I=1024 a=4 55.6 / 53.5, a=12 65.1 / 58.6 / 97; E=20,
+    // k=8, a=48 32-row 105, 128-row 129.
+    const double a = 2.0 * p.T_max * p.k / p.E;
+    const bool large = static_cast<long long>(p.H) * p.I >= (4LL << 20);
+    const bool small_m = p.path == MOE_PATH_SMALL_M;
+    if (p.path == MOE_PATH_AUTO || small_m) {
+        if (a <= 8.0 || (large && a <= 16.0))
+            q.path = kPathPairedSmallM + 16;
+        else if (small_m || a <= (large ? 24.0 : 64.0))
+            q.path = kPathPairedSmallM + 32;
+        else
+            q.path = MOE_PATH_TILED_1CTA;
+    } else {
+        q.path = MOE_PATH_TILED_1CTA;   // CTA pairs: 256-row tiles, which a few tokens do not fill
+    }
     return q;
 }
 

@@ -390,8 +390,9 @@ moe_status_t validate_device();
 // or weight layout that the shape cannot take.
 moe_status_t check_forward(const moe_problem_t &problem);
 // The forward's problem when its rows are paired (moe_layer): twice the tokens,
-// on single CTAs where CTA pairs were asked for or would be taken.
+// and a path of its own choice (an internal value; not for the entry points).
 moe_problem_t paired_problem(const moe_problem_t &problem);
+size_t forward_workspace_bytes(const moe_problem_t &problem);
 // moe_forward after its checks. With `tail` (moe_layer) rows are paired: x has
 // 2 T_max rows, the workspace is paired_problem's, and the combine's place is taken by
 // launch_combine_residual, or by the end of the one-kernel form (`out` is then
