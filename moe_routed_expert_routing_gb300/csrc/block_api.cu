@@ -340,7 +340,8 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
     // a few routed slots: the router's last CTA dispatches them (the one-kernel
     // form of the experts dispatches by itself)
     r.one_kernel = p.experts.forward_form == MOE_FORWARD_ONE_KERNEL;
-    const bool dispatched = p.experts.T_max * p.experts.k <= kRouteDispatchSlots && !r.one_kernel;
+    const bool dispatched = p.experts.T_max <= kRouteJoinTokens &&
+                            p.experts.T_max * p.experts.k <= kRouteDispatchSlots && !r.one_kernel;
     if (dispatched) {
         r.expert_offsets = expert_offsets;
         r.perm = perm;

@@ -269,7 +269,7 @@ struct RouteArgs {
     int normed, x_f32, w_f32, unit_offset;
     const void *w_pre;         // null: no weight
     void *x_out;               // [2 * T_max, H] bf16: each row's leading part and the rest (paired rows)
-    // moe_layer, at most kRouteDispatchSlots slots: moe_dispatch's tables, or null
+    // moe_layer, joined kernel, at most kRouteDispatchSlots slots: moe_dispatch's tables, or null
     int32_t *expert_offsets, *perm, *inv;
     int one_kernel;            // the last CTA selects for up to 16 tokens, in the same kernel
     long long x_stride;
@@ -293,7 +293,7 @@ struct RouteSplit {
 // against 12.5. moe_layer, whose router reads unrounded rows, takes them always.
 constexpr int kRouteFewTokens = 192;
 constexpr int kRouteJoinTokens = 2;
-constexpr int kRouteDispatchSlots = 128;
+constexpr int kRouteDispatchSlots = 32;     // of those tokens, dispatched by the same CTA
 
 inline RouteSplit route_split(int T_max, int E, int H, bool one_kernel = false)
 {

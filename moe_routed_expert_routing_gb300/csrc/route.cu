@@ -12,8 +12,8 @@
 // early behind the first. (One cooperative kernel whose CTAs waited for all
 // others at a grid-wide count took 8.1 us for one token and 2.3 us more when
 // not in a graph: 2 us of it at the count, the rest the cooperative launch.)
-// For moe_layer these kernels also write the rounded rows and, for up to 128
-// routed slots, dispatch them, so that the expert kernel comes next.
+// For moe_layer these kernels also write the experts' rows and, in the joined
+// kernel, dispatch up to 32 routed slots, so that the expert kernel comes next.
 // Products run on mma.sync m16n8k16 with the experts on M and 8 tokens on N:
 // at these sizes the tensor work is nothing, and fragments taken straight
 // from global memory need no staging. A dot product may take its terms in any
@@ -618,15 +618,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) route_few_kernel(const __grid_
 }
 
 // What follows the partial logits of more than two tokens: CTA t selects for
-// token t, CTA T_max + t writes its rounded row (moe_layer), and the last CTA
-// that selected dispatches (moe_layer, up to kRouteDispatchSlots slots).
+// token t, CTA T_max + t writes its rows for the experts (moe_layer). (The last
+// CTA that selected dispatching as well, as the joined kernel's does, measured
+// slower than a dispatch kernel behind this one from 24 slots on: 39.1 against
+// 38.2 us a layer, 59.7 against 55.9 at 128 slots.)
 template <bool kNormed>
 __global__ void __launch_bounds__(kFewThreads) route_finish_kernel(const __grid_constant__ RouteArgs a,
                                                                    const RouteSplit sp)
 {
     __shared__ SelectScratch s_sel;
-    __shared__ int s_ids[kRouteDispatchSlots];
-    __shared__ int s_last;
     pdl_wait();
     pdl_trigger();
     const int T = token_count(a.d_num_tokens, a.T_max);
@@ -643,28 +643,6 @@ __global__ void __launch_bounds__(kFewThreads) route_finish_kernel(const __grid_
         if (threadIdx.x < 32)
             store_block(a, job, s_sel);
     }
-    if (!a.perm)
-        return;
-    if (T == 0) {
-        if (job == 0)
-            dispatch_slots(a, s_ids, 0, 0);
-        return;
-    }
-    if (job >= T)
-        return;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0)
-        s_last = atom_add_acq_rel_gpu(a.counters, 1) == T - 1;
-    __syncthreads();
-    if (!s_last)
-        return;
-    if (threadIdx.x == 0)
-        *a.counters = 0;
-    for (int i = threadIdx.x; i < T * a.k; i += kFewThreads)
-        s_ids[i] = __ldcg(a.ids + i);
-    __syncthreads();
-    dispatch_slots(a, s_ids, T * a.k, 0);
 }
 
 template <int kTiles>

@@ -499,6 +499,7 @@ LAYERS = [
     dict(T=3, E=4, k=2, H=16384, I=64, gate=1),
     dict(T=9, E=32, k=3, H=8256, I=128, h="fp32", score=1),
     dict(T=40, E=300, k=64, H=64, I=64),
+    dict(T=2, E=100, k=64, H=64, I=64, nxt=False),
 ]
 
 
