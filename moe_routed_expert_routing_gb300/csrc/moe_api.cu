@@ -37,6 +37,7 @@ void resolve(const moe_problem_t &p, int *path, int *tile_rows);
 // Internal values of moe_problem_t.path (paired_problem): the M-small path with
 // token tiles of path - kPathPairedSmallM rows.
 constexpr int kPathPairedSmallM = 1000;
+constexpr int kPairedSplitBlocks = 4;    // see down_split_k
 
 // 128-wide K blocks of the down GEMM, the unit its K parts are made of (for
 // every weight layout alike, so that MXFP8 and bf16 weights split the same
@@ -209,7 +210,11 @@ moe_status_t record_stage(void *const *stage_events, int i, cudaStream_t s)
 // least 5% of the waves: each unit costs its readiness wait and epilogue.
 // At one token, E=384, H=7168, I=3072 (336 units of full K): 2 parts give
 // 672 units, 5 on 64 SMs and 4 on 88; 4 parts give 1344, 9 and 8.
-int down_split_k(const moe_problem_t &p, int path, int tile_rows, int sms)
+// min_blocks: 128-wide K blocks a part keeps at least. moe_layer asks for
+// four: with small experts the units' fixed cost outweighs their waves (8
+// tokens of E=64, k=4, H=1024, I=512 42.4 us a layer in four parts of one
+// block, 39.3 in one part; 16 of k=8 55.7 and 50.1).
+int down_split_k(const moe_problem_t &p, int path, int tile_rows, int sms, int min_blocks = 1)
 {
     if (path != MOE_PATH_SMALL_M || tile_rows != 16 || sms <= 0)
         return 1;
@@ -219,7 +224,7 @@ int down_split_k(const moe_problem_t &p, int path, int tile_rows, int sms)
     int best = 1;
     double best_waves = static_cast<double>((units + sms - 1) / sms);
     for (int parts = 2; parts <= 4; parts *= 2) {
-        if (kb % parts != 0)
+        if (kb % parts != 0 || kb / parts < min_blocks)
             continue;
         const double waves = static_cast<double>((units * parts + sms - 1) / sms) / parts;
         if (waves < 0.95 * best_waves) {
@@ -249,7 +254,7 @@ moe_status_t enqueue_expert_compute(const moe_problem_t &p, const void *act, con
     const int sms = device_sm_count();
     if (sms <= 0)
         return MOE_ERR_CUDA;
-    const int parts = down_split_k(p, path, tile_rows, sms);
+    const int parts = down_split_k(p, path, tile_rows, sms, pair ? kPairedSplitBlocks : 1);
     GemmProblem g;
     g.expert_offsets = expert_offsets;
     g.err = at<int32_t>(ws, L.err);
@@ -518,7 +523,7 @@ moe_status_t enqueue_forward(const moe_problem_t &p, const void *x, const int32_
     }
     // a down GEMM that splits K leaves its parts in the workspace's y buffers;
     // the combine sums them in part order
-    const int parts = down_split_k(p, path, tile_rows, sms);
+    const int parts = down_split_k(p, path, tile_rows, sms, pair ? kPairedSplitBlocks : 1);
     // decode-size batches (M-small, 16-row token tiles): both GEMMs run as one
     // persistent kernel whose down units wait on per-expert counts (zero at
     // every launch: the kernel clears them at its tail). Measured in one
