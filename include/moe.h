@@ -476,8 +476,9 @@ moe_status_t moe_layer_workspace_size(const moe_layer_problem_t *problem, size_t
  * then all the rest; as in moe_forward its CTAs wait on one another and the
  * form is refused for problems it does not fit. Otherwise three kernels
  * for one or two tokens (norm, router and dispatch; the experts' two
- * products; combine and residual), more for more. Arguments as in moe_norm, moe_route, moe_forward and moe_norm_residual;
- * w_pre, w_post and w_next follow norm.w_dtype. topk_ids, topk_weights,
+ * products; combine and residual), more for more. Arguments as in moe_norm,
+ * moe_route, moe_forward and moe_norm_residual; w_pre, w_post and w_next
+ * follow norm.w_dtype. topk_ids, topk_weights,
  * expert_offsets and perm are outputs. More tokens than MOE_LAYER_MAX_TOKENS
  * return MOE_ERR_SHAPE: call moe_norm, moe_route, moe_forward and
  * moe_norm_residual in turn (there the router and the experts read the

@@ -15,8 +15,8 @@
 // arithmetic runs on packed pairs (fma.rn.f32x2): at HBM's pace an SM has
 // about 12 issue slots for 32 elements of bf16, and scalar arithmetic with a
 // division and a square root per thread and row took 74% of all issue slots
-// (T=8192, H=4096, bf16: 25.0 us; with the residual in fp32 87 us). Now, of
-// the measured copy rate: 22.5 us, 0.88; 72.8 us, 0.82 (T=8191, fp32 stream,
+// (T=8192, H=4096, bf16: 25.0 us; with the residual in fp32 87 us). Now 43%;
+// of the measured copy rate: 22.5 us, 0.88; 68.5 us, 0.87 (T=8191, fp32 stream,
 // channel gate, next norm). One row of 7168: 2.5 us, the launch.
 #include <type_traits>
 
