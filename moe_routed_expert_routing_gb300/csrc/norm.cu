@@ -206,6 +206,9 @@ __device__ __forceinline__ float row_sum(Pair q, int tpr, float *s)
 }
 
 // Blocks of kBlock threads that share an SM, by the columns a thread holds.
+// Per-channel factors stay in registers where they leave two blocks or more an
+// SM: 16 columns with the residual, T=8191 of 4096 in fp32, 68.5 us so in two
+// blocks and 72.8 with the factors from L1 in three.
 template <bool kF32, int kV, bool kRes, int kBlock>
 struct Plan {
     static constexpr int kHeld = kV * Unit<kF32>::kCols;
