@@ -451,7 +451,8 @@ moe_status_t moe_route(const moe_router_problem_t *problem, const void *x, const
 #define MOE_LAYER_MAX_TOKENS 128
 
 /* The three parts agree in T_max (at most MOE_LAYER_MAX_TOKENS), H, E and k;
- * H is at most 16384. */
+ * H is at most 16384. The layer's sorted rows are its own and follow T_max * k:
+ * a larger experts.capacity changes nothing. */
 typedef struct moe_layer_problem {
     moe_problem_t experts;
     moe_router_problem_t router;

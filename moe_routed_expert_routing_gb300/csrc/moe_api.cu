@@ -439,7 +439,7 @@ moe_problem_t paired_problem(const moe_problem_t &p)
 {
     moe_problem_t q = p;
     q.T_max = 2 * p.T_max;
-    q.capacity = 2 * p.capacity;
+    q.capacity = 0;   // T_max * k: no layer has more rows, and twice a larger capacity may not fit 32 bits
     if (p.weight_layout == MOE_WEIGHTS_MXFP8)
         return q;
     // Token tiles for a = 2 T_max k / E paired rows per expert on average: the

@@ -138,6 +138,21 @@ def test_layer_pointers_and_workspace(B):
     assert so.moe_layer(ctypes.byref(gated), *ok, need, None) == NULL
 
 
+@pytest.mark.parametrize("capacity", [8, 9, 100, 1 << 29, 1 << 30, (1 << 30) + 4, (1 << 31) - 1])
+def test_layer_workspace_does_not_follow_the_capacity(B, capacity):
+    """The layer's sorted rows are its own: T_max * k of them whatever larger capacity the experts' description
+    names (twice that capacity would not fit 32 bits)."""
+    so = B.load_library()
+    need = B.moe_layer_workspace_size(layer(B))
+    p = layer(B, experts=dict(capacity=capacity))
+    assert B.moe_layer_workspace_size(p) == need
+    args = [FAKE, None, FAKE, None, FAKE, FAKE, None, None, None, None, FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE]
+    assert so.moe_layer(ctypes.byref(p), *args, need - 256, None) == WORKSPACE
+    with pytest.raises(B.MoeError) as ei:      # fewer rows than slots are refused as in moe_forward
+        B.moe_layer_workspace_size(layer(B, experts=dict(capacity=7)))
+    assert ei.value.status == SHAPE
+
+
 class _Rows:
     """Stands in for a CUDA tensor: device, type, shape and strides."""
     is_cuda = True
