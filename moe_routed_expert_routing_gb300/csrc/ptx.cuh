@@ -85,6 +85,15 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// Wait for the phase that this CTA's own copies or MMAs in flight complete,
+// whether or not a role has given up; at most `limit_ns` nanoseconds.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < limit_ns) {
+    }
+}
+
 // ---------------------------------------------------------------- clusters (CTA pairs)
 
 __device__ __forceinline__ uint32_t cluster_ctarank()

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (lane == 0) {
             const uint64_t pol_x = l2_policy_evict_first();   // each x row is read by one tile per expert tile
             const uint64_t pol_w = l2_policy_evict_last();
+            int issued = 0;
             for (int i = 0; i < kb1 - kb0; ++i) {
                 const int s = i % C::kStages;
                 const uint32_t phase = (i / C::kStages) & 1;
@@ -115,7 +116,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 mbar_arrive_expect_tx(full, C::kStageBytes);
                 tma_load_2d(dst, &tm_x, full, (kb0 + i) * 64, t0, n_tiles == 1 ? pol_x : l2_policy_evict_normal());
                 tma_load_2d(dst + C::kXBytes, &tm_w, full, (kb0 + i) * 64, e0, pol_w);
+                ++issued;
             }
+            // Every load has landed before this CTA's stages become exchange
+            // buffers, and before it exits, also if a role gave up (the MMAs
+            // otherwise waited for them all).
+            for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+                mbar_drain(smem_u32(&bar_full[i % C::kStages]), (i / C::kStages) & 1, wait_limit_ns);
         }
         __syncwarp();
     } else if (active && warp == 1) {
@@ -133,11 +140,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 umma_commit(smem_u32(&bar_empty[s]));
             }
             umma_commit(smem_u32(&bar_done));
+            // the MMAs issued so far, also after giving up: the accumulators are read and freed below
+            mbar_drain(smem_u32(&bar_done), 0, wait_limit_ns);
         }
         __syncwarp();
     }
     if (active) {
-        // every MMA, and with them every load of this CTA, is complete
+        // every MMA and every load of this CTA is complete at the barrier (or its role gave up twice)
         if (lane == 0)
             mbar_wait_bounded(smem_u32(&bar_done), 0, abort_flag, wait_limit_ns);
         __syncwarp();
