@@ -1779,8 +1779,11 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
         if constexpr (std::is_same<Tail, TailArgs>::value) {
             float *const s_red = reinterpret_cast<float *>(smem);   // the stages are free
             const int last = tail.n.x ? 2 : 1;
-            for (int phase = 0; phase <= last && !s_abort; ++phase) {
-                cta_tail<kSplitDown, kThreads>(fa, tail, s_inv, s_T, s_red, phase);
+            // after giving up a CTA does no more phases, but counts itself for
+            // each, so that the others need not wait the limit
+            for (int phase = 0; phase <= last; ++phase) {
+                if (!s_abort)
+                    cta_tail<kSplitDown, kThreads>(fa, tail, s_inv, s_T, s_red, phase);
                 __syncthreads();
                 if (phase == last)
                     break;
@@ -1788,11 +1791,9 @@ __global__ void __launch_bounds__(FusedCfg<kTileRows, kStages, kFp8>::kThreadsCt
                 if (threadIdx.x == 0) {
                     red_release_gpu_add(fa.done, 1);
                     const uint64_t t0 = global_timer_ns();
-                    while (ld_acquire_gpu(fa.done) < need * (phase + 2)) {
-                        if (global_timer_ns() - t0 > A1.wait_limit_ns) {
+                    while (!s_abort && ld_acquire_gpu(fa.done) < need * (phase + 2)) {
+                        if (global_timer_ns() - t0 > A1.wait_limit_ns)
                             s_abort = 1;
-                            break;
-                        }
                     }
                 }
                 __syncthreads();
