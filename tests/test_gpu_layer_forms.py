@@ -64,3 +64,88 @@ def test_layer_wait_limit_reports_and_recovers(B, form, layout):
     B.moe_clear_device_error(c.ws)
     same_bits(c.run(), clean)
     assert B.moe_last_device_error(c.ws) == 0
+
+
+# (layer, K parts of its down product): at least four 128-wide K blocks a part, up to 16-row tiles' few units
+SPLITS = [
+    (dict(T=1, E=8, k=4, H=512, I=1024), 2),
+    (dict(T=1, E=8, k=4, H=512, I=2048, gate=1), 4),
+    (dict(T=3, E=24, k=2, H=384, I=1280, h="fp32", score=1, bias=True), 2),     # five K blocks a part
+    (dict(T=2, E=16, k=3, H=256, I=2560, post=False, gate=2), 4),
+    (dict(T=16, E=32, k=2, H=320, I=2048, h="fp32", nxt=False), 4),             # H ends inside a tile; rows of 16 bits only
+    (dict(T=1, E=8, k=4, H=512, I=896), 1),                                     # seven K blocks: none
+]
+
+
+def parts_used(c):
+    """K parts whose buffers the last call wrote: the workspace behind its header was 0xA5 before it. Of the larger
+    buffers only unused parts, T * k pairs of fp32 rows each, and the sorted copy of x (half of that, where rows are
+    gathered) stay untouched."""
+    p = c.experts
+    blocks = p.I // 128 if p.I % 128 == 0 else 1
+    most = 4 if blocks % 4 == 0 else 2 if blocks % 2 == 0 else 1
+    part = 4 * 2 * p.T_max * p.k * p.H
+    untouched = 4 * int((c.ws[4608:].view(torch.int32) == -0x5A5A5A5B).sum())
+    return most - untouched // part
+
+
+@pytest.mark.parametrize("layout", [0, 1, 2], ids=["rows", "packed", "mxfp8"])
+@pytest.mark.parametrize("form", [0, 2], ids=["separate", "one_kernel"])
+@pytest.mark.parametrize("case,parts", SPLITS, ids=lambda v: "I{I}".format(**v) if isinstance(v, dict) else f"parts{v}")
+def test_layer_splits_the_down_product(B, case, parts, form, layout):
+    if layout and case["H"] % 128:
+        pytest.skip("packed and MXFP8 weights come in tiles of 128 rows")
+    c = LayerCase(B, form=form, layout=layout, **case)
+    c.ws[4608:].fill_(0xA5)
+    o = c.run()
+    torch.cuda.synchronize()
+    assert parts_used(c) == parts
+    c.verify(o)
+    same_bits(c.run(), o)
+    n = c.T - 1                          # fewer tokens than the description's, by the device count
+    fewer = c.run(T_dev=n)
+    for key, fill in (("h", 7.0), ("x_next", 7.0), ("ids", -9), ("weights", -9.0)):
+        if o[key] is not None:
+            assert torch.equal(fewer[key][:n], o[key][:n]) and (fewer[key][n:] == fill).all(), key
+
+
+# The one-kernel form's tail: a token's row in several items (of 1024 columns, or 2048 with MXFP8 weights) on
+# several CTAs, the last of them partly filled; the row sums meet through the GPU-wide count.
+TAILS = [
+    dict(T=1, E=8, k=2, H=2880, I=128),
+    dict(T=5, E=16, k=3, H=2880, I=192, h="fp32", gate=1),
+    dict(T=16, E=16, k=2, H=7168, I=128, post=False, gate=3),
+    dict(T=9, E=8, k=2, H=7168, I=128, nxt=False, gate=2, w="fp32"),
+    dict(T=3, E=8, k=2, H=7168, I=128, h="fp32", layout=2),
+    dict(T=17, E=16, k=2, H=2880, I=128, h="fp32", offset=True),          # more tokens than the router's last CTA takes
+    dict(T=40, E=64, k=4, H=1088, I=64, score=1, bias=True, post=False, nxt=False),
+    dict(T=128, E=256, k=2, H=1152, I=128, layout=2, gate=1),
+    dict(T=2, E=4, k=1, H=16384, I=64, stride=16392),
+]
+
+
+@pytest.mark.parametrize("case", TAILS, ids=lambda c: "T{T}E{E}k{k}H{H}I{I}".format(**c))
+def test_layer_one_kernel_tail(B, case):
+    c = LayerCase(B, form=2, **case)
+    o = c.run()
+    c.verify(o)
+    for _ in range(8):                   # the sums in any order of the CTAs give the same bits
+        same_bits(c.run(), o)
+    for n in (0, c.T // 2):
+        fewer = c.run(T_dev=n)
+        for key, fill in (("h", 7.0), ("x_next", 7.0), ("ids", -9), ("weights", -9.0)):
+            if o[key] is not None:
+                assert torch.equal(fewer[key][:n], o[key][:n]) and (fewer[key][n:] == fill).all(), (key, n)
+    assert B.moe_last_device_error(c.ws) == 0
+    assert int(c.ws[4:HEADER_BYTES].count_nonzero()) == 0
+
+
+def test_layer_one_kernel_form_is_refused_where_it_does_not_fit(B):
+    """MXFP8 weights and more than two paired rows an expert on average: 32-row tiles, which the form does not have.
+    Nothing is launched."""
+    c = LayerCase(B, T=3, E=4, k=2, H=256, I=128, layout=2, form=2)
+    with pytest.raises(B.MoeError) as ei:
+        c.run()
+    assert ei.value.status == 5
+    torch.cuda.synchronize()
+    assert int(c.ws.count_nonzero()) == 0
