@@ -1,13 +1,16 @@
 """moe_layer in the forms that its shape, its description and its kernels' waits
 bring about: rows beyond the routed slots, K parts of the down product, the
-one-kernel form's rows over several CTAs, waits that run out."""
+one-kernel form's rows over several CTAs, waits that run out; and the precision
+that an fp32 residual stream shows."""
 from __future__ import annotations
 
 import time
 
+import numpy as np
 import pytest
 import torch
 
+import block_reference as ref
 from test_gpu_block import B, LayerCase  # noqa: F401  (B is the module's fixture)
 
 pytestmark = pytest.mark.gpu
@@ -149,3 +152,29 @@ def test_layer_one_kernel_form_is_refused_where_it_does_not_fit(B):
     assert ei.value.status == 5
     torch.cuda.synchronize()
     assert int(c.ws.count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("case", [
+    dict(T=1, E=8, k=4, H=512, I=1024),                       # K parts
+    dict(T=8, E=8, k=4, H=2048, I=512),
+    dict(T=8, E=8, k=4, H=2048, I=512, path=2),               # 16-row tiles, asked for
+    dict(T=64, E=16, k=4, H=1024, I=256),                     # 32-row tiles
+    dict(T=128, E=8, k=4, H=512, I=256),                      # 128-row tiles
+    dict(T=8, E=16, k=2, H=7168, I=128),
+    dict(T=5, E=8, k=2, H=1024, I=512, layout=2),
+    dict(T=64, E=8, k=2, H=512, I=256, layout=2),
+    dict(T=5, E=8, k=2, H=1024, I=512, form=2),
+], ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_layer_precision_of_an_fp32_stream(B, case):
+    """The block's output as an fp32 stream shows it. x and h count with 16 bits: a relative 2^-17 of each element,
+    through gate, up and down together at most 2^-16 of the output's rms; sums truncate by up to 2^-23 for each of
+    their K / 16 steps; the norm's r is within 4e-6, and enters gate, up and their product."""
+    c = LayerCase(B, h="fp32", post=False, nxt=False, **case)
+    o = c.run()
+    c.verify(o)
+    h = ref.f64(c.h)
+    v = ref.norm(h, ref.f64(c.w_pre), 1e-6)
+    y = c.scale * ref.experts(v, o["ids"].cpu().numpy(), ref.f64(o["weights"]), c.ref13, c.ref2)
+    off = np.sqrt(((ref.f64(o["h"]) - h - y) ** 2).mean() / (y ** 2).mean())
+    stored = 2.0 ** -24 * np.sqrt((h ** 2).mean() / (y ** 2).mean())
+    assert off <= 2.0 ** -16 + (case["H"] + case["I"]) / 16 * 2.0 ** -23 + 3 * 4e-6 + stored, off
