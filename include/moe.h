@@ -467,17 +467,27 @@ moe_status_t moe_layer_workspace_size(const moe_layer_problem_t *problem, size_t
  *   ids, weights = the router on v  (as moe_route, but on v before its rounding)
  *   y = the experts on v, weighted and summed, unrounded
  *   h_out, x_next                   as moe_norm_residual, from y before its rounding
- * The experts' matrix instructions take bf16 activations; v and h go to them
- * as two bf16 rows each, leading part and rest, so they count with 16 bits
- * (a few tokens leave the token tiles mostly empty, so the second row costs
- * nothing to speak of). experts.path AUTO picks the token tiles for that
- * (16 or 32 rows, or the tiled path's 128); MOE_PATH_TILED runs as
- * MOE_PATH_TILED_1CTA. With experts.forward_form MOE_FORWARD_ONE_KERNEL the
+ * The experts' matrix instructions take bf16 activations; v and the experts'
+ * inner activations go to them as two bf16 rows each, leading part and rest,
+ * so they count with 16 bits, not 24 (a few tokens leave the token tiles mostly
+ * empty, so the second row costs nothing to speak of). Against 64 bits y is off by
+ * 5e-6 of its rms at H=1024, I=512 and 1.7e-5 at H=7168, I=2048, where the tensor
+ * cores' truncating sums add theirs; in 32 bits throughout it would be 1e-6 and
+ * 4e-7. A bf16 stream's own rounding hides that (1 of 200 elements of h_out
+ * rounds to the other neighbour); an fp32 stream carries it. experts.path AUTO
+ * picks the token tiles for paired rows (16 or 32 rows, or the tiled path's
+ * 128); MOE_PATH_TILED runs as MOE_PATH_TILED_1CTA. With experts.forward_form MOE_FORWARD_ONE_KERNEL the
  * call is two kernels for up to 16 tokens (three beyond): norm and router,
  * then all the rest; as in moe_forward its CTAs wait on one another and the
- * form is refused for problems it does not fit. Otherwise three kernels
- * for one or two tokens (norm, router and dispatch; the experts' two
- * products; combine and residual), more for more. Arguments as in moe_norm,
+ * form is refused for problems it does not fit (MXFP8 weights with more than
+ * two paired rows an expert on average among them). Otherwise: norm and router,
+ * one kernel for T_max <= 2, two beyond; the dispatch, inside that kernel for
+ * T_max <= 2 with T_max*k <= 32, else one kernel (three above 1024 slots); a
+ * gather of the rows for MXFP8 weights and for 128-row tiles; the experts, one
+ * kernel with 16-row tiles or MXFP8 weights, else two; combine and residual. So
+ * a decoded token takes three kernels with bf16 weights and four with MXFP8. The
+ * call beats its four pieces up to about 64 tokens; at 128 the pieces, whose
+ * experts read bf16 x, took 4% to 12% less. Arguments as in moe_norm,
  * moe_route, moe_forward and moe_norm_residual; w_pre, w_post and w_next
  * follow norm.w_dtype. topk_ids, topk_weights,
  * expert_offsets and perm are outputs. More tokens than MOE_LAYER_MAX_TOKENS

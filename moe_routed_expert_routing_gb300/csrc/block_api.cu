@@ -307,7 +307,8 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
         !aligned(topk_ids, 16) || !aligned(topk_weights, 16))
         return MOE_ERR_ALIGN;
     const LayerLayout L = layer_layout(p);
-    if ((st = check_ws(ws, ws_bytes, L.total)) != MOE_OK || (st = validate_device()) != MOE_OK || (st = check_forward(paired_problem(p.experts))) != MOE_OK)
+    if ((st = check_ws(ws, ws_bytes, L.total)) != MOE_OK || (st = validate_device()) != MOE_OK ||
+        (st = check_forward(paired_problem(p.experts))) != MOE_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *x = at<void>(ws, L.x);
@@ -318,7 +319,7 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
     n.w_next = w_next;
     n.h_out = h_out;
     n.x = x_next;
-    // the norm, the router and the rounded rows in one kernel
+    // the norm, the router and the experts' rows: one kernel, or two
     RouteArgs r = route_args(p.router);
     r.x = h;
     r.x_stride = stride_of(p.norm.h_stride, p.norm.H);

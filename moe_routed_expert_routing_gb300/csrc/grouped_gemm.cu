@@ -86,8 +86,11 @@ struct GemmArgs {
     int out_f16;        // tiled down GEMM: y stored as fp16 (saturated at +-65504) instead of fp32
     // 1: paired rows (moe_layer). Each routed row is two activation rows, 2r
     // and 2r + 1: a value's leading bf16 part and the rest, so that x and h
-    // count with 16 bits instead of 8. The few-token GEMMs stream weights past
-    // token tiles that are mostly empty, so the second row is free; the
+    // count with 16 bits instead of 8 (a bf16 stream's error against 64 bits
+    // 1.7e-3, its own rounding, instead of 2.7e-3; a third part, 24 bits, would
+    // show in an fp32 stream only, where y is off by 5e-6 to 2e-5 of its rms,
+    // much of that from the tensor cores' sums). The few-token GEMMs stream
+    // weights past token tiles that are mostly empty, so the second row is free; the
     // gate-up epilogue adds the pair's two sums before SiLU and splits h
     // again, and the down GEMM's two rows are added by the combine. Offsets
     // and perm count routed rows; row counts here, cap and x are doubled.

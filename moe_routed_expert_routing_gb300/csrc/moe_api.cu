@@ -446,10 +446,16 @@ moe_problem_t paired_problem(const moe_problem_t &p)
     // fused 16-row kernel far longer than for whole batches, since few tokens
     // leave its tiles mostly empty even in pairs. Measured per layer, us, with
     // 16-row tiles / 32-row tiles / 128-row tiles (single CTA): E=64, k=8,
-    // H=4096, I=1536 a=4 301 / 339, a=8 352 / 365, a=16 382 / 409 / 443, a=32
-    // 32-row 481, 128-row 458; small experts gain from the wider tiles sooner:
-    // E=16, k=4, H=2048, I=1024 a=4 55.6 / 53.5, a=12 65.1 / 58.6 / 97; E=20,
-    // k=8, a=48 32-row 105, 128-row 129.
+    // H=4096, I=1536 a=4 292 / 331 / 356, a=8 355 / 398 / 423, a=16 385 / 405 /
+    // 428, a=24 476 / 400 / 437, a=32 585 / 466 / 447; smaller experts, H=2048,
+    // I=1024, E=16, k=4 a=4 51.5 / 53.0 / 82.2, a=8 53.3 / 52.7 / 83.2, a=12
+    // 53.3 / 53.3 / 83.6, a=24 66.1 / 57.6 / 88.2; E=64, k=4 a=2 94.8 / 113 /
+    // 155, a=8 132 / 151 / 189; E=20, k=8 a=48 123 / 103 / 120. Between a=8 and
+    // 16 small experts stay near equal or, with many of them, lose by the wider
+    // tiles (E=64, k=4 a=16 150 / 162 / 189).
+    // MXFP8 weights keep moe_forward's rule on the doubled rows: 16, 32 and
+    // 64-row tiles are within 7% up to a=8 (E=64, k=4, H=2048, I=1024 a=2 88.1 /
+    // 90.2 / 93.1, a=4 105 / 108 / 112, a=8 121 / 121 / 125); a=16 159 / 130 / 135.
     const double a = 2.0 * p.T_max * p.k / p.E;
     const bool large = static_cast<long long>(p.H) * p.I >= (4LL << 20);
     const bool small_m = p.path == MOE_PATH_SMALL_M;
