@@ -15,9 +15,10 @@
 // arithmetic runs on packed pairs (fma.rn.f32x2): at HBM's pace an SM has
 // about 12 issue slots for 32 elements of bf16, and scalar arithmetic with a
 // division and a square root per thread and row took 74% of all issue slots
-// (T=8192, H=4096, bf16: 25.0 us; with the residual in fp32 87 us). Now 43%;
-// of the measured copy rate: 22.5 us, 0.88; 68.5 us, 0.87 (T=8191, fp32 stream,
-// channel gate, next norm). One row of 7168: 2.5 us, the launch. Longer rows hold
+// (T=8192, H=4096, bf16: 25.0 us on one buffer, part of which stays in L2; with
+// the residual in fp32 87 us). Now 43%: 22.5 us so, 25.1 us on inputs larger than
+// L2 (0.79 of the measured copy rate; fp32 33.3, 0.89); 68.5 us, 0.87 (T=8191, fp32
+// stream, channel gate, next norm). One row of 7168: 2.5 us, the launch. Longer rows hold
 // 32 columns a thread and take their factors from L1: T=8192, H=7168 50.1 us (0.69
 // of the copy rate; fp32 60.1, 0.87), with the residual 108 (0.64; fp32 162, 0.64).
 #include <type_traits>
