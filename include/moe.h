@@ -501,6 +501,126 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
                        int32_t *expert_offsets, int32_t *perm, void *h_out, void *x_next, void *ws, size_t ws_bytes,
                        void *stream);
 
+/* ------------------------------------------------------------------------
+ * Training: the gradients of the operators above. Written g for "gradient of
+ * the loss by": d_out = g(out) and so on. The conventions above hold. Nothing
+ * is kept from the forward calls but what the arguments name: the routing's
+ * maps (inv and expert_offsets of moe_dispatch), the sorted rows x_sorted, the
+ * experts' y_sorted (only if the routing weights' gradient is wanted) and the
+ * router's logits. The chain of one block, last to first:
+ *   moe_combine_backward   d_out           -> dy_sorted, d_weights
+ *   moe_expert_backward    dy_sorted       -> dx_sorted, dW13, dW2
+ *   moe_route_backward     d_weights       -> dx (the router's part), dw_router
+ *   moe_dispatch_backward  dx_sorted       -> dx (all of it)
+ *   moe_norm_backward      dx              -> dh, dw
+ * Every operator is deterministic: sums go in a fixed order, no atomics.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Gradient of moe_combine, for r = inv[t*k + j]:
+ *   dy_sorted[r, m]  = bf16( w[t, j] * d_out[t, m] )
+ *   d_weights[t, j]  = sum_m d_out[t, m] y_sorted[r, m]       (fp32)
+ *   d_out[T_max, H] bf16, y_sorted[cap, H] fp32 (NULL without d_weights),
+ *   inv[T_max*k] and topk_weights[T_max, k] as for moe_combine,
+ *   dy_sorted[cap, H] bf16 out: rows that no slot holds are not written,
+ *   d_weights[T_max, k] fp32 out, 0 for a dropped slot, or NULL (not wanted).
+ * Slots of tokens >= T are not read or written.
+ */
+moe_status_t moe_combine_backward(const moe_problem_t *problem, const void *d_out, const float *y_sorted,
+                                  const int32_t *inv, const float *topk_weights, const int32_t *d_num_tokens,
+                                  void *dy_sorted, float *d_weights, void *stream);
+
+/*
+ * Gradient of moe_dispatch's row gather:
+ *   dx[t, m] = bf16( sum_{j = 0..k-1} dx_sorted[inv[t*k + j], m] + dx_add[t, m] )
+ * in fp32, j ascending, dropped slots skipped, dx_add last.
+ *   dx_sorted[cap, H] of dx_dtype (moe_dtype_t), dx_add[T_max, H] bf16 or NULL
+ *   (the gradient that reaches x on another path, the router's), dx[T_max, H]
+ *   bf16 out, rows >= T untouched. dx may be dx_add.
+ */
+moe_status_t moe_dispatch_backward(const moe_problem_t *problem, int32_t dx_dtype, const void *dx_sorted,
+                                   const int32_t *inv, const void *dx_add, const int32_t *d_num_tokens, void *dx,
+                                   void *stream);
+
+typedef struct moe_expert_grad_problem {
+    moe_problem_t experts;  /* weight_layout ROW_MAJOR (others: MOE_ERR_UNSUPPORTED); path and forward_form are not read */
+    int32_t dx_dtype;       /* moe_dtype_t of dx_sorted */
+    int32_t dw_dtype;       /* moe_dtype_t of dW13 and dW2 */
+    int32_t accumulate;     /* 1: the weight gradients are added to what dW13 and dW2 hold (FP32 only) */
+} moe_expert_grad_problem_t;
+
+/* Bytes of workspace of moe_expert_backward: the device error word and 6 bytes
+ * for each of cap * I elements (pure host). Zero-filled before its first use. */
+moe_status_t moe_expert_backward_workspace_size(const moe_expert_grad_problem_t *problem, size_t *bytes);
+
+/*
+ * Gradient of moe_expert_compute. With g, u the gate and up products of the
+ * rows (computed again), s = 1 / (1 + exp(-g)), a = g s u, of each expert e and
+ * its rows r:
+ *   da[r]  = dy_sorted[r] W2[e],  du = da g s,  dg = da u s (1 + g (1 - s))
+ *   dx_sorted[r] = [dg du][r] W13[e]
+ *   dW2[e]  = sum_r dy_sorted[r]^T a[r],  dW13[e] = sum_r [dg du][r]^T x_sorted[r]
+ * fp32 sums on the tensor cores; a and [dg du] are rounded to bf16 once, as
+ * their operands, and each output once. An expert without rows gets zero
+ * weight gradients (none added with `accumulate`).
+ *   x_sorted, dy_sorted [cap, H] bf16; expert_offsets[E+1] of moe_dispatch (or
+ *   any non-decreasing offsets, clamped to [0, cap]); W13, W2 as for
+ *   moe_expert_compute; dx_sorted[cap, H], dW13[E, 2I, H], dW2[E, H, I] out, each
+ *   NULL if not wanted, not all. Rows of dx_sorted at and past
+ *   expert_offsets[E] are not written; rows of the inputs there do not count,
+ *   whatever they hold.
+ */
+moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const void *x_sorted,
+                                 const int32_t *expert_offsets, const void *W13, const void *W2, const void *dy_sorted,
+                                 void *dx_sorted, void *dW13, void *dW2, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace of moe_norm_backward (pure host). */
+moe_status_t moe_norm_backward_workspace_size(const moe_norm_problem_t *problem, size_t *bytes);
+
+/*
+ * Gradient of moe_norm (and, with dh_add, of moe_norm_residual's next norm),
+ * r_t and the weight w' (w, or 1 + w with unit_offset) as there, q = dx * w':
+ *   dh[t, m] = r_t ( q[t, m] - h[t, m] r_t^2 mean_m(q h) ) + dh_add[t, m]
+ *   dw[m]    = sum_{t < T} dx[t, m] h[t, m] r_t
+ * in fp32, one rounding per output.
+ *   h[T_max, H] of h_dtype, rows h_stride apart; w[H] of w_dtype or NULL (no
+ *   weight); dx[T_max, H] bf16, rows x_stride apart; dh_add[T_max, H] of
+ *   h_dtype, rows y_stride apart, or NULL (the gradient that reaches h past the
+ *   block); dh[T_max, H] of h_dtype out, rows out_stride apart; dw[H] of
+ *   w_dtype out, or NULL. dh may be h or dh_add, with the same stride.
+ * norm_block, gate and residual_scale are not read. The workspace need not be
+ * cleared.
+ */
+moe_status_t moe_norm_backward(const moe_norm_problem_t *problem, const void *h, const void *w, const void *dx,
+                               const void *dh_add, const int32_t *d_num_tokens, void *dh, void *dw, void *ws,
+                               size_t ws_bytes, void *stream);
+
+/* Bytes of workspace of moe_route_backward (pure host). Zero-filled before its
+ * first use; holds the device error word at its start. */
+moe_status_t moe_route_backward_workspace_size(const moe_router_problem_t *problem, size_t *bytes);
+
+/*
+ * Gradient of moe_route by its weights:
+ *   d_logits[t, e] = g(logits) from d_weights through the score, renormalising
+ *                    and scale, plus d_logits_add[t, e]              (fp32)
+ *   dx[t, m]       = bf16( sum_e d_logits[t, e] w_router[e, m] )
+ *   dw_router[e,m] = sum_{t < T} d_logits[t, e] x[t, m]
+ * The choice of experts and the selection bias have no gradient. The products
+ * take d_logits with 16 bits (two bf16 parts; a relative 2^-16) and sum in fp32.
+ * Logits that are NaN or +inf count as -inf, whose gradient is 0; an id of -1
+ * adds nothing, an id outside [0, E) neither and sets MOE_DEVERR_BAD_EXPERT_ID.
+ *   x[T_max, H] bf16 (NULL without dw_router), w_router[E, H] bf16 (NULL without
+ *   dx), logits[T_max, E], topk_ids[T_max, k] as moe_route wrote them,
+ *   d_weights[T_max, k] fp32, d_logits_add[T_max, E] fp32 or NULL (an auxiliary
+ *   loss's gradient); dx, dw_router[E, H] of dw_dtype (moe_dtype_t) and
+ *   d_logits[T_max, E] fp32 out, each NULL if not wanted, not all. Rows >= T of
+ *   dx and d_logits are not written. d_logits may be d_logits_add.
+ */
+moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_dtype, const void *x,
+                                const void *w_router, const float *logits, const int32_t *topk_ids,
+                                const float *d_weights, const float *d_logits_add, const int32_t *d_num_tokens,
+                                void *dx, void *dw_router, float *d_logits, void *ws, size_t ws_bytes, void *stream);
+
 /* Read the sticky device error word of `ws` into *host_code (0 = none).
  * Synchronises `stream` (the only entry point that does). */
 moe_status_t moe_last_device_error(const void *ws, void *stream, int32_t *host_code);

@@ -63,6 +63,14 @@ EXPORTED_SYMBOLS = (
     "moe_route",
     "moe_layer_workspace_size",
     "moe_layer",
+    "moe_combine_backward",
+    "moe_dispatch_backward",
+    "moe_expert_backward_workspace_size",
+    "moe_expert_backward",
+    "moe_norm_backward_workspace_size",
+    "moe_norm_backward",
+    "moe_route_backward_workspace_size",
+    "moe_route_backward",
 )
 
 
@@ -185,6 +193,17 @@ class LayerProblem(ctypes.Structure):
         return cls(experts, router, norm)
 
 
+class ExpertGradProblem(ctypes.Structure):
+    """``moe_expert_grad_problem_t``: the experts' description, the gradients' types, and whether weight gradients add up."""
+
+    _fields_ = [("experts", Problem), ("dx_dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+    @classmethod
+    def make(cls, experts: Problem, dx_dtype=torch.bfloat16, dw_dtype=torch.bfloat16, accumulate=False):
+        return cls(experts, _dtype_code(dx_dtype), _dtype_code(dw_dtype), int(accumulate))
+
+
 class Profile(ctypes.Structure):
     """``moe_profile_t``: the static launch profile of a problem."""
 
@@ -258,6 +277,18 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.moe_layer_workspace_size.restype = st
     lib.moe_layer.argtypes = [LP] + [_vp] * 17 + [ctypes.c_size_t, _vp]
     lib.moe_layer.restype = st
+    i32, size = ctypes.c_int32, ctypes.c_size_t
+    EP = ctypes.POINTER(ExpertGradProblem)
+    for name, args in (("moe_combine_backward", [_P] + [_vp] * 8), ("moe_dispatch_backward", [_P, i32] + [_vp] * 6),
+                       ("moe_expert_backward_workspace_size", [EP, sz]),
+                       ("moe_expert_backward", [EP] + [_vp] * 9 + [size, _vp]),
+                       ("moe_norm_backward_workspace_size", [NP, sz]),
+                       ("moe_norm_backward", [NP] + [_vp] * 8 + [size, _vp]),
+                       ("moe_route_backward_workspace_size", [RP, sz]),
+                       ("moe_route_backward", [RP, i32] + [_vp] * 11 + [size, _vp])):
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = st
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -593,6 +624,103 @@ def moe_layer(problem: LayerProblem, h, w_pre, w_router, W13, W2, topk_ids, topk
     _check(load_library().moe_layer(ctypes.byref(p), h, w_pre, w_router, bias, _ptr(W13), _ptr(W2), w_post, gate,
                                     w_next, n, ids, weights, offsets, perm, h_out, x_next, _ptr(ws),
                                     ws.numel() * ws.element_size(), _stream(stream)), "moe_layer")
+
+
+def _dtype_of(code):
+    """The torch dtype of a moe_dtype_t."""
+    return torch.float32 if code == MOE_DTYPE_FP32 else torch.bfloat16
+
+
+def moe_combine_backward(problem: Problem, d_out, inv, topk_weights, dy_sorted, y_sorted=None, d_weights=None,
+                         d_num_tokens=None, stream=None):
+    """dy_sorted and, with y_sorted, the routing weights' gradient; see include/moe.h."""
+    p = problem
+    slots, rows = p.T_max * p.k, p.cap * p.H
+    _check(load_library().moe_combine_backward(
+        ctypes.byref(p), _dev(d_out, "d_out", torch.bfloat16, p.T_max * p.H),
+        _dev(y_sorted, "y_sorted", torch.float32, rows), _dev(inv, "inv", torch.int32, slots),
+        _dev(topk_weights, "topk_weights", torch.float32, slots), _dev(d_num_tokens, "d_num_tokens", torch.int32, 1),
+        _dev(dy_sorted, "dy_sorted", torch.bfloat16, rows), _dev(d_weights, "d_weights", torch.float32, slots),
+        _stream(stream)), "moe_combine_backward")
+
+
+def moe_dispatch_backward(problem: Problem, dx_sorted, inv, dx, dx_add=None, d_num_tokens=None, stream=None):
+    """dx = the sum of a token's rows of dx_sorted (bf16 or fp32), plus dx_add; see include/moe.h."""
+    p = problem
+    dtype = torch.bfloat16 if isinstance(dx_sorted, int) or dx_sorted is None else dx_sorted.dtype
+    code = _dtype_code(dtype)
+    _check(load_library().moe_dispatch_backward(
+        ctypes.byref(p), code, _dev(dx_sorted, "dx_sorted", dtype, p.cap * p.H),
+        _dev(inv, "inv", torch.int32, p.T_max * p.k), _dev(dx_add, "dx_add", torch.bfloat16, p.T_max * p.H),
+        _dev(d_num_tokens, "d_num_tokens", torch.int32, 1), _dev(dx, "dx", torch.bfloat16, p.T_max * p.H),
+        _stream(stream)), "moe_dispatch_backward")
+
+
+def moe_expert_backward_workspace_size(problem: ExpertGradProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_expert_backward_workspace_size(ctypes.byref(problem), ctypes.byref(n)),
+           "moe_expert_backward_workspace_size")
+    return n.value
+
+
+def moe_expert_backward(problem: ExpertGradProblem, x_sorted, expert_offsets, W13, W2, dy_sorted, ws, dx_sorted=None,
+                        dW13=None, dW2=None, stream=None):
+    """Gradients of the experts' rows and weights; see include/moe.h."""
+    p = problem.experts
+    rows, n = p.cap * p.H, p.E * p.I * p.H
+    dxt, dwt, bf = _dtype_of(problem.dx_dtype), _dtype_of(problem.dw_dtype), torch.bfloat16
+    _need(ws, "ws", None, 0)
+    _check(load_library().moe_expert_backward(
+        ctypes.byref(problem), _dev(x_sorted, "x_sorted", bf, rows),
+        _dev(expert_offsets, "expert_offsets", torch.int32, p.E + 1),
+        *((_dev(W13, "W13", bf, 2 * n), _dev(W2, "W2", bf, n)) if p.weight_layout != MOE_WEIGHTS_MXFP8
+          else (_ptr(W13), _ptr(W2))),   # a layout that the library refuses
+        _dev(dy_sorted, "dy_sorted", bf, rows), _dev(dx_sorted, "dx_sorted", dxt, rows),
+        _dev(dW13, "dW13", dwt, 2 * n), _dev(dW2, "dW2", dwt, n), _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream)), "moe_expert_backward")
+
+
+def moe_norm_backward_workspace_size(problem: NormProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_norm_backward_workspace_size(ctypes.byref(problem), ctypes.byref(n)),
+           "moe_norm_backward_workspace_size")
+    return n.value
+
+
+def moe_norm_backward(problem: NormProblem, h, w, dx, dh, ws, dh_add=None, dw=None, d_num_tokens=None, stream=None):
+    """dh = the norm's gradient from dx, plus dh_add, and the weight's gradient dw; see include/moe.h."""
+    p = problem
+    T, H, ht, wt = p.T_max, p.H, p.h_torch, p.w_torch
+    _need(ws, "ws", None, 0)
+    _check(load_library().moe_norm_backward(
+        ctypes.byref(p), _need_rows(h, "h", ht, T, H, p.h_stride), _dev(w, "w", wt, H),
+        _need_rows(dx, "dx", torch.bfloat16, T, H, p.x_stride), _need_rows(dh_add, "dh_add", ht, T, H, p.y_stride),
+        _dev(d_num_tokens, "d_num_tokens", torch.int32, 1), _need_rows(dh, "dh", ht, T, H, p.out_stride),
+        _dev(dw, "dw", wt, H), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "moe_norm_backward")
+
+
+def moe_route_backward_workspace_size(problem: RouterProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_route_backward_workspace_size(ctypes.byref(problem), ctypes.byref(n)),
+           "moe_route_backward_workspace_size")
+    return n.value
+
+
+def moe_route_backward(problem: RouterProblem, x, w_router, logits, topk_ids, d_weights, ws, d_logits_add=None,
+                       dx=None, dw_router=None, d_logits=None, d_num_tokens=None, stream=None):
+    """The router's gradients from its weights' (dw_router in bf16 or fp32); see include/moe.h."""
+    p = problem
+    T, slots, bf, f32 = p.T_max, p.T_max * p.k, torch.bfloat16, torch.float32
+    dwt = bf if dw_router is None or isinstance(dw_router, int) else dw_router.dtype
+    code = _dtype_code(dwt)
+    _need(ws, "ws", None, 0)
+    _check(load_library().moe_route_backward(
+        ctypes.byref(p), code, _dev(x, "x", bf, T * p.H), _dev(w_router, "w_router", bf, p.E * p.H),
+        _dev(logits, "logits", f32, T * p.E), _dev(topk_ids, "topk_ids", torch.int32, slots),
+        _dev(d_weights, "d_weights", f32, slots), _dev(d_logits_add, "d_logits_add", f32, T * p.E),
+        _dev(d_num_tokens, "d_num_tokens", torch.int32, 1), _dev(dx, "dx", bf, T * p.H),
+        _dev(dw_router, "dw_router", dwt, p.E * p.H), _dev(d_logits, "d_logits", f32, T * p.E), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)), "moe_route_backward")
 
 
 def moe_last_device_error(ws, stream=None) -> int:

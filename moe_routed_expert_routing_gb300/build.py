@@ -21,8 +21,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["moe_api.cu", "dispatch.cu", "dispatch_noalloc.cu", "combine.cu", "grouped_gemm.cu", "weights_pack.cu",
-           "weights_mx.cu", "norm.cu", "route.cu", "route_gemm.cu", "combine_residual.cu", "block_api.cu"]
-HEADERS = ["ptx.cuh", "moe_internal.h", "route_select.cuh", "row_ops.cuh"]
+           "weights_mx.cu", "norm.cu", "route.cu", "route_gemm.cu", "combine_residual.cu", "block_api.cu",
+           "rows_backward.cu", "expert_backward.cu", "norm_backward.cu", "route_backward.cu", "grad_api.cu"]
+HEADERS = ["ptx.cuh", "moe_internal.h", "route_select.cuh", "row_ops.cuh", "tiles.cuh", "norm_ops.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -187,6 +187,9 @@ moe_status_t check_residual(const moe_norm_problem_t &p, const void *h, const vo
 
 }  // namespace
 
+moe_status_t validate_norm(const moe_norm_problem_t *problem) { return check_norm(problem); }
+moe_status_t validate_router(const moe_router_problem_t *problem) { return check_router(problem); }
+
 }  // namespace moe
 
 using namespace moe;

@@ -61,6 +61,7 @@
 #include "moe_internal.h"
 #include "ptx.cuh"
 #include "row_ops.cuh"
+#include "tiles.cuh"
 
 namespace moe {
 
@@ -70,7 +71,6 @@ constexpr int kThreads = 256;
 constexpr int kUnitRing = 8;     // persistent single-CTA GEMMs: unit ids in flight between their roles
 constexpr int kBK = 64;          // K elements per stage: one 128-byte swizzle row
 constexpr int kUmmaK = 16;       // K of one tcgen05.mma kind::f16
-constexpr unsigned kFull = 0xffffffffu;
 
 struct GemmArgs {
     const int32_t *expert_offsets;
@@ -211,20 +211,6 @@ struct UnitRing {
     }
 };
 
-// Largest e in [0, E) with tp[e] * scale <= u (tp non-decreasing, tp[0] = 0).
-__device__ __forceinline__ int find_expert(const int *tp, int E, int u, int scale)
-{
-    int lo = 0, hi = E - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tp[mid] * scale <= u)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
-}
-
 // Unit u of a grouped GEMM. Two orders, both expert-major:
 // - kWeightOuter: column tile, then row tile. The row tiles of one weight tile
 //   go to neighbouring CTAs, which share it in L2 (the M-small GEMMs, and the
@@ -260,39 +246,6 @@ __device__ __forceinline__ Unit decode_unit(int u, const int *s_off, const int *
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
     return (g / (1.0f + expf(-g))) * u;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
-
-// Per-expert row-tile prefix (one warp): s_tp[e] = sum_{e' < e} ceil(rows(e') / tile_rows).
-__device__ __forceinline__ void build_tile_prefix(const int *s_off, int *s_tp, int E, int tile_rows, int lane)
-{
-    int carry = 0;
-    for (int base = 0; base < E; base += 32) {
-        const int e = base + lane;
-        int tiles = 0;
-        if (e < E) {
-            int c = s_off[e + 1] - s_off[e];
-            c = c < 0 ? 0 : c;
-            tiles = (c + tile_rows - 1) / tile_rows;
-        }
-        int v = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(kFull, v, o);
-            if (lane >= o)
-                v += n;
-        }
-        if (e < E)
-            s_tp[e] = carry + v - tiles;
-        carry += __shfl_sync(kFull, v, 31);
-    }
-    if (lane == 0)
-        s_tp[E] = carry;
 }
 
 // The same prefix by the whole block, for the decode kernel whose prologue is

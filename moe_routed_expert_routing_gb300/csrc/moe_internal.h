@@ -372,6 +372,88 @@ cudaError_t launch_route_gemm(const RouteArgs &a, float *logits, cudaStream_t st
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl);
 
+// ---- gradients (rows_backward.cu, expert_backward.cu, norm_backward.cu, route_backward.cu) ----
+
+// dy_sorted[inv[t*k + j]] = bf16(w[t, j] * d_out[t]) and, with d_weights, the
+// dot products <d_out[t], y_sorted[inv[t*k + j]]>
+cudaError_t launch_combine_backward(const void *d_out, const float *y_sorted, const int32_t *inv,
+                                    const float *topk_weights, const int32_t *d_num_tokens, int T_max, int k, int cap,
+                                    int H, void *dy_sorted, float *d_weights, int num_sms, cudaStream_t stream);
+
+// dx[t] = bf16(sum_j dx_sorted[inv[t*k + j]] + dx_add[t])
+cudaError_t launch_dispatch_backward(const void *dx_sorted, bool f32, const int32_t *inv, const void *dx_add,
+                                     const int32_t *d_num_tokens, int T_max, int k, int cap, int H, void *dx, int num_sms,
+                                     cudaStream_t stream);
+
+// act[r] = a and dgu[r] = [dg du] of the rows r < offsets[E], bf16 (expert_backward.cu)
+cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, const void *W2, const int32_t *offsets,
+                            int E, int cap, int H, int I, void *act, void *dgu, int32_t *err, int num_sms,
+                            cudaStream_t stream);
+
+// One grouped product of bf16 operands, for every expert e with the rows R_e =
+// [offsets[e], offsets[e + 1]):
+//  by_rows:  out[r, n] = sum_k a[r, k] b[e * b_expert_rows + k mod (64 wrap), n], r in R_e, k < 64 k_blocks
+//  else:     out[e, m, n] = sum_{p < parts} sum_{r in R_e} a[r, m + p part_cols] b[r, n], m < M
+// for n < N. a [a_rows, a_cols] and b [b_rows, b_cols] row-major; rows of out ld elements apart.
+struct ProductJob {
+    int by_rows;
+    const void *a, *b;
+    long long a_rows, a_cols, b_rows, b_cols;
+    int M, N;
+    int k_blocks, wrap, b_expert_rows;
+    int parts, part_cols;
+    void *out;
+    int out_f32;            // fp32, else bf16
+    int accumulate;         // fp32, not by_rows: added to what is there
+    long long ld;
+    size_t expert_stride;   // not by_rows: elements between experts
+};
+
+long long product_units(const ProductJob &j, int E, int cap);   // at most, for any offsets
+
+// Up to three products in one launch; their rows are the same batch of `cap` rows.
+cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offsets, int E, int cap, int32_t *err,
+                            int num_sms, cudaStream_t stream);
+
+struct NormGradArgs {
+    const void *h;             // bf16 or fp32
+    const void *w;             // null: no weight
+    const void *dx;            // bf16
+    const void *dh_add;        // type of h; null: none
+    const int32_t *d_num_tokens;
+    void *dh;                  // type of h
+    void *dw;                  // type of w; null: not wanted
+    float *part;               // norm_grad_part_rows() x H partial sums of dw
+    int T_max, H;
+    int h_f32, w_f32, unit_offset;
+    float eps;
+    long long h_stride, dx_stride, add_stride, out_stride;
+};
+
+int norm_grad_part_rows(int T_max, int H, bool h_f32);
+cudaError_t launch_norm_backward(const NormGradArgs &a, cudaStream_t stream);
+
+struct RouteGradArgs {
+    const float *logits;       // [T_max, E]
+    const int32_t *ids;        // [T_max, k]
+    const float *d_weights;    // [T_max, k]
+    const float *d_logits_add; // [T_max, E] or null
+    const int32_t *d_num_tokens;
+    float *d_logits;           // [T_max, E] or null
+    void *parts;               // [T_max, 2 Ep] bf16, Ep = E rounded up to 64: leading parts, then rests
+    int32_t *offsets;          // [segments + 1]: the segments' token ranges
+    int32_t *err;
+    int T_max, E, k;
+    int sigmoid, renormalize;
+    int segments, segment_rows;
+    float scale;
+};
+
+cudaError_t launch_route_grad(const RouteGradArgs &a, int num_sms, cudaStream_t stream);
+// out[i] = sum_s part[s * n + i] in fp32, s ascending, stored as fp32 or bf16; n a multiple of 8
+cudaError_t launch_sum_parts(const float *part, int parts, size_t n, void *out, bool f32, int num_sms,
+                             cudaStream_t stream);
+
 // 2-D bf16 tensor map [rows, cols] (cols contiguous), box of 64 columns x
 // box_rows rows, 128-byte swizzle (grouped_gemm.cu).
 bool make_tile_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
@@ -381,6 +463,9 @@ int device_sm_count();
 
 // host validation shared by the entry points (moe_api.cu)
 moe_status_t validate_problem(const moe_problem_t *problem);
+// (block_api.cu)
+moe_status_t validate_norm(const moe_norm_problem_t *problem);
+moe_status_t validate_router(const moe_router_problem_t *problem);
 // rows of the sorted batch: the problem's capacity, or T_max * k when it is 0
 int capacity_of(const moe_problem_t &problem);
 // blocks of the multi-block dispatch: one per kDispatchSlotsPerBlock routed slots
