@@ -43,12 +43,15 @@ constexpr int kThreads = 256;
 constexpr int kBK = 64;                      // K elements of a stage
 constexpr int kUmmaK = 16;
 constexpr int kTileRows = 256;               // rows of a CTA pair's tile
+constexpr int kSwapRows = 128;               // an expert's last tile of at most this many rows runs swapped
+constexpr int kSwapBox = 32;                 // rows of one of its boxes
 constexpr int kHalf = 128 * 128;             // bytes of one operand's half tile: 128 x 64 bf16
 constexpr int kAtom = 64 * 128;              // bytes of an MN-major block: 64 K rows x 64 columns
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kStages = 6;
-constexpr int kScratch = 4 * 32 * 36 * 4;    // a 32 x 36-word transpose scratch per epilogue warp
-constexpr int kDynSmem = 1024 + kStages * kStageBytes + kScratch;
+constexpr int kStages = 5;
+constexpr int kBox = 32 * 128;               // bytes of an output box: 32 rows x 128 bytes
+constexpr int kBoxes = 3;                    // of each epilogue warp
+constexpr int kDynSmem = 1024 + kStages * kStageBytes + 4 * kBoxes * kBox;
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;   // instruction descriptor: operand is MN-major
 
 // Shared-memory descriptor of an MN-major bf16 tile: blocks of 64 K rows x 64
@@ -71,9 +74,35 @@ __device__ __forceinline__ void fence_proxy_async_shared()
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// A box out of shared memory, stored or (fp32) added; one bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int32_t c0, int32_t c1, bool add)
+{
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(c0), "r"(c1), "r"(src)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(c0), "r"(c1), "r"(src)
+                     : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+// until at most n of this thread's bulk groups still read shared memory
+template <int n>
+__device__ __forceinline__ void bulk_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
+}
+
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // What every thread of a CTA pair's kernel starts from.
 struct PairState {
-    uint8_t *smem;          // stages, 1024-byte aligned
+    uint8_t *smem;          // stages, then the output boxes; 1024-byte aligned
     uint32_t tmem;
     uint32_t rank;
     int cluster, clusters;
@@ -86,11 +115,13 @@ struct PairBars {
     uint64_t tfull[2];
     uint64_t tempty[2];        // used in CTA 0
     uint64_t drain;            // used in CTA 0
+    uint64_t ufull[2], uempty[2];   // batches of units
 };
 
 // Barriers, TMEM, the experts' offsets (clamped to the batch) and their row tiles.
 __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars &bars, uint32_t &s_tmem, int &s_abort,
-                                                int *s_off, int *s_tp, const int32_t *offsets, int E, int cap)
+                                                int *s_off, int *s_tp, const int32_t *offsets, int E, int cap,
+                                                int readers)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     PairState st;
@@ -107,6 +138,8 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars &bar
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&bars.tfull[b]), 1);
             mbar_init(smem_u32(&bars.tempty[b]), 8);   // 4 epilogue warps x 2 CTAs
+            mbar_init(smem_u32(&bars.ufull[b]), 1);
+            mbar_init(smem_u32(&bars.uempty[b]), readers - (st.rank ? 1 : 0));   // the MMA thread reads in CTA 0 only
         }
         mbar_init(smem_u32(&bars.drain), 1);
         s_abort = 0;
@@ -162,12 +195,145 @@ struct Ring {
     }
 };
 
+// ------------------------------------------------------------------ units
+
+// A unit of work, decoded. A warp of its own decodes 32 units at a time, one a
+// lane, into one of two batches in shared memory, and every role reads them
+// from there: decoding takes some 2 us of divisions and searches, which each
+// role spent between two units before (weight gradients of 512 rows an expert,
+// E=128, H=4096, I=1536: 2.8 ms, and with the batches @@).
+struct __align__(16) UnitDesc {
+    int job;             // products: which; -1: no more units
+    int e;
+    int m0, n0;          // first row and column of the output tile
+    int rows;            // output rows of the tile that exist
+    int total;           // K blocks of all parts or phases
+    int period;          // K blocks of one part
+    int rem;             // rows of a part's last K block when that is not whole, else 0
+    int k_row0;          // first K row, where K runs along the batch
+    int swap;            // swapped: rows on the MMA's N side, a multiple of 64; else 0
+    int pad[2];
+};
+
+constexpr int kBatch = 32;
+
+struct UnitReader {
+    const UnitDesc *units;
+    uint64_t *full, *empty;
+    int i;
+    __device__ __forceinline__ UnitReader(const UnitDesc *u, PairBars &b) : units(u), full(b.ufull), empty(b.uempty), i(0) {}
+    // One thread: the next unit, or null at the end or on give-up.
+    __device__ __forceinline__ const UnitDesc *next(volatile int *abort, uint64_t limit_ns)
+    {
+        const int b = (i / kBatch) & 1;
+        if (i % kBatch == 0) {
+            if (i)
+                mbar_arrive(smem_u32(&empty[b ^ 1]));    // the batch before has been used
+            if (!mbar_wait_bounded(smem_u32(&full[b]), (i / (2 * kBatch)) & 1, abort, limit_ns))
+                return nullptr;
+        }
+        const UnitDesc *u = units + b * kBatch + i % kBatch;
+        ++i;
+        return u->job < 0 ? nullptr : u;
+    }
+    // A warp: lane 0 waits.
+    __device__ __forceinline__ const UnitDesc *next_warp(int lane, volatile int *abort, uint64_t limit_ns)
+    {
+        const int b = (i / kBatch) & 1;
+        if (i % kBatch == 0) {
+            int ok = 0;
+            __syncwarp();
+            if (lane == 0) {
+                if (i)
+                    mbar_arrive(smem_u32(&empty[b ^ 1]));
+                ok = mbar_wait_bounded(smem_u32(&full[b]), (i / (2 * kBatch)) & 1, abort, limit_ns) ? 1 : 0;
+            }
+            if (!__shfl_sync(kFull, ok, 0))
+                return nullptr;
+            __syncwarp();
+        }
+        const UnitDesc *u = units + b * kBatch + i % kBatch;
+        ++i;
+        return u->job < 0 ? nullptr : u;
+    }
+};
+
+// The decoding warp: units st.cluster, st.cluster + st.clusters, ... below `units`.
+template <typename Decode>
+__device__ __forceinline__ void publish_units(const PairState &st, PairBars &bars, UnitDesc *s_units, int units,
+                                              volatile int *abort, uint64_t limit_ns, Decode decode)
+{
+    const int lane = threadIdx.x & 31;
+    long long u = st.cluster + static_cast<long long>(lane) * st.clusters;
+    for (int batch = 0;; ++batch, u += static_cast<long long>(kBatch) * st.clusters) {
+        const int b = batch & 1;
+        int ok = 0;
+        if (lane == 0)
+            ok = mbar_wait_bounded(smem_u32(&bars.uempty[b]), ((batch >> 1) & 1) ^ 1u, abort, limit_ns) ? 1 : 0;
+        if (!__shfl_sync(kFull, ok, 0))
+            return;
+        UnitDesc d = {};
+        d.job = -1;
+        if (u < units)
+            decode(static_cast<int>(u), d);
+        s_units[b * kBatch + lane] = d;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_u32(&bars.ufull[b]));
+        if (__any_sync(kFull, u >= units))
+            return;
+    }
+}
+
+// Rows on the N side of a tile of `rows` rows, or 0: runs as usual.
+__device__ __forceinline__ int swap_rows(int rows) { return rows <= kSwapRows ? (rows + 63) & ~63 : 0; }
+
+// 32 rows x 128 bytes of an epilogue warp's box at `box` (128-byte swizzle),
+// rows [first, first + 32) of a tile with `rows` of them, to element (c0, r0 +
+// first) of `map`; boxes that hold rows past the tile go row by row.
+__device__ __forceinline__ void store_box(uint8_t *box, const CUtensorMap *map, int c0, int r0, int first, int rows,
+                                          void *out, long long ld, int esize, bool add)
+{
+    const int lane = threadIdx.x & 31;
+    if (first >= rows)
+        return;
+    if (first + 32 <= rows) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, smem_u32(box), c0, r0 + first, add);
+            bulk_commit();
+        }
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+        const int rr = 4 * it + (lane >> 3), ch = lane & 7;
+        uint4 v = *reinterpret_cast<const uint4 *>(box + rr * 128 + ((ch ^ (rr & 7)) << 4));
+        if (first + rr < rows) {
+            uint4 *const p = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(out) +
+                                                       ((static_cast<long long>(r0) + first + rr) * ld + c0) * esize + ch * 16);
+            if (add) {
+                const float4 o = *reinterpret_cast<const float4 *>(p);
+                v = make_uint4(__float_as_uint(__uint_as_float(v.x) + o.x), __float_as_uint(__uint_as_float(v.y) + o.y),
+                               __float_as_uint(__uint_as_float(v.z) + o.z), __float_as_uint(__uint_as_float(v.w) + o.w));
+            }
+            *p = v;
+        }
+    }
+    __syncwarp();
+}
+
 // ------------------------------------------------------------------ a and [dg du]
 
 struct ActArgs {
     CUtensorMap x, dy;       // [cap, H], boxes of 64 x 128 rows
+    CUtensorMap x32, dy32;   // the same in boxes of 64 x 32 rows
     CUtensorMap w13;         // [E * 2I, H], boxes of 64 x 128 rows
     CUtensorMap w2;          // [E * H, I], boxes of 64 x 64 rows
+    CUtensorMap act_out;     // [cap, I], boxes of 64 x 32 rows
+    CUtensorMap dgu_out;     // [cap, 2I]
     const int32_t *offsets;
     int32_t *err;
     __nv_bfloat16 *act;      // [cap, I]
@@ -176,29 +342,46 @@ struct ActArgs {
     int E, cap, H, I;
 };
 
-struct ActUnit {
-    int e, row0, rows, n0;
-};
-
-// Column tile, then row tile: the row tiles that share one weight tile go to
-// neighbouring pairs.
-__device__ __forceinline__ ActUnit act_unit(int u, const int *s_off, const int *s_tp, int E, int NT)
+// An expert's units: column tiles of 128 x its whole row tiles, column tile
+// outside (the row tiles that share one weight tile go to neighbouring pairs);
+// then, if its last row tile runs swapped, that tile's columns by 256.
+__device__ __forceinline__ int act_units_of(int rows, int NT, int NT2)
 {
-    ActUnit t;
-    t.e = find_expert(s_tp, E, u, NT);
-    const int local = u - s_tp[t.e] * NT;
-    const int tiles = s_tp[t.e + 1] - s_tp[t.e];
-    const int nt = local / tiles;
-    t.row0 = s_off[t.e] + (local - nt * tiles) * kTileRows;
-    t.rows = min(s_off[t.e + 1] - t.row0, kTileRows);
-    t.n0 = nt * 128;
-    return t;
+    const int tiles = (rows + kTileRows - 1) / kTileRows;
+    const int last = rows - (tiles - 1) * kTileRows;
+    return tiles == 0 ? 0 : (swap_rows(last) ? (tiles - 1) * NT + NT2 : tiles * NT);
 }
 
-// One element's gradients from its gate, up and da values.
+__device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, const int *s_up, int E, int NT)
+{
+    const int e = find_expert(s_up, E, u, 1);
+    const int rows = s_off[e + 1] - s_off[e];
+    int tiles = (rows + kTileRows - 1) / kTileRows;
+    const int last = rows - (tiles - 1) * kTileRows;
+    const int swap = swap_rows(last);
+    const int whole = swap ? tiles - 1 : tiles;
+    const int local = u - s_up[e];
+    d.job = 0;
+    d.e = e;
+    if (local < whole * NT) {
+        const int nt = local / whole;
+        const int rt = local - nt * whole;
+        d.m0 = s_off[e] + rt * kTileRows;
+        d.rows = min(rows - rt * kTileRows, kTileRows);
+        d.n0 = nt * 128;
+    } else {
+        d.m0 = s_off[e] + whole * kTileRows;
+        d.rows = last;
+        d.n0 = (local - whole * NT) * 256;
+        d.swap = swap;
+    }
+}
+
+// One element's gradients from its gate, up and da values. The fast exponential
+// and quotient are off by a few 2^-22, far below the rounding to bf16 behind them.
 __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float &a, float &dg, float &du)
 {
-    const float s = 1.0f / (1.0f + expf(-g));
+    const float s = __fdividef(1.0f, 1.0f + __expf(-g));
     const float silu = g * s;
     a = silu * u;
     du = d * silu;
@@ -206,9 +389,11 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float &a,
 }
 
 // TMEM columns: da of even and odd units in 0..127 and 128..255, gate and up
-// in 256..511. A unit's da comes first, so that it can be multiplied while the
-// unit before is still being read out: a third of the unit's MMAs, which hides
-// that unit's epilogue.
+// in 256..383 and 384..511. A unit's da comes first, so that it can be
+// multiplied while the unit before is still being read out: a third of the
+// unit's MMAs, which hides that unit's epilogue. A swapped unit has 256
+// columns of the intermediate size on the MMA's M side and its rows on N, each
+// of da, gate and up a phase of its own.
 __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_constant__ ActArgs args)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -216,26 +401,30 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ int s_off[kMaxExperts + 1];
-    __shared__ int s_tp[kMaxExperts + 1];
+    __shared__ int s_up[kMaxExperts + 1];
+    __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PairState st = pair_begin(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap);
+    const PairState st = pair_begin(smem_raw, bars, s_tmem, s_abort, s_off, s_up, args.offsets, args.E, args.cap, 6);
     volatile int *abort_flag = &s_abort;
-    const int NT = (args.I + 127) / 128;
-    const int units = s_tp[args.E] * NT;
+    const int NT = (args.I + 127) / 128, NT2 = (args.I + 255) / 256;
     const int k_blocks = args.H / kBK;
+    const int rank = static_cast<int>(st.rank);
 
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol_w = l2_policy_evict_normal();
             const uint64_t pol_a = l2_policy_evict_last();
             Ring r;
+            UnitReader units(s_units, bars);
             bool ok = true;
-            for (int u = st.cluster; ok && u < units; u += st.clusters) {
-                const ActUnit t = act_unit(u, s_off, s_tp, args.E, NT);
-                const int a_row = t.row0 + 128 * static_cast<int>(st.rank);
-                const int w2_row = t.e * args.H;
-                const int w13_row = t.e * 2 * args.I + (st.rank ? args.I : 0) + t.n0;
-                for (int kb = 0; kb < 2 * k_blocks; ++kb, r.next()) {
+            while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
+                const int swap = t->swap, half = swap >> 1, n0 = t->n0;
+                const int a_row = swap ? t->m0 + half * rank : t->m0 + 128 * rank;
+                const int w2_row = t->e * args.H;
+                const int gate = t->e * 2 * args.I + n0;
+                int phase = 0, kp = 0;
+                const int total = (swap ? 3 : 2) * k_blocks;
+                for (int kb = 0; kb < total; ++kb, r.next()) {
                     if (!mbar_wait_bounded(smem_u32(&bars.empty[r.stage]), r.phase ^ 1u, abort_flag,
                                            args.wait_limit_ns)) {
                         ok = false;
@@ -244,15 +433,32 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
                     const uint32_t full = map_to_cta(smem_u32(&bars.full[r.stage]), 0);
                     const uint32_t a_dst = smem_u32(st.smem + r.stage * kStageBytes);
                     const uint32_t b_dst = a_dst + kHalf;
-                    if (kb < k_blocks) {
-                        mbar_arrive_expect_tx_cluster(full, kHalf + kAtom);
-                        tma_load_2d_pair(a_dst, &args.dy, full, kb * kBK, a_row, pol_a);
-                        tma_load_2d_pair(b_dst, &args.w2, full, t.n0 + 64 * static_cast<int>(st.rank),
-                                         w2_row + kb * kBK, pol_w);
+                    const int kc = kp * kBK;
+                    if (!swap) {
+                        if (phase == 0) {
+                            mbar_arrive_expect_tx_cluster(full, kHalf + kAtom);
+                            tma_load_2d_pair(a_dst, &args.dy, full, kc, a_row, pol_a);
+                            tma_load_2d_pair(b_dst, &args.w2, full, n0 + 64 * rank, w2_row + kc, pol_w);
+                        } else {
+                            mbar_arrive_expect_tx_cluster(full, kStageBytes);
+                            tma_load_2d_pair(a_dst, &args.x, full, kc, a_row, pol_a);
+                            tma_load_2d_pair(b_dst, &args.w13, full, kc, gate + (rank ? args.I : 0), pol_w);
+                        }
                     } else {
-                        mbar_arrive_expect_tx_cluster(full, kStageBytes);
-                        tma_load_2d_pair(a_dst, &args.x, full, (kb - k_blocks) * kBK, a_row, pol_a);
-                        tma_load_2d_pair(b_dst, &args.w13, full, (kb - k_blocks) * kBK, w13_row, pol_w);
+                        mbar_arrive_expect_tx_cluster(full, kHalf + half * 128);
+                        if (phase == 0) {
+                            tma_load_2d_pair(a_dst, &args.w2, full, n0 + 128 * rank, w2_row + kc, pol_w);
+                            tma_load_2d_pair(a_dst + kAtom, &args.w2, full, n0 + 128 * rank + 64, w2_row + kc, pol_w);
+                        } else {
+                            tma_load_2d_pair(a_dst, &args.w13, full, kc, gate + (phase == 2 ? args.I : 0) + 128 * rank, pol_w);
+                        }
+                        const CUtensorMap *m = phase == 0 ? &args.dy32 : &args.x32;
+                        for (int i = 0; i < half; i += kSwapBox)
+                            tma_load_2d_pair(b_dst + i * 128, m, full, kc, a_row + i, pol_a);
+                    }
+                    if (++kp == k_blocks) {
+                        kp = 0;
+                        ++phase;
                     }
                 }
             }
@@ -260,52 +466,80 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0 && st.rank == 0) {
-            constexpr uint32_t kIdescDa = idesc_bf16_f32(256, 128) | kMajorB;
-            constexpr uint32_t kIdescGu = idesc_bf16_f32(256, 256);
             Ring r;
+            UnitReader units(s_units, bars);
             bool ok = true;
             int local = 0;
-            for (int u = st.cluster; ok && u < units; u += st.clusters, ++local) {
-                for (int kb = 0; kb < 2 * k_blocks; ++kb, r.next()) {
-                    const bool da = kb < k_blocks;
-                    if (kb == k_blocks) {
-                        // gate and up of the unit before have been read (and with them the da before that)
-                        if (!mbar_wait_bounded(smem_u32(&bars.tempty[0]), (local & 1) ^ 1u, abort_flag,
-                                               args.wait_limit_ns)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                    if (!mbar_wait_bounded(smem_u32(&bars.full[r.stage]), r.phase, abort_flag, args.wait_limit_ns)) {
+            while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
+                const int swap = t->swap;
+                const int phases = swap ? 3 : 2;
+                for (int phase = 0; ok && phase < phases; ++phase) {
+                    // gate and up of the unit before have been read (and with them the da before that)
+                    if (phase == 1 && !mbar_wait_bounded(smem_u32(&bars.tempty[0]), (local & 1) ^ 1u, abort_flag,
+                                                         args.wait_limit_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
-                    const uint32_t b_addr = a_addr + kHalf;
-                    const uint32_t d = st.tmem + (da ? 128 * (local & 1) : 256);
-                    const bool first = kb == 0 || kb == k_blocks;
+                    const uint32_t d = st.tmem + (phase == 0 ? 128 * (local & 1) : 128 + 128 * phase);
+                    // K advances 16 elements a step: 32 bytes of a K-major tile, 2048 of an MN-major one
+                    const bool a_mn = swap && phase == 0, b_mn = !swap && phase == 0;
+                    const uint32_t idesc = swap ? idesc_bf16_f32(256, swap) | (a_mn ? kMajorA : 0u)
+                                                : (b_mn ? idesc_bf16_f32(256, 128) | kMajorB : idesc_bf16_f32(256, 256));
+                    for (int kb = 0; kb < k_blocks; ++kb, r.next()) {
+                        if (!mbar_wait_bounded(smem_u32(&bars.full[r.stage]), r.phase, abort_flag, args.wait_limit_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
+                        const uint32_t b_addr = a_addr + kHalf;
+                        const uint64_t a0 = a_mn ? smem_desc_mnmajor_sw128(a_addr) : smem_desc_kmajor_sw128(a_addr);
+                        const uint64_t b0 = b_mn ? smem_desc_mnmajor_sw128(b_addr) : smem_desc_kmajor_sw128(b_addr);
+                        const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
-                    for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
-                        const uint64_t b_desc = da ? smem_desc_mnmajor_sw128(b_addr + kk * 2048)
-                                                   : smem_desc_kmajor_sw128(b_addr + kk * 32);
-                        umma_bf16_pair(d, smem_desc_kmajor_sw128(a_addr + kk * 32), b_desc, da ? kIdescDa : kIdescGu,
-                                       (first && kk == 0) ? 0u : 1u);
+                        for (int kk = 0; kk < kBK / kUmmaK; ++kk)
+                            umma_bf16_pair(d, a0 + kk * sa, b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                     }
-                    umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (ok)
                     umma_commit_pair(smem_u32(&bars.tfull[0]), 0x3);
+                ++local;
             }
             umma_commit_pair(smem_u32(&bars.drain), 0x1);
             mbar_drain(smem_u32(&bars.drain), 0, args.wait_limit_ns);
         }
         __syncwarp();
+    } else if (warp == 2) {
+        // s_up so far counts row tiles; the units of each expert need the rows of its last tile too
+        int carry = 0;
+        for (int base = 0; base < args.E; base += 32) {
+            const int e = base + lane;
+            int n = e < args.E ? act_units_of(max(s_off[e + 1] - s_off[e], 0), NT, NT2) : 0, v = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int w = __shfl_up_sync(kFull, v, o);
+                if (lane >= o)
+                    v += w;
+            }
+            if (e < args.E)
+                s_up[e] = carry + v - n;
+            carry += __shfl_sync(kFull, v, 31);
+        }
+        if (lane == 0)
+            s_up[args.E] = carry;
+        __syncwarp();
+        publish_units(st, bars, s_units, carry, abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
+            act_unit(u, d, s_off, s_up, args.E, NT);
+        });
     } else if (warp >= 4) {
         const int q = warp - 4;
+        uint8_t *const boxes = st.smem + kStages * kStageBytes + q * kBoxes * kBox;
+        UnitReader units(s_units, bars);
         int local = 0;
-        for (int u = st.cluster; u < units; u += st.clusters, ++local) {
-            const ActUnit t = act_unit(u, s_off, s_tp, args.E, NT);
+        for (; const UnitDesc *tp = units.next_warp(lane, abort_flag, args.wait_limit_ns); ++local) {
+            const UnitDesc t = *tp;
             int ok = 0;
             if (lane == 0)
                 ok = mbar_wait_bounded(smem_u32(&bars.tfull[0]), local & 1, abort_flag, args.wait_limit_ns) ? 1 : 0;
@@ -314,38 +548,68 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
             tc_fence_after();
             const uint32_t lanes = st.tmem + (static_cast<uint32_t>(q * 32) << 16);
             const uint32_t t_da = lanes + 128 * (local & 1), t_gu = lanes + 256;
-            const int r = 128 * static_cast<int>(st.rank) + q * 32 + lane;
-            const bool valid = r < t.rows;
-            const size_t row = static_cast<size_t>(t.row0 + r);
-            __nv_bfloat16 *const act = args.act + row * args.I + t.n0;
-            __nv_bfloat16 *const dg = args.dgu + row * 2 * args.I + t.n0;
-            __nv_bfloat16 *const du = dg + args.I;
-            const int cols = args.I - t.n0;
+            if (!t.swap) {
+                const int first = 128 * rank + q * 32;
+                const int cols = min(args.I - t.n0, 128);     // a multiple of 64
 #pragma unroll 1
-            for (int c = 0; c < 128 && c < cols; c += 16) {
-                uint32_t vg[16], vu[16], vd[16];
-                tmem_ld_32x32b_x16(t_gu + c, vg);
-                tmem_ld_32x32b_x16(t_gu + 128 + c, vu);
-                tmem_ld_32x32b_x16(t_da + c, vd);
-                tmem_wait_ld();
-                uint32_t oa[8], og[8], ou[8];
+                for (int c = 0; c < cols; c += 64) {
+                    if (lane == 0)
+                        bulk_wait_read<0>();
+                    __syncwarp();
+#pragma unroll 1
+                    for (int cc = 0; cc < 64; cc += 16) {
+                        uint32_t vg[16], vu[16], vd[16];
+                        tmem_ld_32x32b_x16(t_gu + c + cc, vg);
+                        tmem_ld_32x32b_x16(t_gu + 128 + c + cc, vu);
+                        tmem_ld_32x32b_x16(t_da + c + cc, vd);
+                        tmem_wait_ld();
+                        uint32_t o[3][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float a[2], g[2], w[2];
+                        for (int i = 0; i < 8; ++i) {
+                            float a[2], g[2], w[2];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        swiglu_grad(__uint_as_float(vg[2 * i + j]), __uint_as_float(vu[2 * i + j]),
-                                    __uint_as_float(vd[2 * i + j]), a[j], g[j], w[j]);
-                    oa[i] = pack_bf16x2(a[0], a[1]);
-                    og[i] = pack_bf16x2(g[0], g[1]);
-                    ou[i] = pack_bf16x2(w[0], w[1]);
+                            for (int j = 0; j < 2; ++j)
+                                swiglu_grad(__uint_as_float(vg[2 * i + j]), __uint_as_float(vu[2 * i + j]),
+                                            __uint_as_float(vd[2 * i + j]), a[j], g[j], w[j]);
+                            o[0][i] = pack_bf16x2(a[0], a[1]);
+                            o[1][i] = pack_bf16x2(g[0], g[1]);
+                            o[2][i] = pack_bf16x2(w[0], w[1]);
+                        }
+#pragma unroll
+                        for (int b = 0; b < 3; ++b)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                *reinterpret_cast<uint4 *>(boxes + b * kBox + lane * 128 + (((cc / 8 + i) ^ (lane & 7)) << 4)) =
+                                    make_uint4(o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]);
+                    }
+                    const int n = t.n0 + c;
+                    store_box(boxes, &args.act_out, n, t.m0, first, t.rows, args.act, args.I, 2, false);
+                    store_box(boxes + kBox, &args.dgu_out, n, t.m0, first, t.rows, args.dgu, 2LL * args.I, 2, false);
+                    store_box(boxes + 2 * kBox, &args.dgu_out, args.I + n, t.m0, first, t.rows, args.dgu, 2LL * args.I, 2, false);
                 }
-                if (valid) {
+            } else {
+                // lane = column, TMEM columns = the unit's rows
+                const int n = t.n0 + 128 * rank + q * 32 + lane;
+                const bool col_ok = n < args.I;
+                __nv_bfloat16 *const act = args.act + static_cast<size_t>(t.m0) * args.I + n;
+                __nv_bfloat16 *const dgu = args.dgu + static_cast<size_t>(t.m0) * 2 * args.I + n;
+#pragma unroll 1
+                for (int c = 0; c < t.rows; c += 16) {
+                    uint32_t vg[16], vu[16], vd[16];
+                    tmem_ld_32x32b_x16(t_gu + c, vg);
+                    tmem_ld_32x32b_x16(t_gu + 128 + c, vu);
+                    tmem_ld_32x32b_x16(t_da + c, vd);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        reinterpret_cast<uint4 *>(act + c)[i] = make_uint4(oa[4 * i], oa[4 * i + 1], oa[4 * i + 2], oa[4 * i + 3]);
-                        reinterpret_cast<uint4 *>(dg + c)[i] = make_uint4(og[4 * i], og[4 * i + 1], og[4 * i + 2], og[4 * i + 3]);
-                        reinterpret_cast<uint4 *>(du + c)[i] = make_uint4(ou[4 * i], ou[4 * i + 1], ou[4 * i + 2], ou[4 * i + 3]);
+                    for (int i = 0; i < 16; ++i) {
+                        float a, g, w;
+                        swiglu_grad(__uint_as_float(vg[i]), __uint_as_float(vu[i]), __uint_as_float(vd[i]), a, g, w);
+                        if (col_ok && c + i < t.rows) {
+                            const size_t r = static_cast<size_t>(c + i);
+                            act[r * args.I] = __float2bfloat16_rn(a);
+                            dgu[r * 2 * args.I] = __float2bfloat16_rn(g);
+                            dgu[r * 2 * args.I + args.I] = __float2bfloat16_rn(w);
+                        }
                     }
                 }
             }
@@ -354,23 +618,19 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
             if (lane == 0)
                 mbar_arrive_cluster(map_to_cta(smem_u32(&bars.tempty[0]), 0));
         }
+        if (lane == 0)
+            bulk_wait_all();
+        __syncwarp();
     }
     pair_end(st, s_abort, args.err);
 }
 
 // ------------------------------------------------------------------ products
 
-struct ProductUnit {
-    int job, e;
-    int m0, rows;        // first output row (rows kind: of the sorted batch) and how many of the 256 there are
-    int n0;
-    int k_blocks, rem;   // K blocks of one part; rows of its last block when that is not whole, else 0
-    int k_row0;          // weights kind: first K row
-};
-
 struct ProductArgs {
     ProductJob job[3];
-    CUtensorMap map[6];      // A and B of each job
+    CUtensorMap a[3], b[3], out[3];
+    CUtensorMap a32[3];      // rows kind: A in boxes of 32 rows
     const int32_t *offsets;
     int32_t *err;
     uint64_t wait_limit_ns;
@@ -383,55 +643,56 @@ __device__ __forceinline__ int job_units(const ProductJob &j, const int *s_tp, i
     return j.by_rows ? s_tp[E] * NT : E * ((j.M + 255) / 256) * NT;
 }
 
-__device__ __forceinline__ ProductUnit product_unit(int u, const ProductArgs &args, const int *s_off, const int *s_tp)
+__device__ __forceinline__ void product_unit(int u, UnitDesc &d, const ProductArgs &args, const int *s_off,
+                                             const int *s_tp)
 {
-    ProductUnit t;
-    t.job = 0;
-    for (; t.job + 1 < args.jobs; ++t.job) {
-        const int n = job_units(args.job[t.job], s_tp, args.E);
+    int job = 0;
+    for (; job + 1 < args.jobs; ++job) {
+        const int n = job_units(args.job[job], s_tp, args.E);
         if (u < n)
             break;
         u -= n;
     }
-    const ProductJob &j = args.job[t.job];
+    const ProductJob &j = args.job[job];
     const int NT = (j.N + 255) / 256;
+    d.job = job;
     if (j.by_rows) {
         const int rt = u / NT;
-        t.n0 = (u - rt * NT) * 256;
-        t.e = find_expert(s_tp, args.E, rt, 1);
-        t.m0 = s_off[t.e] + (rt - s_tp[t.e]) * kTileRows;
-        t.rows = min(s_off[t.e + 1] - t.m0, kTileRows);
-        t.k_blocks = j.k_blocks;
-        t.rem = 0;
-        t.k_row0 = 0;
+        d.n0 = (u - rt * NT) * 256;
+        d.e = find_expert(s_tp, args.E, rt, 1);
+        d.m0 = s_off[d.e] + (rt - s_tp[d.e]) * kTileRows;
+        d.rows = min(s_off[d.e + 1] - d.m0, kTileRows);
+        d.total = j.k_blocks;
+        d.period = j.wrap;
+        d.swap = swap_rows(d.rows);
     } else {
         const int MT = (j.M + 255) / 256;
-        t.e = u / (MT * NT);
-        u -= t.e * MT * NT;
+        d.e = u / (MT * NT);
+        u -= d.e * MT * NT;
         const int mt = u / NT;
-        t.m0 = mt * 256;
-        t.n0 = (u - mt * NT) * 256;
-        t.rows = min(j.M - t.m0, 256);
-        const int k = max(s_off[t.e + 1] - s_off[t.e], 0);
-        t.k_blocks = (k + kBK - 1) / kBK;
-        t.rem = k % kBK;
-        t.k_row0 = s_off[t.e];
+        d.m0 = mt * 256;
+        d.n0 = (u - mt * NT) * 256;
+        d.rows = min(j.M - d.m0, 256);
+        const int k = max(s_off[d.e + 1] - s_off[d.e], 0);
+        d.period = (k + kBK - 1) / kBK;
+        d.total = d.period * j.parts;
+        d.rem = k % kBK;
+        d.k_row0 = s_off[d.e];
     }
-    return t;
 }
 
-// Rows m0 + 128 rank + 32 q .. + 31 of a tile out of TMEM (or zeros) into
-// [*, ld] memory at `base` + row * ld + n0. Through shared memory, so that 8
-// lanes store 128 whole bytes of one row.
-__device__ __forceinline__ void store_rows(uint32_t t_row, float *scratch, const ProductJob &j, size_t base, int first,
-                                           int rows, int n0, bool zero)
+// A tile's rows first .. first + 31 out of TMEM (or zeros) to memory, one box
+// of 128-byte rows at a time, the warp's boxes in turn.
+__device__ __forceinline__ void store_tile(uint32_t t_row, uint8_t *boxes, int &turn, const ProductJob &j,
+                                           const CUtensorMap *map, int r0, int first, int rows, int n0, bool zero)
 {
     const int lane = threadIdx.x & 31;
     const int cols = min(j.N - n0, 256);     // a multiple of 64
-    uint4 *const mine = reinterpret_cast<uint4 *>(scratch + lane * 36);
     const int step = j.out_f32 ? 32 : 64;
 #pragma unroll 1
     for (int c = 0; c < cols; c += step) {
+        uint8_t *const box = boxes + turn * kBox;
+        turn = turn + 1 == kBoxes ? 0 : turn + 1;
         uint32_t d[32];
         if (zero) {
 #pragma unroll
@@ -441,46 +702,26 @@ __device__ __forceinline__ void store_rows(uint32_t t_row, float *scratch, const
             tmem_ld_32x32b_x32(t_row + c, d);
             tmem_wait_ld();
         } else {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(t_row + c, v);
+            uint32_t v[64];
+            tmem_ld_32x32b_x32(t_row + c, *reinterpret_cast<uint32_t(*)[32]>(v));
+            tmem_ld_32x32b_x32(t_row + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 32; ++i)
                 d[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            tmem_ld_32x32b_x32(t_row + c + 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                d[16 + i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
         }
+        if (lane == 0) {
+            if (first + 32 <= rows)
+                bulk_wait_read<kBoxes - 1>();    // the box's store of kBoxes turns ago has read it
+            else
+                bulk_wait_read<0>();             // turns that go row by row commit no group
+        }
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            mine[i] = make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int it = 0; it < 8; ++it) {
-            const int rr = 4 * it + (lane >> 3);
-            uint4 v = *reinterpret_cast<const uint4 *>(scratch + rr * 36 + (lane & 7) * 4);
-            if (first + rr < rows) {
-                const size_t o = base + static_cast<size_t>(first + rr) * j.ld + n0 + c + (lane & 7) * (step / 8);
-                if (j.out_f32) {
-                    float4 *const p = reinterpret_cast<float4 *>(static_cast<float *>(j.out) + o);
-                    float4 f = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
-                                           __uint_as_float(v.w));
-                    if (j.accumulate) {
-                        const float4 old = *p;
-                        f.x += old.x;
-                        f.y += old.y;
-                        f.z += old.z;
-                        f.w += old.w;
-                    }
-                    *p = f;
-                } else {
-                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(j.out) + o) = v;
-                }
-            }
-        }
-        __syncwarp();
+            *reinterpret_cast<uint4 *>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+        store_box(box, map, n0 + c, r0, first, rows, j.out, j.N, j.out_f32 ? 4 : 2, j.accumulate != 0);
     }
 }
 
@@ -492,27 +733,31 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
     __shared__ int s_abort;
     __shared__ int s_off[kMaxExperts + 1];
     __shared__ int s_tp[kMaxExperts + 1];
+    __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PairState st = pair_begin(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap);
+    const PairState st = pair_begin(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap, 7);
     volatile int *abort_flag = &s_abort;
-    int units = 0;
-    for (int j = 0; j < args.jobs; ++j)
-        units += job_units(args.job[j], s_tp, args.E);
+    const int rank = static_cast<int>(st.rank);
 
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol = l2_policy_evict_normal();
-            const int half = 128 * static_cast<int>(st.rank);
             Ring r;
+            UnitReader units(s_units, bars);
             bool ok = true;
-            for (int u = st.cluster; ok && u < units; u += st.clusters) {
-                const ProductUnit t = product_unit(u, args, s_off, s_tp);
+            while (const UnitDesc *tp = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
+                const UnitDesc t = *tp;
                 const ProductJob &j = args.job[t.job];
-                const CUtensorMap *ma = &args.map[2 * t.job], *mb = ma + 1;
-                const int total = t.k_blocks * (j.by_rows ? 1 : j.parts);
-                int part = 0, kp = 0;     // weights kind: the part, and the K block inside it; rows kind: kp mod wrap
-                const int period = j.by_rows ? j.wrap : t.k_blocks;
-                for (int kb = 0; kb < total; ++kb, r.next()) {
+                const CUtensorMap *ma = &args.a[t.job], *mb = &args.b[t.job], *ma32 = &args.a32[t.job];
+                const bool by_rows = j.by_rows != 0;
+                const int half = t.swap >> 1;
+                const int b_col = t.n0 + 128 * rank;
+                const int a_row = t.m0 + (t.swap ? half : 128) * rank;    // rows kind
+                const int b_row0 = t.e * j.b_expert_rows;
+                int a_col = t.m0 + 128 * rank;                            // weights kind
+                const int part_cols = j.part_cols;
+                int kp = 0;
+                for (int kb = 0; kb < t.total; ++kb, r.next()) {
                     if (!mbar_wait_bounded(smem_u32(&bars.empty[r.stage]), r.phase ^ 1u, abort_flag,
                                            args.wait_limit_ns)) {
                         ok = false;
@@ -521,33 +766,38 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                     const uint32_t full = map_to_cta(smem_u32(&bars.full[r.stage]), 0);
                     const uint32_t a_dst = smem_u32(st.smem + r.stage * kStageBytes);
                     const uint32_t b_dst = a_dst + kHalf;
-                    if (j.by_rows) {
-                        const int b_row = t.e * j.b_expert_rows + kp * kBK;
-                        mbar_arrive_expect_tx_cluster(full, kStageBytes);
-                        tma_load_2d_pair(a_dst, ma, full, kb * kBK, t.m0 + half, pol);
-                        tma_load_2d_pair(b_dst, mb, full, t.n0 + half, b_row, pol);
-                        tma_load_2d_pair(b_dst + kAtom, mb, full, t.n0 + half + 64, b_row, pol);
+                    if (by_rows) {
+                        const int b_row = b_row0 + kp * kBK;
+                        // swapped: B's columns on the MMA's M side
+                        const uint32_t w_dst = t.swap ? a_dst : b_dst;
+                        mbar_arrive_expect_tx_cluster(full, t.swap ? kHalf + half * 128 : kStageBytes);
+                        tma_load_2d_pair(w_dst, mb, full, b_col, b_row, pol);
+                        tma_load_2d_pair(w_dst + kAtom, mb, full, b_col + 64, b_row, pol);
+                        if (!t.swap)
+                            tma_load_2d_pair(a_dst, ma, full, kb * kBK, a_row, pol);
+                        else
+                            for (int i = 0; i < half; i += kSwapBox)
+                                tma_load_2d_pair(b_dst + i * 128, ma32, full, kb * kBK, a_row + i, pol);
                     } else {
-                        const int a_col = t.m0 + half + part * j.part_cols;
                         const int row = t.k_row0 + kp * kBK;
-                        if (t.rem && kp + 1 == t.k_blocks) {
+                        if (t.rem && kp + 1 == t.period) {
                             const uint32_t tail = smem_u32(&bars.tail[r.stage]);
                             mbar_arrive_expect_tx(tail, kStageBytes);
                             tma_load_2d(a_dst, ma, tail, a_col, row, pol);
                             tma_load_2d(a_dst + kAtom, ma, tail, a_col + 64, row, pol);
-                            tma_load_2d(b_dst, mb, tail, t.n0 + half, row, pol);
-                            tma_load_2d(b_dst + kAtom, mb, tail, t.n0 + half + 64, row, pol);
+                            tma_load_2d(b_dst, mb, tail, b_col, row, pol);
+                            tma_load_2d(b_dst + kAtom, mb, tail, b_col + 64, row, pol);
                         } else {
                             mbar_arrive_expect_tx_cluster(full, kStageBytes);
                             tma_load_2d_pair(a_dst, ma, full, a_col, row, pol);
                             tma_load_2d_pair(a_dst + kAtom, ma, full, a_col + 64, row, pol);
-                            tma_load_2d_pair(b_dst, mb, full, t.n0 + half, row, pol);
-                            tma_load_2d_pair(b_dst + kAtom, mb, full, t.n0 + half + 64, row, pol);
+                            tma_load_2d_pair(b_dst, mb, full, b_col, row, pol);
+                            tma_load_2d_pair(b_dst + kAtom, mb, full, b_col + 64, row, pol);
                         }
                     }
-                    if (++kp == period) {
+                    if (++kp == t.period) {
                         kp = 0;
-                        ++part;
+                        a_col += part_cols;
                     }
                 }
             }
@@ -556,13 +806,17 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
     } else if (warp == 1) {
         if (lane == 0 && st.rank == 0) {
             Ring r;
+            UnitReader units(s_units, bars);
             bool ok = true;
             int local = 0;
-            for (int u = st.cluster; ok && u < units; u += st.clusters, ++local) {
-                const ProductUnit t = product_unit(u, args, s_off, s_tp);
-                const ProductJob &j = args.job[t.job];
-                const int total = t.k_blocks * (j.by_rows ? 1 : j.parts);
-                const uint32_t idesc = idesc_bf16_f32(256, 256) | kMajorB | (j.by_rows ? 0u : kMajorA);
+            while (const UnitDesc *tp = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
+                const int total = tp->total, period = tp->period, rem = tp->rem, swap = tp->swap;
+                const bool by_rows = args.job[tp->job].by_rows != 0;
+                // rows kind: A K-major, B MN-major, or the other way round when swapped; weights kind: both MN-major
+                const bool a_mn = !by_rows || swap, b_mn = !swap;
+                const uint32_t idesc =
+                    idesc_bf16_f32(256, swap ? swap : 256) | (a_mn ? kMajorA : 0u) | (b_mn ? kMajorB : 0u);
+                const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
                 const int buf = local & 1;
                 if (!mbar_wait_bounded(smem_u32(&bars.tempty[buf]), ((local >> 1) & 1) ^ 1u, abort_flag,
                                        args.wait_limit_ns)) {
@@ -580,42 +834,47 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
                     const uint32_t b_addr = a_addr + kHalf;
-                    const bool last = ++kp == t.k_blocks;
+                    const uint64_t a0 = a_mn ? smem_desc_mnmajor_sw128(a_addr) : smem_desc_kmajor_sw128(a_addr);
+                    const uint64_t b0 = b_mn ? smem_desc_mnmajor_sw128(b_addr) : smem_desc_kmajor_sw128(b_addr);
+                    const bool last = ++kp == period;
                     if (last)
                         kp = 0;
-                    const int steps = (last && t.rem) ? (t.rem + kUmmaK - 1) / kUmmaK : kBK / kUmmaK;
+                    const int steps = (last && rem) ? (rem + kUmmaK - 1) / kUmmaK : kBK / kUmmaK;
 #pragma unroll
                     for (int kk = 0; kk < kBK / kUmmaK; ++kk)
-                        if (kk < steps) {
-                            const uint64_t a_desc = j.by_rows ? smem_desc_kmajor_sw128(a_addr + kk * 32)
-                                                              : smem_desc_mnmajor_sw128(a_addr + kk * 2048);
-                            umma_bf16_pair(d, a_desc, smem_desc_mnmajor_sw128(b_addr + kk * 2048), idesc,
-                                           (kb > 0 || kk > 0) ? 1u : 0u);
-                        }
+                        if (kk < steps)
+                            umma_bf16_pair(d, a0 + kk * sa, b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
                     umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (ok)
                     umma_commit_pair(smem_u32(&bars.tfull[buf]), 0x3);
+                ++local;
             }
             umma_commit_pair(smem_u32(&bars.drain), 0x1);
             mbar_drain(smem_u32(&bars.drain), 0, args.wait_limit_ns);
         }
         __syncwarp();
+    } else if (warp == 2) {
+        int units = 0;
+        for (int j = 0; j < args.jobs; ++j)
+            units += job_units(args.job[j], s_tp, args.E);
+        publish_units(st, bars, s_units, units, abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
+            product_unit(u, d, args, s_off, s_tp);
+        });
     } else if (warp == 3) {
         // the rows of a partial last K block that no longer belong to the expert
         Ring r;
+        UnitReader units(s_units, bars);
         uint32_t parity = 0;      // of each stage's tail barrier
         bool ok = true;
-        for (int u = st.cluster; ok && u < units; u += st.clusters) {
-            const ProductUnit t = product_unit(u, args, s_off, s_tp);
-            const ProductJob &j = args.job[t.job];
-            const int total = t.k_blocks * (j.by_rows ? 1 : j.parts);
+        while (const UnitDesc *tp = ok ? units.next_warp(lane, abort_flag, args.wait_limit_ns) : nullptr) {
+            const int total = tp->total, period = tp->period, rem = tp->rem;
             int kp = 0;
-            for (int kb = 0; ok && kb < total; ++kb, r.next()) {
-                if (++kp != t.k_blocks)
+            for (int kb = 0; kb < total; ++kb, r.next()) {
+                if (++kp != period)
                     continue;
                 kp = 0;
-                if (!t.rem)
+                if (!rem)
                     continue;
                 int got = 0;
                 if (lane == 0)
@@ -629,11 +888,11 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                 }
                 parity ^= 1u << r.stage;
                 uint4 *const s = reinterpret_cast<uint4 *>(st.smem + r.stage * kStageBytes);
-                const int n = ((t.rem + kUmmaK - 1) / kUmmaK * kUmmaK - t.rem) * 8;   // 16-byte words of a block to zero
-                for (int i = lane; i < 4 * n; i += 32) {
-                    const int block = i / n;
-                    s[block * (kAtom / 16) + t.rem * 8 + (i - block * n)] = make_uint4(0u, 0u, 0u, 0u);
-                }
+                const int n = ((rem + kUmmaK - 1) / kUmmaK * kUmmaK - rem) * 8;   // 16-byte words of a block to zero
+                for (int i = lane; i < n; i += 32)
+#pragma unroll
+                    for (int block = 0; block < 4; ++block)
+                        s[block * (kAtom / 16) + rem * 8 + i] = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0)
@@ -642,10 +901,11 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
         }
     } else if (warp >= 4) {
         const int q = warp - 4;
-        float *const scratch = reinterpret_cast<float *>(st.smem + kStages * kStageBytes) + q * 32 * 36;
-        int local = 0;
-        for (int u = st.cluster; u < units; u += st.clusters, ++local) {
-            const ProductUnit t = product_unit(u, args, s_off, s_tp);
+        uint8_t *const boxes = st.smem + kStages * kStageBytes + q * kBoxes * kBox;
+        UnitReader units(s_units, bars);
+        int local = 0, turn = 0;
+        for (; const UnitDesc *tp = units.next_warp(lane, abort_flag, args.wait_limit_ns); ++local) {
+            const UnitDesc t = *tp;
             const ProductJob &j = args.job[t.job];
             const int buf = local & 1;
             int ok = 0;
@@ -655,14 +915,39 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                 break;
             tc_fence_after();
             const uint32_t t_row = st.tmem + buf * 256 + (static_cast<uint32_t>(q * 32) << 16);
-            const size_t base = (j.by_rows ? 0 : static_cast<size_t>(t.e) * j.expert_stride) + static_cast<size_t>(t.m0) * j.ld;
-            if (t.k_blocks || !j.accumulate)
-                store_rows(t_row, scratch, j, base, 128 * static_cast<int>(st.rank) + q * 32, t.rows, t.n0, t.k_blocks == 0);
+            if (!t.swap) {
+                const int r0 = t.m0 + (j.by_rows ? 0 : t.e * j.M);
+                if (t.total || !j.accumulate)
+                    store_tile(t_row, boxes, turn, j, &args.out[t.job], r0, 128 * rank + q * 32, t.rows, t.n0, t.total == 0);
+            } else {
+                // lane = column, TMEM columns = the unit's rows
+                const int col = t.n0 + 128 * rank + q * 32 + lane;
+                const bool col_ok = col < j.N;
+#pragma unroll 1
+                for (int c = 0; c < t.rows; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(t_row + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (!col_ok || c + i >= t.rows)
+                            continue;
+                        const size_t o = static_cast<size_t>(t.m0 + c + i) * j.N + col;
+                        if (j.out_f32)
+                            static_cast<float *>(j.out)[o] = __uint_as_float(v[i]);
+                        else
+                            static_cast<__nv_bfloat16 *>(j.out)[o] = __float2bfloat16_rn(__uint_as_float(v[i]));
+                    }
+                }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive_cluster(map_to_cta(smem_u32(&bars.tempty[buf]), 0));
         }
+        if (lane == 0)
+            bulk_wait_all();
+        __syncwarp();
     }
     pair_end(st, s_abort, args.err);
 }
@@ -723,9 +1008,13 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
     for (int i = 0; i < n; ++i) {
         const ProductJob &j = jobs[i];
         a.job[i] = j;
-        if (!make_tile_map(&a.map[2 * i], j.a, static_cast<uint64_t>(j.a_rows), static_cast<uint64_t>(j.a_cols),
-                           j.by_rows ? 128 : 64) ||
-            !make_tile_map(&a.map[2 * i + 1], j.b, static_cast<uint64_t>(j.b_rows), static_cast<uint64_t>(j.b_cols), 64))
+        const uint64_t a_rows = j.a_rows, a_cols = j.a_cols;
+        const uint64_t out_rows = j.by_rows ? static_cast<uint64_t>(cap) : static_cast<uint64_t>(E) * j.M;
+        if (!make_tile_map(&a.a[i], j.a, a_rows, a_cols, j.by_rows ? 128 : 64) ||
+            (j.by_rows && !make_tile_map(&a.a32[i], j.a, a_rows, a_cols, kSwapBox)) ||
+            !make_tile_map(&a.b[i], j.b, static_cast<uint64_t>(j.b_rows), static_cast<uint64_t>(j.b_cols), 64) ||
+            !(j.out_f32 ? make_tile_map_f32(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32)
+                        : make_tile_map(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32)))
             return cudaErrorInvalidValue;
         units += product_units(j, E, cap);
     }
@@ -745,7 +1034,9 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
     ActArgs a = {};
     const uint64_t rows = cap, h = H, i = I, e = E;
     if (!make_tile_map(&a.x, x, rows, h, 128) || !make_tile_map(&a.dy, dy, rows, h, 128) ||
-        !make_tile_map(&a.w13, W13, e * 2 * i, h, 128) || !make_tile_map(&a.w2, W2, e * h, i, 64))
+        !make_tile_map(&a.x32, x, rows, h, kSwapBox) || !make_tile_map(&a.dy32, dy, rows, h, kSwapBox) ||
+        !make_tile_map(&a.w13, W13, e * 2 * i, h, 128) || !make_tile_map(&a.w2, W2, e * h, i, 64) ||
+        !make_tile_map(&a.act_out, act, rows, i, 32) || !make_tile_map(&a.dgu_out, dgu, rows, 2 * i, 32))
         return cudaErrorInvalidValue;
     a.offsets = offsets;
     a.err = err;

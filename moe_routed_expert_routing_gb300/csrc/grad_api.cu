@@ -240,7 +240,6 @@ moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const
         j.parts = 1;
         j.out = dx_sorted;
         j.out_f32 = problem->dx_dtype == MOE_DTYPE_FP32;
-        j.ld = p.H;
         jobs[n++] = j;
     }
     ProductJob w = {};
@@ -257,8 +256,6 @@ moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const
         j.M = 2 * p.I;
         j.N = p.H;
         j.out = dW13;
-        j.ld = p.H;
-        j.expert_stride = 2 * static_cast<size_t>(p.I) * p.H;
         jobs[n++] = j;
     }
     if (dW2) {
@@ -270,8 +267,6 @@ moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const
         j.M = p.H;
         j.N = p.I;
         j.out = dW2;
-        j.ld = p.I;
-        j.expert_stride = static_cast<size_t>(p.H) * p.I;
         jobs[n++] = j;
     }
     return cuda_status(launch_products(jobs, n, expert_offsets, p.E, cap, err, sms, s));
@@ -399,8 +394,6 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
         j.part_cols = Ep;
         j.out = seg.segments > 1 ? at<void>(ws, L.sums) : dw_router;
         j.out_f32 = seg.segments > 1 || dw_dtype == MOE_DTYPE_FP32;
-        j.ld = p.H;
-        j.expert_stride = static_cast<size_t>(p.E) * p.H;
         jobs[n++] = j;
     }
     if (dx) {
@@ -417,7 +410,6 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
         j.wrap = Ep / 64;
         j.parts = 1;
         j.out = dx;
-        j.ld = p.H;
         jobs[n++] = j;
     }
     if (n && (st = cuda_status(launch_products(jobs, n, a.offsets, seg.segments, p.T_max, a.err, sms, s))) != MOE_OK)

@@ -394,7 +394,7 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
 // [offsets[e], offsets[e + 1]):
 //  by_rows:  out[r, n] = sum_k a[r, k] b[e * b_expert_rows + k mod (64 wrap), n], r in R_e, k < 64 k_blocks
 //  else:     out[e, m, n] = sum_{p < parts} sum_{r in R_e} a[r, m + p part_cols] b[r, n], m < M
-// for n < N. a [a_rows, a_cols] and b [b_rows, b_cols] row-major; rows of out ld elements apart.
+// for n < N. a [a_rows, a_cols], b [b_rows, b_cols] and out ([cap, N] or [E, M, N]) row-major.
 struct ProductJob {
     int by_rows;
     const void *a, *b;
@@ -405,8 +405,6 @@ struct ProductJob {
     void *out;
     int out_f32;            // fp32, else bf16
     int accumulate;         // fp32, not by_rows: added to what is there
-    long long ld;
-    size_t expert_stride;   // not by_rows: elements between experts
 };
 
 long long product_units(const ProductJob &j, int E, int cap);   // at most, for any offsets
@@ -457,6 +455,8 @@ cudaError_t launch_sum_parts(const float *part, int parts, size_t n, void *out, 
 // 2-D bf16 tensor map [rows, cols] (cols contiguous), box of 64 columns x
 // box_rows rows, 128-byte swizzle (grouped_gemm.cu).
 bool make_tile_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// the same for fp32: boxes of 32 columns
+bool make_tile_map_f32(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 
 // number of SMs of the current device (cached)
 int device_sm_count();
