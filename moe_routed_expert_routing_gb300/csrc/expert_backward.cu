@@ -24,11 +24,15 @@
 // kinds fill the same 16 KB half stages, so one ring serves every unit.
 //
 // Rows behind an expert's last one. As M rows they are multiplied and not
-// stored. As K rows (weight gradients) they must not count: the last K block
-// of an expert with rows % 64 != 0 lands on a barrier of the CTA's own, one
-// warp zeroes the rows up to the next multiple of 16 in both operands (they
-// may hold another expert's rows or, past the valid ones, anything), and the
-// MMAs beyond that multiple are not issued.
+// stored. As K rows (weight gradients) they must not count, whatever they hold:
+// another expert's rows or, past the valid ones, anything. Of an expert's last K
+// block only its own rows are loaded, 16 at a time (the K of one MMA) and the
+// last of them one by one (tile::gather4), filled up to 16 with a row of zeros
+// that the workspace keeps behind a, [dg du] and the router's gradient, against
+// the expert's own last row in the other operand. (Zeroing the rows in shared
+// memory instead, by a warp between the copy and the MMAs, cost about 1 us for
+// every tile of 256 x 256, in a loop that waits for its copies: weight
+// gradients of 512 rows an expert, E=128, H=4096, I=1536, @@.)
 #include <cuda_bf16.h>
 
 #include "moe_internal.h"
@@ -48,10 +52,10 @@ constexpr int kSwapBox = 32;                 // rows of one of its boxes
 constexpr int kHalf = 128 * 128;             // bytes of one operand's half tile: 128 x 64 bf16
 constexpr int kAtom = 64 * 128;              // bytes of an MN-major block: 64 K rows x 64 columns
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kStages = 5;
-constexpr int kBox = 32 * 128;               // bytes of an output box: 32 rows x 128 bytes
-constexpr int kBoxes = 3;                    // of each epilogue warp
-constexpr int kDynSmem = 1024 + kStages * kStageBytes + 4 * kBoxes * kBox;
+constexpr int kStages = 6;
+constexpr int kBox = 32 * 128;               // bytes of an output box: 32 rows x 128 bytes, one of each epilogue warp
+constexpr int kActSmem = 1024 + kStages * kStageBytes;
+constexpr int kProductSmem = kActSmem + 4 * kBox;
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;   // instruction descriptor: operand is MN-major
 
 // Shared-memory descriptor of an MN-major bf16 tile: blocks of 64 K rows x 64
@@ -64,14 +68,28 @@ __device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t saddr)
            static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
 }
 
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_bar)
+// tma_gather4 completing an mbarrier of either CTA of the pair.
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap *map, uint32_t cluster_bar, int32_t c0,
+                                                 const int (&rows)[4], uint64_t policy)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+                 ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(rows[0]), "r"(rows[1]), "r"(rows[2]), "r"(rows[3]),
+                 "r"(cluster_bar), "l"(policy)
+                 : "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async_shared()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// 32 bytes of one row, 32-byte aligned: whole sectors.
+__device__ __forceinline__ void store32(void *p, const uint32_t *v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // A box out of shared memory, stored or (fp32) added; one bulk group.
@@ -91,12 +109,8 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t sr
 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
-// until at most n of this thread's bulk groups still read shared memory
-template <int n>
-__device__ __forceinline__ void bulk_wait_read()
-{
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
-}
+// until this thread's bulk groups have read shared memory
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
@@ -111,7 +125,6 @@ struct PairState {
 struct PairBars {
     uint64_t full[kStages];    // used in CTA 0: one arrival and the bytes of each CTA
     uint64_t empty[kStages];
-    uint64_t tail[kStages];    // a K block whose rows one warp zeroes before it counts as full
     uint64_t tfull[2];
     uint64_t tempty[2];        // used in CTA 0
     uint64_t drain;            // used in CTA 0
@@ -133,7 +146,6 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars &bar
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&bars.full[s]), 2);
             mbar_init(smem_u32(&bars.empty[s]), 1);
-            mbar_init(smem_u32(&bars.tail[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&bars.tfull[b]), 1);
@@ -332,12 +344,10 @@ struct ActArgs {
     CUtensorMap x32, dy32;   // the same in boxes of 64 x 32 rows
     CUtensorMap w13;         // [E * 2I, H], boxes of 64 x 128 rows
     CUtensorMap w2;          // [E * H, I], boxes of 64 x 64 rows
-    CUtensorMap act_out;     // [cap, I], boxes of 64 x 32 rows
-    CUtensorMap dgu_out;     // [cap, 2I]
     const int32_t *offsets;
     int32_t *err;
-    __nv_bfloat16 *act;      // [cap, I]
-    __nv_bfloat16 *dgu;      // [cap, 2I]
+    __nv_bfloat16 *act;      // [cap + 1, I]: the last row is zeros
+    __nv_bfloat16 *dgu;      // [cap + 1, 2I]
     uint64_t wait_limit_ns;
     int E, cap, H, I;
 };
@@ -408,6 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
     volatile int *abort_flag = &s_abort;
     const int NT = (args.I + 127) / 128, NT2 = (args.I + 255) / 256;
     const int k_blocks = args.H / kBK;
+    if (blockIdx.x == 0 && warp == 3) {
+        // the rows of zeros behind a and [dg du]
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = lane; i < args.I / 8; i += 32)
+            reinterpret_cast<uint4 *>(args.act + static_cast<size_t>(args.cap) * args.I)[i] = zero;
+        for (int i = lane; i < args.I / 4; i += 32)
+            reinterpret_cast<uint4 *>(args.dgu + static_cast<size_t>(args.cap) * 2 * args.I)[i] = zero;
+    }
     const int rank = static_cast<int>(st.rank);
 
     if (warp == 0) {
@@ -535,7 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
         });
     } else if (warp >= 4) {
         const int q = warp - 4;
-        uint8_t *const boxes = st.smem + kStages * kStageBytes + q * kBoxes * kBox;
         UnitReader units(s_units, bars);
         int local = 0;
         for (; const UnitDesc *tp = units.next_warp(lane, abort_flag, args.wait_limit_ns); ++local) {
@@ -549,43 +566,35 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
             const uint32_t lanes = st.tmem + (static_cast<uint32_t>(q * 32) << 16);
             const uint32_t t_da = lanes + 128 * (local & 1), t_gu = lanes + 256;
             if (!t.swap) {
-                const int first = 128 * rank + q * 32;
+                const int r = 128 * rank + q * 32 + lane;
+                const bool valid = r < t.rows;
                 const int cols = min(args.I - t.n0, 128);     // a multiple of 64
+                __nv_bfloat16 *const act = args.act + static_cast<size_t>(t.m0 + r) * args.I + t.n0;
+                __nv_bfloat16 *const dgu = args.dgu + static_cast<size_t>(t.m0 + r) * 2 * args.I + t.n0;
 #pragma unroll 1
-                for (int c = 0; c < cols; c += 64) {
-                    if (lane == 0)
-                        bulk_wait_read<0>();
-                    __syncwarp();
-#pragma unroll 1
-                    for (int cc = 0; cc < 64; cc += 16) {
-                        uint32_t vg[16], vu[16], vd[16];
-                        tmem_ld_32x32b_x16(t_gu + c + cc, vg);
-                        tmem_ld_32x32b_x16(t_gu + 128 + c + cc, vu);
-                        tmem_ld_32x32b_x16(t_da + c + cc, vd);
-                        tmem_wait_ld();
-                        uint32_t o[3][8];
+                for (int c = 0; c < cols; c += 16) {
+                    uint32_t vg[16], vu[16], vd[16];
+                    tmem_ld_32x32b_x16(t_gu + c, vg);
+                    tmem_ld_32x32b_x16(t_gu + 128 + c, vu);
+                    tmem_ld_32x32b_x16(t_da + c, vd);
+                    tmem_wait_ld();
+                    uint32_t o[3][8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float a[2], g[2], w[2];
+                    for (int i = 0; i < 8; ++i) {
+                        float a[2], g[2], w[2];
 #pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                swiglu_grad(__uint_as_float(vg[2 * i + j]), __uint_as_float(vu[2 * i + j]),
-                                            __uint_as_float(vd[2 * i + j]), a[j], g[j], w[j]);
-                            o[0][i] = pack_bf16x2(a[0], a[1]);
-                            o[1][i] = pack_bf16x2(g[0], g[1]);
-                            o[2][i] = pack_bf16x2(w[0], w[1]);
-                        }
-#pragma unroll
-                        for (int b = 0; b < 3; ++b)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                *reinterpret_cast<uint4 *>(boxes + b * kBox + lane * 128 + (((cc / 8 + i) ^ (lane & 7)) << 4)) =
-                                    make_uint4(o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]);
+                        for (int j = 0; j < 2; ++j)
+                            swiglu_grad(__uint_as_float(vg[2 * i + j]), __uint_as_float(vu[2 * i + j]),
+                                        __uint_as_float(vd[2 * i + j]), a[j], g[j], w[j]);
+                        o[0][i] = pack_bf16x2(a[0], a[1]);
+                        o[1][i] = pack_bf16x2(g[0], g[1]);
+                        o[2][i] = pack_bf16x2(w[0], w[1]);
                     }
-                    const int n = t.n0 + c;
-                    store_box(boxes, &args.act_out, n, t.m0, first, t.rows, args.act, args.I, 2, false);
-                    store_box(boxes + kBox, &args.dgu_out, n, t.m0, first, t.rows, args.dgu, 2LL * args.I, 2, false);
-                    store_box(boxes + 2 * kBox, &args.dgu_out, args.I + n, t.m0, first, t.rows, args.dgu, 2LL * args.I, 2, false);
+                    if (valid) {   // the workspace is 256-byte aligned, its rows whole 128-byte lines
+                        store32(act + c, o[0]);
+                        store32(dgu + c, o[1]);
+                        store32(dgu + args.I + c, o[2]);
+                    }
                 }
             } else {
                 // lane = column, TMEM columns = the unit's rows
@@ -618,9 +627,6 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
             if (lane == 0)
                 mbar_arrive_cluster(map_to_cta(smem_u32(&bars.tempty[0]), 0));
         }
-        if (lane == 0)
-            bulk_wait_all();
-        __syncwarp();
     }
     pair_end(st, s_abort, args.err);
 }
@@ -630,7 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
 struct ProductArgs {
     ProductJob job[3];
     CUtensorMap a[3], b[3], out[3];
-    CUtensorMap a32[3];      // rows kind: A in boxes of 32 rows
+    CUtensorMap a32[3];             // rows kind: A in boxes of 32 rows
+    CUtensorMap a16[3], b16[3];     // weights kind: both in boxes of 16 rows
+    CUtensorMap a1[3], b1[3];       // and of one row, for gathers
     const int32_t *offsets;
     int32_t *err;
     uint64_t wait_limit_ns;
@@ -682,8 +690,8 @@ __device__ __forceinline__ void product_unit(int u, UnitDesc &d, const ProductAr
 }
 
 // A tile's rows first .. first + 31 out of TMEM (or zeros) to memory, one box
-// of 128-byte rows at a time, the warp's boxes in turn.
-__device__ __forceinline__ void store_tile(uint32_t t_row, uint8_t *boxes, int &turn, const ProductJob &j,
+// of 128-byte rows at a time.
+__device__ __forceinline__ void store_tile(uint32_t t_row, uint8_t *box, const ProductJob &j,
                                            const CUtensorMap *map, int r0, int first, int rows, int n0, bool zero)
 {
     const int lane = threadIdx.x & 31;
@@ -691,8 +699,6 @@ __device__ __forceinline__ void store_tile(uint32_t t_row, uint8_t *boxes, int &
     const int step = j.out_f32 ? 32 : 64;
 #pragma unroll 1
     for (int c = 0; c < cols; c += step) {
-        uint8_t *const box = boxes + turn * kBox;
-        turn = turn + 1 == kBoxes ? 0 : turn + 1;
         uint32_t d[32];
         if (zero) {
 #pragma unroll
@@ -710,12 +716,8 @@ __device__ __forceinline__ void store_tile(uint32_t t_row, uint8_t *boxes, int &
             for (int i = 0; i < 32; ++i)
                 d[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
         }
-        if (lane == 0) {
-            if (first + 32 <= rows)
-                bulk_wait_read<kBoxes - 1>();    // the box's store of kBoxes turns ago has read it
-            else
-                bulk_wait_read<0>();             // turns that go row by row commit no group
-        }
+        if (lane == 0)
+            bulk_wait_read();
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
     __shared__ int s_tp[kMaxExperts + 1];
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PairState st = pair_begin(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap, 7);
+    const PairState st = pair_begin(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap, 6);
     volatile int *abort_flag = &s_abort;
     const int rank = static_cast<int>(st.rank);
 
@@ -781,12 +783,37 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                     } else {
                         const int row = t.k_row0 + kp * kBK;
                         if (t.rem && kp + 1 == t.period) {
-                            const uint32_t tail = smem_u32(&bars.tail[r.stage]);
-                            mbar_arrive_expect_tx(tail, kStageBytes);
-                            tma_load_2d(a_dst, ma, tail, a_col, row, pol);
-                            tma_load_2d(a_dst + kAtom, ma, tail, a_col + 64, row, pol);
-                            tma_load_2d(b_dst, mb, tail, b_col, row, pol);
-                            tma_load_2d(b_dst + kAtom, mb, tail, b_col + 64, row, pol);
+                            // the rows there are, 16 at a time; the last of them row by row, filled up to 16
+                            // with the row of zeros in one operand, the expert's last row in the other
+                            const int slabs = (t.rem + kUmmaK - 1) / kUmmaK, whole = t.rem / kUmmaK;
+                            mbar_arrive_expect_tx_cluster(full, slabs * 4 * kUmmaK * 128);
+                            for (int i = 0; i < whole; ++i) {
+                                const uint32_t o = i * kUmmaK * 128;
+                                const int r16 = row + i * kUmmaK;
+                                tma_load_2d_pair(a_dst + o, &args.a16[t.job], full, a_col, r16, pol);
+                                tma_load_2d_pair(a_dst + kAtom + o, &args.a16[t.job], full, a_col + 64, r16, pol);
+                                tma_load_2d_pair(b_dst + o, &args.b16[t.job], full, b_col, r16, pol);
+                                tma_load_2d_pair(b_dst + kAtom + o, &args.b16[t.job], full, b_col + 64, r16, pol);
+                            }
+                            if (whole < slabs) {
+                                const int last = row + t.rem - 1;
+                                const int fill_a = j.zero_in_a ? args.cap : last, fill_b = j.zero_in_a ? last : args.cap;
+#pragma unroll 1
+                                for (int q = 0; q < kUmmaK / 4; ++q) {
+                                    int ra[4], rb[4];
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const int r0 = row + whole * kUmmaK + 4 * q + i;
+                                        ra[i] = r0 <= last ? r0 : fill_a;
+                                        rb[i] = r0 <= last ? r0 : fill_b;
+                                    }
+                                    const uint32_t o = (whole * kUmmaK + 4 * q) * 128;
+                                    tma_gather4_pair(a_dst + o, &args.a1[t.job], full, a_col, ra, pol);
+                                    tma_gather4_pair(a_dst + kAtom + o, &args.a1[t.job], full, a_col + 64, ra, pol);
+                                    tma_gather4_pair(b_dst + o, &args.b1[t.job], full, b_col, rb, pol);
+                                    tma_gather4_pair(b_dst + kAtom + o, &args.b1[t.job], full, b_col + 64, rb, pol);
+                                }
+                            }
                         } else {
                             mbar_arrive_expect_tx_cluster(full, kStageBytes);
                             tma_load_2d_pair(a_dst, ma, full, a_col, row, pol);
@@ -861,49 +888,11 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
         publish_units(st, bars, s_units, units, abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
             product_unit(u, d, args, s_off, s_tp);
         });
-    } else if (warp == 3) {
-        // the rows of a partial last K block that no longer belong to the expert
-        Ring r;
-        UnitReader units(s_units, bars);
-        uint32_t parity = 0;      // of each stage's tail barrier
-        bool ok = true;
-        while (const UnitDesc *tp = ok ? units.next_warp(lane, abort_flag, args.wait_limit_ns) : nullptr) {
-            const int total = tp->total, period = tp->period, rem = tp->rem;
-            int kp = 0;
-            for (int kb = 0; kb < total; ++kb, r.next()) {
-                if (++kp != period)
-                    continue;
-                kp = 0;
-                if (!rem)
-                    continue;
-                int got = 0;
-                if (lane == 0)
-                    got = mbar_wait_bounded(smem_u32(&bars.tail[r.stage]), (parity >> r.stage) & 1u, abort_flag,
-                                            args.wait_limit_ns)
-                              ? 1
-                              : 0;
-                if (!__shfl_sync(kFull, got, 0)) {
-                    ok = false;
-                    break;
-                }
-                parity ^= 1u << r.stage;
-                uint4 *const s = reinterpret_cast<uint4 *>(st.smem + r.stage * kStageBytes);
-                const int n = ((rem + kUmmaK - 1) / kUmmaK * kUmmaK - rem) * 8;   // 16-byte words of a block to zero
-                for (int i = lane; i < n; i += 32)
-#pragma unroll
-                    for (int block = 0; block < 4; ++block)
-                        s[block * (kAtom / 16) + rem * 8 + i] = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_release_cluster(map_to_cta(smem_u32(&bars.full[r.stage]), 0));
-            }
-        }
     } else if (warp >= 4) {
         const int q = warp - 4;
-        uint8_t *const boxes = st.smem + kStages * kStageBytes + q * kBoxes * kBox;
+        uint8_t *const box = st.smem + kStages * kStageBytes + q * kBox;
         UnitReader units(s_units, bars);
-        int local = 0, turn = 0;
+        int local = 0;
         for (; const UnitDesc *tp = units.next_warp(lane, abort_flag, args.wait_limit_ns); ++local) {
             const UnitDesc t = *tp;
             const ProductJob &j = args.job[t.job];
@@ -918,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
             if (!t.swap) {
                 const int r0 = t.m0 + (j.by_rows ? 0 : t.e * j.M);
                 if (t.total || !j.accumulate)
-                    store_tile(t_row, boxes, turn, j, &args.out[t.job], r0, 128 * rank + q * 32, t.rows, t.n0, t.total == 0);
+                    store_tile(t_row, box, j, &args.out[t.job], r0, 128 * rank + q * 32, t.rows, t.n0, t.total == 0);
             } else {
                 // lane = column, TMEM columns = the unit's rows
                 const int col = t.n0 + 128 * rank + q * 32 + lane;
@@ -957,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
 // Launch a CTA-pair kernel with at most `units` pairs. The attribute and the
 // occupancy are looked up once per host thread, device and kernel.
 template <typename Args>
-cudaError_t launch_pair(void (*kern)(Args), const Args &args, long long units, int num_sms, cudaStream_t stream)
+cudaError_t launch_pair(void (*kern)(Args), const Args &args, int smem, long long units, int num_sms, cudaStream_t stream)
 {
     static thread_local int done_for_device = -1;
     static thread_local int max_clusters = 0;
@@ -972,12 +961,12 @@ cudaError_t launch_pair(void (*kern)(Args), const Args &args, long long units, i
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kDynSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (done_for_device != dev) {
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmem)) != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
             return e;
         cfg.gridDim = dim3(2 * (num_sms / 2));
         int n = 0;
@@ -1010,9 +999,14 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
         a.job[i] = j;
         const uint64_t a_rows = j.a_rows, a_cols = j.a_cols;
         const uint64_t out_rows = j.by_rows ? static_cast<uint64_t>(cap) : static_cast<uint64_t>(E) * j.M;
+        const uint64_t b_rows = j.b_rows, b_cols = j.b_cols;
         if (!make_tile_map(&a.a[i], j.a, a_rows, a_cols, j.by_rows ? 128 : 64) ||
             (j.by_rows && !make_tile_map(&a.a32[i], j.a, a_rows, a_cols, kSwapBox)) ||
-            !make_tile_map(&a.b[i], j.b, static_cast<uint64_t>(j.b_rows), static_cast<uint64_t>(j.b_cols), 64) ||
+            (!j.by_rows && (!make_tile_map(&a.a16[i], j.a, a_rows, a_cols, kUmmaK) ||
+                            !make_tile_map(&a.b16[i], j.b, b_rows, b_cols, kUmmaK) ||
+                            !make_tile_map(&a.a1[i], j.a, a_rows, a_cols, 1) ||
+                            !make_tile_map(&a.b1[i], j.b, b_rows, b_cols, 1))) ||
+            !make_tile_map(&a.b[i], j.b, b_rows, b_cols, 64) ||
             !(j.out_f32 ? make_tile_map_f32(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32)
                         : make_tile_map(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32)))
             return cudaErrorInvalidValue;
@@ -1024,7 +1018,7 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
     a.cap = cap;
     a.err = err;
     a.wait_limit_ns = kWaitLimitNs;
-    return launch_pair(products_kernel, a, units, num_sms, stream);
+    return launch_pair(products_kernel, a, kProductSmem, units, num_sms, stream);
 }
 
 cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, const void *W2, const int32_t *offsets,
@@ -1035,8 +1029,7 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
     const uint64_t rows = cap, h = H, i = I, e = E;
     if (!make_tile_map(&a.x, x, rows, h, 128) || !make_tile_map(&a.dy, dy, rows, h, 128) ||
         !make_tile_map(&a.x32, x, rows, h, kSwapBox) || !make_tile_map(&a.dy32, dy, rows, h, kSwapBox) ||
-        !make_tile_map(&a.w13, W13, e * 2 * i, h, 128) || !make_tile_map(&a.w2, W2, e * h, i, 64) ||
-        !make_tile_map(&a.act_out, act, rows, i, 32) || !make_tile_map(&a.dgu_out, dgu, rows, 2 * i, 32))
+        !make_tile_map(&a.w13, W13, e * 2 * i, h, 128) || !make_tile_map(&a.w2, W2, e * h, i, 64))
         return cudaErrorInvalidValue;
     a.offsets = offsets;
     a.err = err;
@@ -1047,7 +1040,7 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
     a.cap = cap;
     a.H = H;
     a.I = I;
-    return launch_pair(act_grad_kernel, a, (tiles_of(cap) + E) * ((I + 127) / 128), num_sms, stream);
+    return launch_pair(act_grad_kernel, a, kActSmem, (tiles_of(cap) + E) * ((I + 127) / 128), num_sms, stream);
 }
 
 }  // namespace moe

@@ -36,7 +36,7 @@ moe_status_t check_ws(const void *ws, size_t have, size_t need)
 
 // ---- experts ----
 
-// Workspace: the header (error word), a [cap, I] and [dg du] [cap, 2I] in bf16.
+// Workspace: the header (error word), a [cap + 1, I] and [dg du] [cap + 1, 2I] in bf16.
 struct ExpertLayout {
     size_t act, dgu, total;
 };
@@ -46,8 +46,8 @@ ExpertLayout expert_layout(const moe_problem_t &p)
     const size_t cap = static_cast<size_t>(capacity_of(p)), I = static_cast<size_t>(p.I);
     ExpertLayout L;
     L.act = workspace_header_bytes();
-    L.dgu = align_up(L.act + 2 * cap * I);
-    L.total = align_up(L.dgu + 4 * cap * I);
+    L.dgu = align_up(L.act + 2 * (cap + 1) * I);
+    L.total = align_up(L.dgu + 4 * (cap + 1) * I);
     return L;
 }
 
@@ -132,7 +132,7 @@ RouteGradLayout route_grad_layout(const moe_router_problem_t &p)
     RouteGradLayout L;
     L.offsets = workspace_header_bytes();
     L.parts = align_up(L.offsets + sizeof(int32_t) * (s.segments + 1));
-    L.sums = align_up(L.parts + 4 * Ep * static_cast<size_t>(p.T_max));
+    L.sums = align_up(L.parts + 4 * Ep * (static_cast<size_t>(p.T_max) + 1));
     const size_t sums = s.segments > 1 ? sizeof(float) * s.segments * p.E * static_cast<size_t>(p.H) : 0;
     L.total = align_up(L.sums + sums);
     return L;
@@ -250,6 +250,8 @@ moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const
     if (dW13) {
         ProductJob j = w;
         j.a = dgu;
+        j.a_rows = cap + 1LL;
+        j.zero_in_a = 1;
         j.a_cols = 2LL * p.I;
         j.b = x_sorted;
         j.b_cols = p.H;
@@ -263,6 +265,7 @@ moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const
         j.a = dy_sorted;
         j.a_cols = p.H;
         j.b = act;
+        j.b_rows = cap + 1LL;
         j.b_cols = p.I;
         j.M = p.H;
         j.N = p.I;
@@ -382,7 +385,8 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
     if (dw_router) {
         ProductJob j = {};
         j.a = a.parts;
-        j.a_rows = p.T_max;
+        j.a_rows = p.T_max + 1LL;
+        j.zero_in_a = 1;
         j.a_cols = 2LL * Ep;
         j.b = x;
         j.b_rows = p.T_max;

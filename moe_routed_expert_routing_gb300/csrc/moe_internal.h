@@ -385,7 +385,7 @@ cudaError_t launch_dispatch_backward(const void *dx_sorted, bool f32, const int3
                                      const int32_t *d_num_tokens, int T_max, int k, int cap, int H, void *dx, int num_sms,
                                      cudaStream_t stream);
 
-// act[r] = a and dgu[r] = [dg du] of the rows r < offsets[E], bf16 (expert_backward.cu)
+// act[r] = a and dgu[r] = [dg du] of the rows r < offsets[E], bf16, and row `cap` of both = 0 (expert_backward.cu)
 cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, const void *W2, const int32_t *offsets,
                             int E, int cap, int H, int I, void *act, void *dgu, int32_t *err, int num_sms,
                             cudaStream_t stream);
@@ -402,6 +402,7 @@ struct ProductJob {
     int M, N;
     int k_blocks, wrap, b_expert_rows;
     int parts, part_cols;
+    int zero_in_a;          // not by_rows: row `cap` of a (else of b) exists and holds zeros
     void *out;
     int out_f32;            // fp32, else bf16
     int accumulate;         // fp32, not by_rows: added to what is there
@@ -438,7 +439,8 @@ struct RouteGradArgs {
     const float *d_logits_add; // [T_max, E] or null
     const int32_t *d_num_tokens;
     float *d_logits;           // [T_max, E] or null
-    void *parts;               // [T_max, 2 Ep] bf16, Ep = E rounded up to 64: leading parts, then rests
+    void *parts;               // [T_max + 1, 2 Ep] bf16, Ep = E rounded up to 64: leading parts, then rests;
+                               // the last row is set to zeros
     int32_t *offsets;          // [segments + 1]: the segments' token ranges
     int32_t *err;
     int T_max, E, k;

@@ -63,6 +63,9 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
     if (blockIdx.x == 0)
         for (int s = threadIdx.x; s <= a.segments; s += kThreads)
             a.offsets[s] = static_cast<int>(min(static_cast<long long>(T), static_cast<long long>(s) * a.segment_rows));
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < Ep; i += kThreads)     // 2 Ep bf16 zeros
+            reinterpret_cast<uint32_t *>(a.parts)[static_cast<size_t>(a.T_max) * Ep + i] = 0u;
     for (int t = blockIdx.x * (kThreads / 32) + warp; t < T; t += gridDim.x * (kThreads / 32)) {
         const float *const logits = a.logits + static_cast<size_t>(t) * E;
         const int32_t *const ids = a.ids + static_cast<size_t>(t) * k;
