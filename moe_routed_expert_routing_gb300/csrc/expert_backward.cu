@@ -43,7 +43,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kBK = 64;                      // K elements of a stage
 constexpr int kUmmaK = 16;
 constexpr int kTileRows = 256;               // rows of a CTA pair's tile
@@ -52,10 +51,20 @@ constexpr int kSwapBox = 32;                 // rows of one of its boxes
 constexpr int kHalf = 128 * 128;             // bytes of one operand's half tile: 128 x 64 bf16
 constexpr int kAtom = 64 * 128;              // bytes of an MN-major block: 64 K rows x 64 columns
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kStages = 6;
-constexpr int kBox = 32 * 128;               // bytes of an output box: 32 rows x 128 bytes, one of each epilogue warp
-constexpr int kActSmem = 1024 + kStages * kStageBytes;
-constexpr int kProductSmem = kActSmem + 4 * kBox;
+constexpr int kBox = 32 * 128;               // bytes of an output box: 32 rows x 128 bytes
+
+// A kernel's pipeline stages and epilogue warps: four, one for each quarter of
+// the TMEM lanes, or eight, each with half the columns.
+template <int kStages_, int kWarps_, bool kBoxes>
+struct Config {
+    static constexpr int kStages = kStages_, kWarps = kWarps_;
+    static constexpr int kThreads = 128 + 32 * kWarps;
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + (kBoxes ? kWarps * kBox : 0);
+};
+using ActConfig = Config<6, 4, false>;
+using DeepConfig = Config<6, 4, true>;       // products with many K blocks a tile: more copies in flight
+using WideConfig = Config<5, 8, true>;       // with a few: the epilogue is most of the time
+constexpr int kWideBlocks = 8;               // fewer K blocks a tile than this on average
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;   // instruction descriptor: operand is MN-major
 
 // Shared-memory descriptor of an MN-major bf16 tile: blocks of 64 K rows x 64
@@ -122,6 +131,7 @@ struct PairState {
     int cluster, clusters;
 };
 
+template <int kStages>
 struct PairBars {
     uint64_t full[kStages];    // used in CTA 0: one arrival and the bytes of each CTA
     uint64_t empty[kStages];
@@ -132,9 +142,9 @@ struct PairBars {
 };
 
 // Barriers, TMEM, the experts' offsets (clamped to the batch) and their row tiles.
-__device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars &bars, uint32_t &s_tmem, int &s_abort,
-                                                int *s_off, int *s_tp, const int32_t *offsets, int E, int cap,
-                                                int readers)
+template <class C>
+__device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::kStages> &bars, uint32_t &s_tmem, int &s_abort,
+                                                int *s_off, int *s_tp, const int32_t *offsets, int E, int cap)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     PairState st;
@@ -143,15 +153,15 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars &bar
     st.cluster = blockIdx.x >> 1;
     st.clusters = gridDim.x >> 1;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < C::kStages; ++s) {
             mbar_init(smem_u32(&bars.full[s]), 2);
             mbar_init(smem_u32(&bars.empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&bars.tfull[b]), 1);
-            mbar_init(smem_u32(&bars.tempty[b]), 8);   // 4 epilogue warps x 2 CTAs
+            mbar_init(smem_u32(&bars.tempty[b]), 2 * C::kWarps);   // both CTAs' epilogue warps
             mbar_init(smem_u32(&bars.ufull[b]), 1);
-            mbar_init(smem_u32(&bars.uempty[b]), readers - (st.rank ? 1 : 0));   // the MMA thread reads in CTA 0 only
+            mbar_init(smem_u32(&bars.uempty[b]), C::kWarps + (st.rank ? 1 : 2));   // loads, MMAs (CTA 0), epilogue
         }
         mbar_init(smem_u32(&bars.drain), 1);
         s_abort = 0;
@@ -161,7 +171,8 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars &bar
         tmem_alloc_pair(smem_u32(&s_tmem), 512);
         tmem_relinquish_pair();
     }
-    for (int i = threadIdx.x; i <= E; i += kThreads) {
+    pdl_wait();
+    for (int i = threadIdx.x; i <= E; i += C::kThreads) {
         const int o = offsets[i];
         s_off[i] = o < 0 ? 0 : (o > cap ? cap : o);
     }
@@ -195,6 +206,7 @@ __device__ __forceinline__ void pair_end(const PairState &st, int &s_abort, int3
         atomicOr(err, MOE_DEVERR_WAIT_TIMEOUT);
 }
 
+template <int kStages>
 struct Ring {
     int stage = 0;
     uint32_t phase = 0;
@@ -219,11 +231,11 @@ struct __align__(16) UnitDesc {
     int e;
     int m0, n0;          // first row and column of the output tile
     int rows;            // output rows of the tile that exist
-    int total;           // K blocks of all parts or phases
-    int period;          // K blocks of one part
-    int rem;             // rows of a part's last K block when that is not whole, else 0
+    int total;           // K blocks
+    int period;          // after how many of them B begins again
+    int rem;             // rows of the last K block when that is not whole, else 0
     int k_row0;          // first K row, where K runs along the batch
-    int swap;            // swapped: rows on the MMA's N side, a multiple of 64; else 0
+    int swap;            // output rows on the MMA's N side: how many, a multiple of 64; else 0
     int pad[2];
 };
 
@@ -233,7 +245,7 @@ struct UnitReader {
     const UnitDesc *units;
     uint64_t *full, *empty;
     int i;
-    __device__ __forceinline__ UnitReader(const UnitDesc *u, PairBars &b) : units(u), full(b.ufull), empty(b.uempty), i(0) {}
+    __device__ __forceinline__ UnitReader(const UnitDesc *u, uint64_t *f, uint64_t *e) : units(u), full(f), empty(e), i(0) {}
     // One thread: the next unit, or null at the end or on give-up.
     __device__ __forceinline__ const UnitDesc *next(volatile int *abort, uint64_t limit_ns)
     {
@@ -271,8 +283,8 @@ struct UnitReader {
 };
 
 // The decoding warp: units st.cluster, st.cluster + st.clusters, ... below `units`.
-template <typename Decode>
-__device__ __forceinline__ void publish_units(const PairState &st, PairBars &bars, UnitDesc *s_units, int units,
+template <int kStages, typename Decode>
+__device__ __forceinline__ void publish_units(const PairState &st, PairBars<kStages> &bars, UnitDesc *s_units, int units,
                                               volatile int *abort, uint64_t limit_ns, Decode decode)
 {
     const int lane = threadIdx.x & 31;
@@ -404,20 +416,21 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float &a,
 // unit's MMAs, which hides that unit's epilogue. A swapped unit has 256
 // columns of the intermediate size on the MMA's M side and its rows on N, each
 // of da, gate and up a phase of its own.
-__global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_constant__ ActArgs args)
+__global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const __grid_constant__ ActArgs args)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) PairBars bars;
+    __shared__ __align__(8) PairBars<ActConfig::kStages> bars;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ int s_off[kMaxExperts + 1];
     __shared__ int s_up[kMaxExperts + 1];
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PairState st = pair_begin(smem_raw, bars, s_tmem, s_abort, s_off, s_up, args.offsets, args.E, args.cap, 6);
+    const PairState st = pair_begin<ActConfig>(smem_raw, bars, s_tmem, s_abort, s_off, s_up, args.offsets, args.E, args.cap);
     volatile int *abort_flag = &s_abort;
     const int NT = (args.I + 127) / 128, NT2 = (args.I + 255) / 256;
     const int k_blocks = args.H / kBK;
+    pdl_trigger();    // the products' CTAs need this kernel's shared memory: each starts as one here ends
     if (blockIdx.x == 0 && warp == 3) {
         // the rows of zeros behind a and [dg du]
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -432,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
         if (lane == 0) {
             const uint64_t pol_w = l2_policy_evict_normal();
             const uint64_t pol_a = l2_policy_evict_last();
-            Ring r;
-            UnitReader units(s_units, bars);
+            Ring<ActConfig::kStages> r;
+            UnitReader units(s_units, bars.ufull, bars.uempty);
             bool ok = true;
             while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
                 const int swap = t->swap, half = swap >> 1, n0 = t->n0;
@@ -484,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0 && st.rank == 0) {
-            Ring r;
-            UnitReader units(s_units, bars);
+            Ring<ActConfig::kStages> r;
+            UnitReader units(s_units, bars.ufull, bars.uempty);
             bool ok = true;
             int local = 0;
             while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
@@ -553,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) act_grad_kernel(const __grid_cons
         });
     } else if (warp >= 4) {
         const int q = warp - 4;
-        UnitReader units(s_units, bars);
+        UnitReader units(s_units, bars.ufull, bars.uempty);
         int local = 0;
         for (; const UnitDesc *tp = units.next_warp(lane, abort_flag, args.wait_limit_ns); ++local) {
             const UnitDesc t = *tp;
@@ -647,7 +660,7 @@ struct ProductArgs {
 
 __device__ __forceinline__ int job_units(const ProductJob &j, const int *s_tp, int E)
 {
-    const int NT = (j.N + 255) / 256;
+    const int tile_n = j.rows_on_n ? 128 : 256, NT = (j.N + tile_n - 1) / tile_n;
     return j.by_rows ? s_tp[E] * NT : E * ((j.M + 255) / 256) * NT;
 }
 
@@ -662,7 +675,7 @@ __device__ __forceinline__ void product_unit(int u, UnitDesc &d, const ProductAr
         u -= n;
     }
     const ProductJob &j = args.job[job];
-    const int NT = (j.N + 255) / 256;
+    const int tile_n = j.rows_on_n ? 128 : 256, NT = (j.N + tile_n - 1) / tile_n;
     d.job = job;
     if (j.by_rows) {
         const int rt = u / NT;
@@ -679,26 +692,32 @@ __device__ __forceinline__ void product_unit(int u, UnitDesc &d, const ProductAr
         u -= d.e * MT * NT;
         const int mt = u / NT;
         d.m0 = mt * 256;
-        d.n0 = (u - mt * NT) * 256;
-        d.rows = min(j.M - d.m0, 256);
+        d.n0 = (u - mt * NT) * tile_n;
+        if (j.rows_on_n) {
+            d.rows = min(j.N - d.n0, 128);
+            d.swap = 128;
+        } else {
+            d.rows = min(j.M - d.m0, 256);
+        }
         const int k = max(s_off[d.e + 1] - s_off[d.e], 0);
         d.period = (k + kBK - 1) / kBK;
-        d.total = d.period * j.parts;
+        d.total = d.period;
         d.rem = k % kBK;
         d.k_row0 = s_off[d.e];
     }
 }
 
-// A tile's rows first .. first + 31 out of TMEM (or zeros) to memory, one box
-// of 128-byte rows at a time.
+// Rows first .. first + 31 of a tile, columns c_begin .. c_end - 1, out of TMEM
+// (or zeros) to memory, one box of 128-byte rows at a time.
 __device__ __forceinline__ void store_tile(uint32_t t_row, uint8_t *box, const ProductJob &j,
-                                           const CUtensorMap *map, int r0, int first, int rows, int n0, bool zero)
+                                           const CUtensorMap *map, int r0, int first, int rows, int n0, int c_begin,
+                                           int c_end, bool zero)
 {
     const int lane = threadIdx.x & 31;
-    const int cols = min(j.N - n0, 256);     // a multiple of 64
+    const int cols = min(j.N - n0, c_end);     // a multiple of 64
     const int step = j.out_f32 ? 32 : 64;
 #pragma unroll 1
-    for (int c = 0; c < cols; c += step) {
+    for (int c = c_begin; c < cols; c += step) {
         uint32_t d[32];
         if (zero) {
 #pragma unroll
@@ -727,25 +746,26 @@ __device__ __forceinline__ void store_tile(uint32_t t_row, uint8_t *box, const P
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_constant__ ProductArgs args)
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_constant__ ProductArgs args)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) PairBars bars;
+    __shared__ __align__(8) PairBars<C::kStages> bars;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ int s_off[kMaxExperts + 1];
     __shared__ int s_tp[kMaxExperts + 1];
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PairState st = pair_begin(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap, 6);
+    const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap);
     volatile int *abort_flag = &s_abort;
     const int rank = static_cast<int>(st.rank);
 
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol = l2_policy_evict_normal();
-            Ring r;
-            UnitReader units(s_units, bars);
+            Ring<C::kStages> r;
+            UnitReader units(s_units, bars.ufull, bars.uempty);
             bool ok = true;
             while (const UnitDesc *tp = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
                 const UnitDesc t = *tp;
@@ -753,11 +773,12 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                 const CUtensorMap *ma = &args.a[t.job], *mb = &args.b[t.job], *ma32 = &args.a32[t.job];
                 const bool by_rows = j.by_rows != 0;
                 const int half = t.swap >> 1;
-                const int b_col = t.n0 + 128 * rank;
+                const bool on_n = j.rows_on_n != 0;
+                // B's two blocks of 64 columns in this CTA: neighbours, or the two parts of 64 columns
+                const int b_col = t.n0 + (on_n ? 64 : 128) * rank, b_next = on_n ? j.part_cols : 64;
                 const int a_row = t.m0 + (t.swap ? half : 128) * rank;    // rows kind
                 const int b_row0 = t.e * j.b_expert_rows;
-                int a_col = t.m0 + 128 * rank;                            // weights kind
-                const int part_cols = j.part_cols;
+                const int a_col = t.m0 + 128 * rank;                      // weights kind
                 int kp = 0;
                 for (int kb = 0; kb < t.total; ++kb, r.next()) {
                     if (!mbar_wait_bounded(smem_u32(&bars.empty[r.stage]), r.phase ^ 1u, abort_flag,
@@ -793,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                                 tma_load_2d_pair(a_dst + o, &args.a16[t.job], full, a_col, r16, pol);
                                 tma_load_2d_pair(a_dst + kAtom + o, &args.a16[t.job], full, a_col + 64, r16, pol);
                                 tma_load_2d_pair(b_dst + o, &args.b16[t.job], full, b_col, r16, pol);
-                                tma_load_2d_pair(b_dst + kAtom + o, &args.b16[t.job], full, b_col + 64, r16, pol);
+                                tma_load_2d_pair(b_dst + kAtom + o, &args.b16[t.job], full, b_col + b_next, r16, pol);
                             }
                             if (whole < slabs) {
                                 const int last = row + t.rem - 1;
@@ -811,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                                     tma_gather4_pair(a_dst + o, &args.a1[t.job], full, a_col, ra, pol);
                                     tma_gather4_pair(a_dst + kAtom + o, &args.a1[t.job], full, a_col + 64, ra, pol);
                                     tma_gather4_pair(b_dst + o, &args.b1[t.job], full, b_col, rb, pol);
-                                    tma_gather4_pair(b_dst + kAtom + o, &args.b1[t.job], full, b_col + 64, rb, pol);
+                                    tma_gather4_pair(b_dst + kAtom + o, &args.b1[t.job], full, b_col + b_next, rb, pol);
                                 }
                             }
                         } else {
@@ -819,28 +840,26 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                             tma_load_2d_pair(a_dst, ma, full, a_col, row, pol);
                             tma_load_2d_pair(a_dst + kAtom, ma, full, a_col + 64, row, pol);
                             tma_load_2d_pair(b_dst, mb, full, b_col, row, pol);
-                            tma_load_2d_pair(b_dst + kAtom, mb, full, b_col + 64, row, pol);
+                            tma_load_2d_pair(b_dst + kAtom, mb, full, b_col + b_next, row, pol);
                         }
                     }
-                    if (++kp == t.period) {
+                    if (++kp == t.period)
                         kp = 0;
-                        a_col += part_cols;
-                    }
                 }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0 && st.rank == 0) {
-            Ring r;
-            UnitReader units(s_units, bars);
+            Ring<C::kStages> r;
+            UnitReader units(s_units, bars.ufull, bars.uempty);
             bool ok = true;
             int local = 0;
             while (const UnitDesc *tp = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
-                const int total = tp->total, period = tp->period, rem = tp->rem, swap = tp->swap;
-                const bool by_rows = args.job[tp->job].by_rows != 0;
+                const int total = tp->total, rem = tp->rem, swap = tp->swap;
+                const bool by_rows = args.job[tp->job].by_rows != 0, on_n = args.job[tp->job].rows_on_n != 0;
                 // rows kind: A K-major, B MN-major, or the other way round when swapped; weights kind: both MN-major
-                const bool a_mn = !by_rows || swap, b_mn = !swap;
+                const bool a_mn = !by_rows || swap, b_mn = !by_rows || !swap;
                 const uint32_t idesc =
                     idesc_bf16_f32(256, swap ? swap : 256) | (a_mn ? kMajorA : 0u) | (b_mn ? kMajorB : 0u);
                 const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
@@ -852,7 +871,6 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                 }
                 tc_fence_after();
                 const uint32_t d = st.tmem + buf * 256;
-                int kp = 0;
                 for (int kb = 0; kb < total; ++kb, r.next()) {
                     if (!mbar_wait_bounded(smem_u32(&bars.full[r.stage]), r.phase, abort_flag, args.wait_limit_ns)) {
                         ok = false;
@@ -863,14 +881,14 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
                     const uint32_t b_addr = a_addr + kHalf;
                     const uint64_t a0 = a_mn ? smem_desc_mnmajor_sw128(a_addr) : smem_desc_kmajor_sw128(a_addr);
                     const uint64_t b0 = b_mn ? smem_desc_mnmajor_sw128(b_addr) : smem_desc_kmajor_sw128(b_addr);
-                    const bool last = ++kp == period;
-                    if (last)
-                        kp = 0;
-                    const int steps = (last && rem) ? (rem + kUmmaK - 1) / kUmmaK : kBK / kUmmaK;
+                    const int steps = (rem && kb + 1 == total) ? (rem + kUmmaK - 1) / kUmmaK : kBK / kUmmaK;
 #pragma unroll
                     for (int kk = 0; kk < kBK / kUmmaK; ++kk)
-                        if (kk < steps)
+                        if (kk < steps) {
                             umma_bf16_pair(d, a0 + kk * sa, b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                            if (on_n)     // B's second part
+                                umma_bf16_pair(d, a0 + kk * sa, b0 + (kAtom >> 4) + kk * sb, idesc, 1u);
+                        }
                     umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (ok)
@@ -889,9 +907,10 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
             product_unit(u, d, args, s_off, s_tp);
         });
     } else if (warp >= 4) {
-        const int q = warp - 4;
-        uint8_t *const box = st.smem + kStages * kStageBytes + q * kBox;
-        UnitReader units(s_units, bars);
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        constexpr int kHalves = C::kWarps / 4;
+        uint8_t *const box = st.smem + C::kStages * kStageBytes + (warp - 4) * kBox;
+        UnitReader units(s_units, bars.ufull, bars.uempty);
         int local = 0;
         for (; const UnitDesc *tp = units.next_warp(lane, abort_flag, args.wait_limit_ns); ++local) {
             const UnitDesc t = *tp;
@@ -907,25 +926,36 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
             if (!t.swap) {
                 const int r0 = t.m0 + (j.by_rows ? 0 : t.e * j.M);
                 if (t.total || !j.accumulate)
-                    store_tile(t_row, box, j, &args.out[t.job], r0, 128 * rank + q * 32, t.rows, t.n0, t.total == 0);
+                    store_tile(t_row, box, j, &args.out[t.job], r0, 128 * rank + q * 32, t.rows, t.n0, half * 128,
+                               kHalves == 1 ? 256 : half * 128 + 128, t.total == 0);
             } else {
                 // lane = column, TMEM columns = the unit's rows
-                const int col = t.n0 + 128 * rank + q * 32 + lane;
-                const bool col_ok = col < j.N;
+                const int col = (j.by_rows ? t.n0 : t.m0) + 128 * rank + q * 32 + lane;
+                const int cols = j.by_rows ? j.N : j.M;
+                const size_t row0 = j.by_rows ? static_cast<size_t>(t.m0) : static_cast<size_t>(t.e) * j.N + t.n0;
+                const bool col_ok = col < cols;
 #pragma unroll 1
-                for (int c = 0; c < t.rows; c += 16) {
+                for (int c = 16 * half; c < t.rows; c += 16 * kHalves) {
                     uint32_t v[16];
                     tmem_ld_32x32b_x16(t_row + c, v);
                     tmem_wait_ld();
+                    if (t.total == 0)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (!col_ok || c + i >= t.rows)
-                            continue;
-                        const size_t o = static_cast<size_t>(t.m0 + c + i) * j.N + col;
-                        if (j.out_f32)
-                            static_cast<float *>(j.out)[o] = __uint_as_float(v[i]);
-                        else
-                            static_cast<__nv_bfloat16 *>(j.out)[o] = __float2bfloat16_rn(__uint_as_float(v[i]));
+                        for (int i = 0; i < 16; ++i)
+                            v[i] = 0u;
+                    const int n = col_ok ? t.rows - c : 0;      // rows of these 16 to store
+                    if (j.out_f32) {
+                        float *p = static_cast<float *>(j.out) + (row0 + c) * cols + col;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i, p += cols)
+                            if (i < n)
+                                *p = __uint_as_float(v[i]);
+                    } else {
+                        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(j.out) + (row0 + c) * cols + col;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i, p += cols)
+                            if (i < n)
+                                *p = __float2bfloat16_rn(__uint_as_float(v[i]));
                     }
                 }
             }
@@ -938,15 +968,17 @@ __global__ void __launch_bounds__(kThreads, 1) products_kernel(const __grid_cons
             bulk_wait_all();
         __syncwarp();
     }
+    pdl_trigger();
     pair_end(st, s_abort, args.err);
 }
 
 // ------------------------------------------------------------------ host side
 
 // Launch a CTA-pair kernel with at most `units` pairs. The attribute and the
-// occupancy are looked up once per host thread, device and kernel.
-template <typename Args>
-cudaError_t launch_pair(void (*kern)(Args), const Args &args, int smem, long long units, int num_sms, cudaStream_t stream)
+// occupancy are looked up once per host thread, device and kernel (each has a
+// configuration type of its own).
+template <class C, typename Args>
+cudaError_t launch_pair(void (*kern)(Args), const Args &args, long long units, int num_sms, cudaStream_t stream)
 {
     static thread_local int done_for_device = -1;
     static thread_local int max_clusters = 0;
@@ -955,18 +987,20 @@ cudaError_t launch_pair(void (*kern)(Args), const Args &args, int smem, long lon
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (done_for_device != dev) {
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess)
             return e;
         cfg.gridDim = dim3(2 * (num_sms / 2));
         int n = 0;
@@ -986,14 +1020,15 @@ long long tiles_of(long long n) { return (n + 255) / 256; }
 
 long long product_units(const ProductJob &j, int E, int cap)
 {
-    return j.by_rows ? (tiles_of(cap) + E) * tiles_of(j.N) : E * tiles_of(j.M) * tiles_of(j.N);
+    return j.by_rows ? (tiles_of(cap) + E) * tiles_of(j.N)
+                     : E * tiles_of(j.M) * (j.rows_on_n ? (j.N + 127LL) / 128 : tiles_of(j.N));
 }
 
 cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offsets, int E, int cap, int32_t *err,
                             int num_sms, cudaStream_t stream)
 {
     ProductArgs a = {};
-    long long units = 0;
+    long long units = 0, live = 0, blocks = 0;
     for (int i = 0; i < n; ++i) {
         const ProductJob &j = jobs[i];
         a.job[i] = j;
@@ -1007,10 +1042,15 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
                             !make_tile_map(&a.a1[i], j.a, a_rows, a_cols, 1) ||
                             !make_tile_map(&a.b1[i], j.b, b_rows, b_cols, 1))) ||
             !make_tile_map(&a.b[i], j.b, b_rows, b_cols, 64) ||
-            !(j.out_f32 ? make_tile_map_f32(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32)
-                        : make_tile_map(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32)))
+            (!j.rows_on_n && !(j.out_f32 ? make_tile_map_f32(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32)
+                        : make_tile_map(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32))))
             return cudaErrorInvalidValue;
         units += product_units(j, E, cap);
+        // units with rows spread evenly, and their K blocks
+        const long long n_live = j.by_rows ? (tiles_of(cap) > E ? tiles_of(cap) : (cap < E ? cap : E)) * tiles_of(j.N)
+                                           : product_units(j, E, cap);
+        live += n_live;
+        blocks += n_live * (j.by_rows ? j.k_blocks : (cap / E + kBK - 1) / kBK);
     }
     a.jobs = n;
     a.offsets = offsets;
@@ -1018,7 +1058,9 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
     a.cap = cap;
     a.err = err;
     a.wait_limit_ns = kWaitLimitNs;
-    return launch_pair(products_kernel, a, kProductSmem, units, num_sms, stream);
+    if (blocks < kWideBlocks * live)
+        return launch_pair<WideConfig>(products_kernel<WideConfig>, a, units, num_sms, stream);
+    return launch_pair<DeepConfig>(products_kernel<DeepConfig>, a, units, num_sms, stream);
 }
 
 cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, const void *W2, const int32_t *offsets,
@@ -1040,7 +1082,7 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
     a.cap = cap;
     a.H = H;
     a.I = I;
-    return launch_pair(act_grad_kernel, a, kActSmem, (tiles_of(cap) + E) * ((I + 127) / 128), num_sms, stream);
+    return launch_pair<ActConfig>(act_grad_kernel, a, (tiles_of(cap) + E) * ((I + 127) / 128), num_sms, stream);
 }
 
 }  // namespace moe

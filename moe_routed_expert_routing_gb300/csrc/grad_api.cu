@@ -98,7 +98,9 @@ struct RouteSplitK {
 RouteSplitK route_segments(const moe_router_problem_t &p)
 {
     const long long tiles = ((p.E + 255LL) / 256) * ((p.H + 255LL) / 256);
-    long long want = 152 / tiles;      // two units a CTA pair
+    long long want = 76 / tiles;       // a unit for each CTA pair, or two where that leaves one range
+    if (want < 2)
+        want = 152 / tiles;
     if (want < 1)
         want = 1;
     long long rows = (p.T_max + want - 1) / want;
@@ -384,15 +386,15 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
     int n = 0;
     if (dw_router) {
         ProductJob j = {};
-        j.a = a.parts;
-        j.a_rows = p.T_max + 1LL;
-        j.zero_in_a = 1;
-        j.a_cols = 2LL * Ep;
-        j.b = x;
-        j.b_rows = p.T_max;
-        j.b_cols = p.H;
-        j.M = p.E;
-        j.N = p.H;
+        j.rows_on_n = 1;
+        j.a = x;
+        j.a_rows = p.T_max;
+        j.a_cols = p.H;
+        j.b = a.parts;
+        j.b_rows = p.T_max + 1LL;
+        j.b_cols = 2LL * Ep;
+        j.M = p.H;
+        j.N = p.E;
         j.wrap = 1;
         j.parts = 2;
         j.part_cols = Ep;

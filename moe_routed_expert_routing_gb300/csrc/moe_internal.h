@@ -393,10 +393,12 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
 // One grouped product of bf16 operands, for every expert e with the rows R_e =
 // [offsets[e], offsets[e + 1]):
 //  by_rows:  out[r, n] = sum_k a[r, k] b[e * b_expert_rows + k mod (64 wrap), n], r in R_e, k < 64 k_blocks
-//  else:     out[e, m, n] = sum_{p < parts} sum_{r in R_e} a[r, m + p part_cols] b[r, n], m < M
-// for n < N. a [a_rows, a_cols], b [b_rows, b_cols] and out ([cap, N] or [E, M, N]) row-major.
+//  else:     out[e, m, n] = sum_{r in R_e} a[r, m] b[r, n], m < M
+//  rows_on_n: out[e, n, m] = sum_{p < parts} sum_{r in R_e} a[r, m] b[r, n + p part_cols], m < M: as above with
+//            the output transposed, for an N below 256 columns: the MMAs and B's loads follow it in steps of 128
+// for n < N. a [a_rows, a_cols], b [b_rows, b_cols] and out ([cap, N], [E, M, N] or [E, N, M]) row-major.
 struct ProductJob {
-    int by_rows;
+    int by_rows, rows_on_n;
     const void *a, *b;
     long long a_rows, a_cols, b_rows, b_cols;
     int M, N;

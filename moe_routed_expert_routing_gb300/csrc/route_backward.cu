@@ -51,10 +51,13 @@ __device__ __forceinline__ float as_logit(float l) { return l < INFINITY ? l : -
 // the chosen experts' terms, each added by the lane its expert falls to.
 __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_constant__ RouteGradArgs a)
 {
-    extern __shared__ float s_row[];
+    extern __shared__ float4 s_row[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = a.E, k = a.k, Ep = (E + 63) & ~63;
-    float *const dl = s_row + warp * Ep;
+    const bool whole = E % 4 == 0;
+    float *const dl = reinterpret_cast<float *>(s_row) + warp * Ep;
+    pdl_wait();
+    pdl_trigger();
     int T = a.T_max;
     if (a.d_num_tokens) {
         T = *a.d_num_tokens;
@@ -139,47 +142,74 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
                 term[i] = l[i] > -INFINITY ? g[i] * (expf(l[i] - mx) * inv_sum) : 0.f;
             base = -warp_sum(term[0] + term[1]);
         }
-        for (int e = lane; e < Ep; e += 32) {
-            float v = 0.f;
-            if (dense && e < E) {
-                const float x = as_logit(logits[e]);
-                v = x > -INFINITY ? base * (expf(x - mx) * inv_sum) : 0.f;
-            }
-            dl[e] = v;
+        // four consecutive experts a lane
+        for (int e = 4 * lane; e < Ep; e += 128) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            if (dense)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (e + i < E) {
+                        const float x = as_logit(logits[e + i]);
+                        v[i] = x > -INFINITY ? base * (expf(x - mx) * inv_sum) : 0.f;
+                    }
+            *reinterpret_cast<float4 *>(dl + e) = make_float4(v[0], v[1], v[2], v[3]);
         }
         __syncwarp();
         for (int j = 0; j < k; ++j) {
             const int e = __shfl_sync(0xffffffffu, j < 32 ? id[0] : id[1], j & 31);
             const float v = __shfl_sync(0xffffffffu, j < 32 ? term[0] : term[1], j & 31);
-            if (e >= 0 && (e & 31) == lane)
+            if (e >= 0 && ((e >> 2) & 31) == lane)
                 dl[e] += v;
         }
         __syncwarp();
         __nv_bfloat16 *const parts = static_cast<__nv_bfloat16 *>(a.parts) + static_cast<size_t>(t) * 2 * Ep;
-        for (int e = lane; e < Ep; e += 32) {
-            float v = dl[e];
-            if (e < E) {
-                if (a.d_logits_add)
-                    v += a.d_logits_add[static_cast<size_t>(t) * E + e];
+        const size_t at = static_cast<size_t>(t) * E;
+        for (int e = 4 * lane; e < Ep; e += 128) {
+            const float4 s4 = *reinterpret_cast<const float4 *>(dl + e);
+            float v[4] = {s4.x, s4.y, s4.z, s4.w};
+            if (whole && e < E) {         // E a multiple of 4: rows of whole 16-byte words
+                if (a.d_logits_add) {
+                    const float4 o = *reinterpret_cast<const float4 *>(a.d_logits_add + at + e);
+                    v[0] += o.x;
+                    v[1] += o.y;
+                    v[2] += o.z;
+                    v[3] += o.w;
+                }
                 if (a.d_logits)
-                    a.d_logits[static_cast<size_t>(t) * E + e] = v;
+                    *reinterpret_cast<float4 *>(a.d_logits + at + e) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (e + i < E) {
+                        if (a.d_logits_add)
+                            v[i] += a.d_logits_add[at + e + i];
+                        if (a.d_logits)
+                            a.d_logits[at + e + i] = v[i];
+                    }
             }
-            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-            parts[e] = hi;
-            parts[Ep + e] = __float2bfloat16_rn(v - __bfloat162float(hi));
+            __align__(8) __nv_bfloat16 hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hi[i] = __float2bfloat16_rn(v[i]);
+                lo[i] = __float2bfloat16_rn(v[i] - __bfloat162float(hi[i]));
+            }
+            *reinterpret_cast<uint2 *>(parts + e) = *reinterpret_cast<const uint2 *>(hi);
+            *reinterpret_cast<uint2 *>(parts + Ep + e) = *reinterpret_cast<const uint2 *>(lo);
         }
         __syncwarp();
     }
 }
 
-__global__ void __launch_bounds__(kThreads) sum_parts_kernel(const float4 *__restrict__ part, int parts, size_t n4,
+__global__ void __launch_bounds__(kThreads) sum_parts_kernel(const float4 *part, int parts, size_t n4,
                                                              void *out, int f32)
 {
+    pdl_wait();
+    pdl_trigger();
     for (size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x; i < n4;
          i += static_cast<size_t>(gridDim.x) * kThreads) {
-        float4 sum = __ldg(part + i);
+        float4 sum = part[i];
         for (int p = 1; p < parts; ++p) {
-            const float4 e = __ldg(part + p * n4 + i);
+            const float4 e = part[p * n4 + i];
             sum.x += e.x;
             sum.y += e.y;
             sum.z += e.z;
@@ -205,7 +235,7 @@ cudaError_t launch_route_grad(const RouteGradArgs &a, int num_sms, cudaStream_t 
     const long long need = (static_cast<long long>(a.T_max) + kThreads / 32 - 1) / (kThreads / 32);
     const long long most = num_sms * 8LL;
     return launch_k(route_grad_kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(kThreads),
-                    sizeof(float) * Ep * (kThreads / 32), stream, false, a);
+                    sizeof(float) * Ep * (kThreads / 32), stream, true, a);
 }
 
 cudaError_t launch_sum_parts(const float *part, int parts, size_t n, void *out, bool f32, int num_sms,
@@ -214,7 +244,7 @@ cudaError_t launch_sum_parts(const float *part, int parts, size_t n, void *out, 
     const size_t need = (n / 4 + kThreads - 1) / kThreads;
     const size_t most = num_sms * 8;
     return launch_k(sum_parts_kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(kThreads), 0, stream,
-                    false, reinterpret_cast<const float4 *>(part), parts, n / 4, out, f32 ? 1 : 0);
+                    true, reinterpret_cast<const float4 *>(part), parts, n / 4, out, f32 ? 1 : 0);
 }
 
 }  // namespace moe
