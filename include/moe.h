@@ -588,8 +588,9 @@ moe_status_t moe_norm_backward_workspace_size(const moe_norm_problem_t *problem,
  *   h_dtype, rows y_stride apart, or NULL (the gradient that reaches h past the
  *   block); dh[T_max, H] of h_dtype out, rows out_stride apart; dw[H] of
  *   w_dtype out, or NULL. dh may be h or dh_add, with the same stride.
- * norm_block, gate and residual_scale are not read. The workspace need not be
- * cleared.
+ * norm_block, gate and residual_scale are not read. ws: only its device error
+ * word has to start at zero (a wait inside the kernel that gave up sets
+ * MOE_DEVERR_WAIT_TIMEOUT).
  */
 moe_status_t moe_norm_backward(const moe_norm_problem_t *problem, const void *h, const void *w, const void *dx,
                                const void *dh_add, const int32_t *d_num_tokens, void *dh, void *dw, void *ws,

@@ -313,6 +313,7 @@ moe_status_t moe_norm_backward(const moe_norm_problem_t *problem, const void *h,
     a.dh = dh;
     a.dw = dw;
     a.part = at<float>(ws, L.part);
+    a.err = at<int32_t>(ws, 0);
     a.T_max = p.T_max;
     a.H = p.H;
     a.h_f32 = p.h_dtype == MOE_DTYPE_FP32;

@@ -425,6 +425,7 @@ struct NormGradArgs {
     void *dh;                  // type of h
     void *dw;                  // type of w; null: not wanted
     float *part;               // norm_grad_part_rows() x H partial sums of dw
+    int32_t *err;
     int T_max, H;
     int h_f32, w_f32, unit_offset;
     float eps;
