@@ -362,25 +362,26 @@ struct ActArgs {
     __nv_bfloat16 *dgu;      // [cap + 1, 2I]
     uint64_t wait_limit_ns;
     int E, cap, H, I;
+    int swaps;               // an expert's last rows may run swapped
 };
 
 // An expert's units: column tiles of 128 x its whole row tiles, column tile
 // outside (the row tiles that share one weight tile go to neighbouring pairs);
 // then, if its last row tile runs swapped, that tile's columns by 256.
-__device__ __forceinline__ int act_units_of(int rows, int NT, int NT2)
+__device__ __forceinline__ int act_units_of(int rows, int NT, int NT2, bool swaps)
 {
     const int tiles = (rows + kTileRows - 1) / kTileRows;
     const int last = rows - (tiles - 1) * kTileRows;
-    return tiles == 0 ? 0 : (swap_rows(last) ? (tiles - 1) * NT + NT2 : tiles * NT);
+    return tiles == 0 ? 0 : (swaps && swap_rows(last) ? (tiles - 1) * NT + NT2 : tiles * NT);
 }
 
-__device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, const int *s_up, int E, int NT)
+__device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, const int *s_up, int E, int NT, bool swaps)
 {
     const int e = find_expert(s_up, E, u, 1);
     const int rows = s_off[e + 1] - s_off[e];
     int tiles = (rows + kTileRows - 1) / kTileRows;
     const int last = rows - (tiles - 1) * kTileRows;
-    const int swap = swap_rows(last);
+    const int swap = swaps ? swap_rows(last) : 0;
     const int whole = swap ? tiles - 1 : tiles;
     const int local = u - s_up[e];
     d.job = 0;
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
         int carry = 0;
         for (int base = 0; base < args.E; base += 32) {
             const int e = base + lane;
-            int n = e < args.E ? act_units_of(max(s_off[e + 1] - s_off[e], 0), NT, NT2) : 0, v = n;
+            int n = e < args.E ? act_units_of(max(s_off[e + 1] - s_off[e], 0), NT, NT2, args.swaps != 0) : 0, v = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int w = __shfl_up_sync(kFull, v, o);
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
             s_up[args.E] = carry;
         __syncwarp();
         publish_units(st, bars, s_units, carry, abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
-            act_unit(u, d, s_off, s_up, args.E, NT);
+            act_unit(u, d, s_off, s_up, args.E, NT, args.swaps != 0);
         });
     } else if (warp >= 4) {
         const int q = warp - 4;
@@ -1082,6 +1083,10 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
     a.cap = cap;
     a.H = H;
     a.I = I;
+    // Swapped units are half as many: not while the others leave CTA pairs idle
+    // (E=16, 64 tokens of 4 experts, H=1024, I=512: @@ us so, @@ swapped)
+    const long long tiles = tiles_of(cap) > E ? tiles_of(cap) : (cap < E ? cap : E);
+    a.swaps = tiles * ((I + 127) / 128) > num_sms / 2;
     return launch_pair<ActConfig>(act_grad_kernel, a, (tiles_of(cap) + E) * ((I + 127) / 128), num_sms, stream);
 }
 
