@@ -61,7 +61,7 @@ struct Config {
     static constexpr int kThreads = 128 + 32 * kWarps;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + (kBoxes ? kWarps * kBox : 0);
 };
-using ActConfig = Config<6, 4, false>;
+using ActConfig = Config<6, 8, false>;
 using DeepConfig = Config<6, 4, true>;       // products with many K blocks a tile: more copies in flight
 using WideConfig = Config<5, 8, true>;       // with a few: the epilogue is most of the time
 constexpr int kWideBlocks = 8;               // fewer K blocks a tile than this on average
@@ -123,6 +123,21 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// The rows of a tile that this CTA's half of A needs, `n` of 128, as whole 32-row
+// boxes, or one box where all are there. MMA rows past them keep whatever the
+// stage held before: they are never stored.
+__device__ __forceinline__ int boxed_rows(int n) { return n <= 0 ? 0 : (n >= 128 ? 128 : (n + kSwapBox - 1) / kSwapBox * kSwapBox); }
+
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, const CUtensorMap *map32, uint32_t full,
+                                          int col, int row, int boxed, uint64_t policy)
+{
+    if (boxed == 128)
+        tma_load_2d_pair(dst, map, full, col, row, policy);
+    else
+        for (int i = 0; i < boxed; i += kSwapBox)
+            tma_load_2d_pair(dst + i * 128, map32, full, col, row + i, policy);
+}
+
 // What every thread of a CTA pair's kernel starts from.
 struct PairState {
     uint8_t *smem;          // stages, then the output boxes; 1024-byte aligned
@@ -141,10 +156,12 @@ struct PairBars {
     uint64_t ufull[2], uempty[2];   // batches of units
 };
 
-// Barriers, TMEM, the experts' offsets (clamped to the batch) and their row tiles.
-template <class C>
+// Barriers, TMEM, the experts' offsets (clamped to the batch) and s_tp, the
+// running sum of count(rows) over the experts.
+template <class C, typename Count>
 __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::kStages> &bars, uint32_t &s_tmem, int &s_abort,
-                                                int *s_off, int *s_tp, const int32_t *offsets, int E, int cap)
+                                                int *s_off, int *s_tp, const int32_t *offsets, int E, int cap,
+                                                Count count)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     PairState st;
@@ -177,8 +194,25 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::k
         s_off[i] = o < 0 ? 0 : (o > cap ? cap : o);
     }
     __syncthreads();
-    if (warp == 3)
-        build_tile_prefix(s_off, s_tp, E, kTileRows, lane);
+    if (warp == 3) {
+        int carry = 0;
+        for (int base = 0; base < E; base += 32) {
+            const int e = base + lane;
+            const int n = e < E ? count(max(s_off[e + 1] - s_off[e], 0)) : 0;
+            int v = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int w = __shfl_up_sync(kFull, v, o);
+                if (lane >= o)
+                    v += w;
+            }
+            if (e < E)
+                s_tp[e] = carry + v - n;
+            carry += __shfl_sync(kFull, v, 31);
+        }
+        if (lane == 0)
+            s_tp[E] = carry;
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // both CTAs' barriers initialised before any remote arrive
@@ -427,9 +461,10 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
     __shared__ int s_up[kMaxExperts + 1];
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PairState st = pair_begin<ActConfig>(smem_raw, bars, s_tmem, s_abort, s_off, s_up, args.offsets, args.E, args.cap);
-    volatile int *abort_flag = &s_abort;
     const int NT = (args.I + 127) / 128, NT2 = (args.I + 255) / 256;
+    const PairState st = pair_begin<ActConfig>(smem_raw, bars, s_tmem, s_abort, s_off, s_up, args.offsets, args.E, args.cap,
+                                               [&](int rows) { return act_units_of(rows, NT, NT2, args.swaps != 0); });
+    volatile int *abort_flag = &s_abort;
     const int k_blocks = args.H / kBK;
     pdl_trigger();    // the products' CTAs need this kernel's shared memory: each starts as one here ends
     if (blockIdx.x == 0 && warp == 3) {
@@ -451,7 +486,8 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
             bool ok = true;
             while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
                 const int swap = t->swap, half = swap >> 1, n0 = t->n0;
-                const int a_row = swap ? t->m0 + half * rank : t->m0 + 128 * rank;
+                const int a_row = t->m0 + (swap ? half : 128) * rank;
+                const int boxed = boxed_rows(t->rows - 128 * rank);
                 const int w2_row = t->e * args.H;
                 const int gate = t->e * 2 * args.I + n0;
                 int phase = 0, kp = 0;
@@ -468,12 +504,12 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
                     const int kc = kp * kBK;
                     if (!swap) {
                         if (phase == 0) {
-                            mbar_arrive_expect_tx_cluster(full, kHalf + kAtom);
-                            tma_load_2d_pair(a_dst, &args.dy, full, kc, a_row, pol_a);
+                            mbar_arrive_expect_tx_cluster(full, boxed * 128 + kAtom);
+                            load_rows(a_dst, &args.dy, &args.dy32, full, kc, a_row, boxed, pol_a);
                             tma_load_2d_pair(b_dst, &args.w2, full, n0 + 64 * rank, w2_row + kc, pol_w);
                         } else {
-                            mbar_arrive_expect_tx_cluster(full, kStageBytes);
-                            tma_load_2d_pair(a_dst, &args.x, full, kc, a_row, pol_a);
+                            mbar_arrive_expect_tx_cluster(full, boxed * 128 + kHalf);
+                            load_rows(a_dst, &args.x, &args.x32, full, kc, a_row, boxed, pol_a);
                             tma_load_2d_pair(b_dst, &args.w13, full, kc, gate + (rank ? args.I : 0), pol_w);
                         }
                     } else {
@@ -544,29 +580,11 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
         }
         __syncwarp();
     } else if (warp == 2) {
-        // s_up so far counts row tiles; the units of each expert need the rows of its last tile too
-        int carry = 0;
-        for (int base = 0; base < args.E; base += 32) {
-            const int e = base + lane;
-            int n = e < args.E ? act_units_of(max(s_off[e + 1] - s_off[e], 0), NT, NT2, args.swaps != 0) : 0, v = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int w = __shfl_up_sync(kFull, v, o);
-                if (lane >= o)
-                    v += w;
-            }
-            if (e < args.E)
-                s_up[e] = carry + v - n;
-            carry += __shfl_sync(kFull, v, 31);
-        }
-        if (lane == 0)
-            s_up[args.E] = carry;
-        __syncwarp();
-        publish_units(st, bars, s_units, carry, abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
+        publish_units(st, bars, s_units, s_up[args.E], abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
             act_unit(u, d, s_off, s_up, args.E, NT, args.swaps != 0);
         });
     } else if (warp >= 4) {
-        const int q = warp - 4;
+        const int q = warp & 3, half = (warp - 4) >> 2;
         UnitReader units(s_units, bars.ufull, bars.uempty);
         int local = 0;
         for (; const UnitDesc *tp = units.next_warp(lane, abort_flag, args.wait_limit_ns); ++local) {
@@ -586,7 +604,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
                 __nv_bfloat16 *const act = args.act + static_cast<size_t>(t.m0 + r) * args.I + t.n0;
                 __nv_bfloat16 *const dgu = args.dgu + static_cast<size_t>(t.m0 + r) * 2 * args.I + t.n0;
 #pragma unroll 1
-                for (int c = 0; c < cols; c += 16) {
+                for (int c = 64 * half; c < cols && c < 64 * half + 64; c += 16) {
                     uint32_t vg[16], vu[16], vd[16];
                     tmem_ld_32x32b_x16(t_gu + c, vg);
                     tmem_ld_32x32b_x16(t_gu + 128 + c, vu);
@@ -617,7 +635,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
                 __nv_bfloat16 *const act = args.act + static_cast<size_t>(t.m0) * args.I + n;
                 __nv_bfloat16 *const dgu = args.dgu + static_cast<size_t>(t.m0) * 2 * args.I + n;
 #pragma unroll 1
-                for (int c = 0; c < t.rows; c += 16) {
+                for (int c = 16 * half; c < t.rows; c += 32) {
                     uint32_t vg[16], vu[16], vd[16];
                     tmem_ld_32x32b_x16(t_gu + c, vg);
                     tmem_ld_32x32b_x16(t_gu + 128 + c, vu);
@@ -758,7 +776,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
     __shared__ int s_tp[kMaxExperts + 1];
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap);
+    const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap,
+                                       [](int rows) { return (rows + kTileRows - 1) / kTileRows; });
     volatile int *abort_flag = &s_abort;
     const int rank = static_cast<int>(st.rank);
 
@@ -779,6 +798,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                 const int b_col = t.n0 + (on_n ? 64 : 128) * rank, b_next = on_n ? j.part_cols : 64;
                 const int a_row = t.m0 + (t.swap ? half : 128) * rank;    // rows kind
                 const int b_row0 = t.e * j.b_expert_rows;
+                const int boxed = boxed_rows(t.rows - 128 * rank);
                 const int a_col = t.m0 + 128 * rank;                      // weights kind
                 int kp = 0;
                 for (int kb = 0; kb < t.total; ++kb, r.next()) {
@@ -794,11 +814,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                         const int b_row = b_row0 + kp * kBK;
                         // swapped: B's columns on the MMA's M side
                         const uint32_t w_dst = t.swap ? a_dst : b_dst;
-                        mbar_arrive_expect_tx_cluster(full, t.swap ? kHalf + half * 128 : kStageBytes);
+                        mbar_arrive_expect_tx_cluster(full, kHalf + (t.swap ? half : boxed) * 128);
                         tma_load_2d_pair(w_dst, mb, full, b_col, b_row, pol);
                         tma_load_2d_pair(w_dst + kAtom, mb, full, b_col + 64, b_row, pol);
                         if (!t.swap)
-                            tma_load_2d_pair(a_dst, ma, full, kb * kBK, a_row, pol);
+                            load_rows(a_dst, ma, ma32, full, kb * kBK, a_row, boxed, pol);
                         else
                             for (int i = 0; i < half; i += kSwapBox)
                                 tma_load_2d_pair(b_dst + i * 128, ma32, full, kb * kBK, a_row + i, pol);
