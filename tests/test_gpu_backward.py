@@ -198,6 +198,9 @@ def run_experts(B, p, x, dy, W13, W2, bounds, **out):
     ([0, 0, 0, 515, 0], 512, 256, 1),
     ([40, 30, 20, 10, 5, 2, 1, 0] * 4, 256, 128, 64),
     ([300, 7], 1088, 576, 0),
+    ([0, 0], 128, 64, 9),                 # nothing routed
+    ([1500, 1300], 256, 128, 3),          # many K blocks a tile
+    ([256, 384, 385, 513], 192, 128, 0),  # a last tile of 128 rows, of 129, of 1
 ])
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 def test_expert_backward(B, counts, H, I, spare, kind):
@@ -281,6 +284,65 @@ def test_expert_backward_extreme_gates(B):
         check(out[n], want[key], tol[key], n)
 
 
+def test_expert_backward_into_the_middle_of_a_buffer(B):
+    """Outputs and inputs that are 16-byte aligned and no more."""
+    counts, H, I = [40, 100], 128, 64
+    x, dy, W13, W2, bounds = expert_inputs(11, counts, H, I)
+    for dt in (BF, F32):
+        p = expert_problem(B, counts, H, I, dx_dtype=dt, dw_dtype=dt)
+        names = {"dx_sorted": x.shape, "dW13": W13.shape, "dW2": W2.shape}
+        want = run_experts(B, p, x, dy, W13, W2, bounds, **{n: empty(s, dt) for n, s in names.items()})
+
+        def shifted(t):
+            step = 16 // t.element_size()
+            buf = torch.zeros(t.numel() + step, dtype=t.dtype, device="cuda")
+            buf[step:] = t.reshape(-1)
+            return buf[step:].view(t.shape)
+
+        got = run_experts(B, p, shifted(x), shifted(dy), shifted(W13), shifted(W2), bounds,
+                          **{n: shifted(empty(s, dt)) for n, s in names.items()})
+        for n in names:
+            assert torch.equal(got[n], want[n]), n
+
+
+def test_offsets_beyond_32_bits(B):
+    """Rows and weights whose elements pass 2^31: the last ones come out right."""
+    T, k, H, E = 8192, 9, 32768, 16
+    _, inv, valid = routing(5, T, E, k)
+    g = gen(5)
+    p = B.Problem.make(T, E, k, H, 64)
+    assert p.cap * H > 2 ** 31
+    dout, w = randn(g, (T, H)), torch.rand((T, k), generator=g, device="cuda")
+    y = torch.empty((p.cap, H), device="cuda").normal_(generator=g)
+    dy, dw, dx, d_inv = empty((p.cap, H)), empty((T, k), F32), empty((T, H)), torch.from_numpy(inv).cuda()
+    B.moe_combine_backward(p, dout, d_inv, w, dy, y_sorted=y, d_weights=dw)
+    B.moe_dispatch_backward(p, dy, d_inv, dx)
+    slot = np.argsort(inv)[-3:]                       # the slots of the last rows of the batch
+    for s in slot:
+        t, r = int(s) // k, int(inv[s])
+        a, b = ref.f64(dout[t]), ref.f64(y[r])
+        check(dy[r], float(w.view(-1)[s]) * a, U * np.abs(a), "dy")
+        assert abs(float(dw.view(-1)[s]) - (a * b).sum()) <= (H / 256 + 21) * U * np.abs(a * b).sum()
+        rows = [int(v) for v in inv[t * k: t * k + k]]
+        terms = ref.f64(dy[rows])
+        check(dx[t], terms.sum(0), (k + 1) * U * np.abs(terms).sum(0), "dx")
+    del y, dy, dx, dout
+    E, H, I = 264, 4096, 1024
+    counts = [0] * (E - 2) + [70, 30]
+    x, dgy, _, _, bounds = expert_inputs(12, [70, 30], H, I)
+    bounds = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    W13, W2 = randn(g, (E, 2 * I, H), BF, H ** -0.5), randn(g, (E, H, I), BF, I ** -0.5)
+    assert W13.numel() > 2 ** 31
+    p = expert_problem(B, counts, H, I)
+    out = run_experts(B, p, x, dgy, W13, W2, bounds, dx_sorted=empty(x.shape), dW13=torch.empty_like(W13),
+                      dW2=torch.empty_like(W2))
+    want, tol = back.experts(ref.f64(x), ref.f64(dgy), ref.f64(W13[-2:]), ref.f64(W2[-2:]), [0, 70, 100])
+    check(out["dx_sorted"], want["dx"], tol["dx"], "dx")
+    check(out["dW13"][-2:], want["dW13"], tol["dW13"], "dW13")
+    check(out["dW2"][-2:], want["dW2"], tol["dW2"], "dW2")
+    assert not out["dW13"][: E - 2].any() and not out["dW2"][: E - 2].any()
+
+
 # ------------------------------------------------------------------ norm
 
 def rows_apart(t, stride):
@@ -306,6 +368,10 @@ def rows_apart(t, stride):
     (160, 20480, "fp32", "bf16", 0, False, True),
     (3000, 128, "bf16", "bf16", 0, False, False),
     (5000, 256, "fp32", "fp32", 0, False, True),
+    (16, 576, "fp32", "bf16", 584, True, True),
+    (17, 64, "bf16", "bf16", 0, False, True),
+    (900, 8192, "fp32", "fp32", 0, False, True),
+    (400, 8192, "bf16", None, 8200, False, False),
 ])
 def test_norm_backward(B, T, H, h, w, stride, offset, add):
     g = gen(T + H)
@@ -355,6 +421,25 @@ def test_norm_backward_zero_rows_and_token_count(B):
 
 
 # ------------------------------------------------------------------ router
+
+def test_norm_backward_many_rows_and_token_count(B):
+    T, H = 700, 1088
+    g = gen(2)
+    h, dx, w = randn(g, (T, H)), randn(g, (T, H)), randn(g, (H,), BF, 0.1, 1.0)
+    p = B.NormProblem.make(T, H, eps=1e-6)
+    ws = torch.zeros(B.moe_norm_backward_workspace_size(p), dtype=torch.uint8, device="cuda")
+    for n, rows in [(699, 699), (153, 153), (1, 1), (0, 0), (-1, 0), (4000, T)]:
+        h2, dx2 = h.clone(), dx.clone()
+        h2[rows:], dx2[rows:] = float("nan"), float("nan")
+        dh, dw = empty((T, H)), empty((H,))
+        B.moe_norm_backward(p, h2, w, dx2, dh, ws, dw=dw, d_num_tokens=count(n))
+        want, want_dw, mag, mag_dw = back.norm(ref.f64(h)[:rows], ref.f64(dx)[:rows], ref.f64(w)) if rows else (
+            np.zeros((0, H)), np.zeros(H), np.zeros((0, H)), np.zeros(H))
+        check(dh[:rows], want, 90 * U * mag, "dh")
+        check(dw, want_dw, 160 * U * mag_dw, "dw")
+        assert (dh[rows:] == 7.0).all()
+    assert B.moe_last_device_error(ws) == 0
+
 
 def route_inputs(B, seed, T, E, k, H, score, renorm):
     g = gen(seed)
