@@ -381,6 +381,16 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
     a.scale = p.scale;
     a.segments = seg.segments;
     a.segment_rows = seg.rows;
+    if (route_grad_few(a)) {
+        RouteFewArgs f = {};
+        f.x = static_cast<const __nv_bfloat16 *>(x);
+        f.w = static_cast<const __nv_bfloat16 *>(w_router);
+        f.dx = dx;
+        f.dw = dw_router;
+        f.dw_f32 = dw_dtype == MOE_DTYPE_FP32;
+        f.H = p.H;
+        return cuda_status(launch_route_grad_few(a, f, s));
+    }
     if ((st = cuda_status(launch_route_grad(a, sms, s))) != MOE_OK)
         return st;
     ProductJob jobs[2];

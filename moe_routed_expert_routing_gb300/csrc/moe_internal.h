@@ -7,6 +7,7 @@
 #include <utility>
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "moe.h"
@@ -453,6 +454,29 @@ struct RouteGradArgs {
 };
 
 cudaError_t launch_route_grad(const RouteGradArgs &a, int num_sms, cudaStream_t stream);
+
+// The whole gradient where dl is zero but at the chosen experts and there are few
+// slots, in all and of an expert on average. Graph replays, so and by the products:
+// T=61, E=256, k=8, H=7168 8.8 us and 15.6; T=16, E=64, k=4, H=2048 2.7 and 7.8;
+// T=128, E=384, k=8, H=7168 13.5 and 17.4; with 16 slots an expert (T=256, E=64,
+// k=4, H=2048) 6.6 and 9.9, with 120 (T=120, E=8, k=8, H=4096) 13.3 and 9.5.
+constexpr int kRouteFewSlots = 1024;
+
+struct RouteFewArgs {
+    const __nv_bfloat16 *x, *w;
+    void *dx, *dw;             // null: not wanted
+    int dw_f32, H;
+};
+
+inline bool route_grad_few(const RouteGradArgs &a)
+{
+    const long long slots = static_cast<long long>(a.T_max) * a.k;
+    return !a.d_logits_add && (a.sigmoid || a.renormalize) && a.T_max <= 256 && slots <= kRouteFewSlots &&
+           slots <= 16LL * a.E;
+}
+
+// (parts, offsets, segments of `a` are not used)
+cudaError_t launch_route_grad_few(const RouteGradArgs &a, const RouteFewArgs &f, cudaStream_t stream);
 // out[i] = sum_s part[s * n + i] in fp32, s ascending, stored as fp32 or bf16; n a multiple of 8
 cudaError_t launch_sum_parts(const float *part, int parts, size_t n, void *out, bool f32, int num_sms,
                              cudaStream_t stream);
