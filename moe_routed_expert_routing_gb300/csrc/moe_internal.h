@@ -457,7 +457,7 @@ cudaError_t launch_route_grad(const RouteGradArgs &a, int num_sms, cudaStream_t 
 
 // The whole gradient where dl is zero but at the chosen experts and there are few
 // slots, in all and of an expert on average. Graph replays, so and by the products:
-// T=61, E=256, k=8, H=7168 8.8 us and 15.6; T=16, E=64, k=4, H=2048 2.7 and 7.8;
+// T=61, E=256, k=8, H=7168 9.6 us and 15.6; T=16, E=64, k=4, H=2048 2.7 and 7.8;
 // T=128, E=384, k=8, H=7168 13.5 and 17.4; with 16 slots an expert (T=256, E=64,
 // k=4, H=2048) 6.6 and 9.9, with 120 (T=120, E=8, k=8, H=4096) 13.3 and 9.5.
 constexpr int kRouteFewSlots = 1024;
