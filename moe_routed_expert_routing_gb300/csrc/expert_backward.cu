@@ -46,8 +46,7 @@ namespace {
 constexpr int kBK = 64;                      // K elements of a stage
 constexpr int kUmmaK = 16;
 constexpr int kTileRows = 256;               // rows of a CTA pair's tile
-constexpr int kSwapRows = 128;               // an expert's last tile of at most this many rows runs swapped
-constexpr int kSwapBox = 32;                 // rows of one of its boxes
+constexpr int kRowBox = 32;                  // rows of a box of a partial tile
 constexpr int kHalf = 128 * 128;             // bytes of one operand's half tile: 128 x 64 bf16
 constexpr int kAtom = 64 * 128;              // bytes of an MN-major block: 64 K rows x 64 columns
 constexpr int kStageBytes = 2 * kHalf;
@@ -62,9 +61,13 @@ struct Config {
     static constexpr int kSmem = 1024 + kStages * kStageBytes + (kBoxes ? kWarps * kBox : 0);
 };
 using ActConfig = Config<6, 8, false>;
-using DeepConfig = Config<6, 4, true>;       // products with many K blocks a tile: more copies in flight
-using WideConfig = Config<5, 8, true>;       // with a few: the epilogue is most of the time
-constexpr int kWideBlocks = 8;               // fewer K blocks a tile than this on average
+using DeepConfig = Config<6, 4, true>;       // products: more copies in flight
+// Small problems, where each unit's way from its first copy to its last store
+// counts: E=16, 64 tokens of 4 experts, H=1024, I=512 (5.9 units a pair) 38.5 us, with
+// DeepConfig 41.7; E=50, 1000 tokens (150 units) 691.6 and 690.9; T=8192, E=128, H=4096,
+// I=1536 5.71 and 5.60 ms.
+using WideConfig = Config<5, 8, true>;
+constexpr int kWideUnits = 6;                // up to so many units a CTA pair
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;   // instruction descriptor: operand is MN-major
 
 // Shared-memory descriptor of an MN-major bf16 tile: blocks of 64 K rows x 64
@@ -126,7 +129,7 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 // The rows of a tile that this CTA's half of A needs, `n` of 128, as whole 32-row
 // boxes, or one box where all are there. MMA rows past them keep whatever the
 // stage held before: they are never stored.
-__device__ __forceinline__ int boxed_rows(int n) { return n <= 0 ? 0 : (n >= 128 ? 128 : (n + kSwapBox - 1) / kSwapBox * kSwapBox); }
+__device__ __forceinline__ int boxed_rows(int n) { return n <= 0 ? 0 : (n >= 128 ? 128 : (n + kRowBox - 1) / kRowBox * kRowBox); }
 
 __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, const CUtensorMap *map32, uint32_t full,
                                           int col, int row, int boxed, uint64_t policy)
@@ -134,7 +137,7 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, 
     if (boxed == 128)
         tma_load_2d_pair(dst, map, full, col, row, policy);
     else
-        for (int i = 0; i < boxed; i += kSwapBox)
+        for (int i = 0; i < boxed; i += kRowBox)
             tma_load_2d_pair(dst + i * 128, map32, full, col, row + i, policy);
 }
 
@@ -156,12 +159,10 @@ struct PairBars {
     uint64_t ufull[2], uempty[2];   // batches of units
 };
 
-// Barriers, TMEM, the experts' offsets (clamped to the batch) and s_tp, the
-// running sum of count(rows) over the experts.
-template <class C, typename Count>
+// Barriers, TMEM, the experts' offsets (clamped to the batch) and their row tiles.
+template <class C>
 __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::kStages> &bars, uint32_t &s_tmem, int &s_abort,
-                                                int *s_off, int *s_tp, const int32_t *offsets, int E, int cap,
-                                                Count count)
+                                                int *s_off, int *s_tp, const int32_t *offsets, int E, int cap)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     PairState st;
@@ -194,25 +195,8 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::k
         s_off[i] = o < 0 ? 0 : (o > cap ? cap : o);
     }
     __syncthreads();
-    if (warp == 3) {
-        int carry = 0;
-        for (int base = 0; base < E; base += 32) {
-            const int e = base + lane;
-            const int n = e < E ? count(max(s_off[e + 1] - s_off[e], 0)) : 0;
-            int v = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int w = __shfl_up_sync(kFull, v, o);
-                if (lane >= o)
-                    v += w;
-            }
-            if (e < E)
-                s_tp[e] = carry + v - n;
-            carry += __shfl_sync(kFull, v, 31);
-        }
-        if (lane == 0)
-            s_tp[E] = carry;
-    }
+    if (warp == 3)
+        build_tile_prefix(s_off, s_tp, E, kTileRows, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // both CTAs' barriers initialised before any remote arrive
@@ -269,8 +253,7 @@ struct __align__(16) UnitDesc {
     int period;          // after how many of them B begins again
     int rem;             // rows of the last K block when that is not whole, else 0
     int k_row0;          // first K row, where K runs along the batch
-    int swap;            // output rows on the MMA's N side: how many, a multiple of 64; else 0
-    int pad[2];
+    int pad[3];
 };
 
 constexpr int kBatch = 32;
@@ -343,9 +326,6 @@ __device__ __forceinline__ void publish_units(const PairState &st, PairBars<kSta
     }
 }
 
-// Rows on the N side of a tile of `rows` rows, or 0: runs as usual.
-__device__ __forceinline__ int swap_rows(int rows) { return rows <= kSwapRows ? (rows + 63) & ~63 : 0; }
-
 // 32 rows x 128 bytes of an epilogue warp's box at `box` (128-byte swizzle),
 // rows [first, first + 32) of a tile with `rows` of them, to element (c0, r0 +
 // first) of `map`; boxes that hold rows past the tile go row by row.
@@ -396,42 +376,25 @@ struct ActArgs {
     __nv_bfloat16 *dgu;      // [cap + 1, 2I]
     uint64_t wait_limit_ns;
     int E, cap, H, I;
-    int swaps;               // an expert's last rows may run swapped
 };
 
-// An expert's units: column tiles of 128 x its whole row tiles, column tile
-// outside (the row tiles that share one weight tile go to neighbouring pairs);
-// then, if its last row tile runs swapped, that tile's columns by 256.
-__device__ __forceinline__ int act_units_of(int rows, int NT, int NT2, bool swaps)
+// Column tile, then row tile: the row tiles that share one weight tile go to
+// neighbouring pairs. (A last tile of at most 128 rows turned round, weights on
+// the MMAs' M side and its rows on N, saves MMAs on padding, but with partial
+// tiles that load only their rows it does not pay: 256 rows an expert, E=128, H=4096,
+// I=1536 3.48 ms with it and 3.35 without, 120 rows 702 us and 690; only very few long
+// ones gain, 10 rows of each of 5 experts, H=3904, I=960 92 us and 100.)
+__device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, const int *s_tp, int E, int NT)
 {
-    const int tiles = (rows + kTileRows - 1) / kTileRows;
-    const int last = rows - (tiles - 1) * kTileRows;
-    return tiles == 0 ? 0 : (swaps && swap_rows(last) ? (tiles - 1) * NT + NT2 : tiles * NT);
-}
-
-__device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, const int *s_up, int E, int NT, bool swaps)
-{
-    const int e = find_expert(s_up, E, u, 1);
-    const int rows = s_off[e + 1] - s_off[e];
-    int tiles = (rows + kTileRows - 1) / kTileRows;
-    const int last = rows - (tiles - 1) * kTileRows;
-    const int swap = swaps ? swap_rows(last) : 0;
-    const int whole = swap ? tiles - 1 : tiles;
-    const int local = u - s_up[e];
+    const int e = find_expert(s_tp, E, u, NT);
+    const int local = u - s_tp[e] * NT;
+    const int tiles = s_tp[e + 1] - s_tp[e];
+    const int nt = local / tiles;
     d.job = 0;
     d.e = e;
-    if (local < whole * NT) {
-        const int nt = local / whole;
-        const int rt = local - nt * whole;
-        d.m0 = s_off[e] + rt * kTileRows;
-        d.rows = min(rows - rt * kTileRows, kTileRows);
-        d.n0 = nt * 128;
-    } else {
-        d.m0 = s_off[e] + whole * kTileRows;
-        d.rows = last;
-        d.n0 = (local - whole * NT) * 256;
-        d.swap = swap;
-    }
+    d.m0 = s_off[e] + (local - nt * tiles) * kTileRows;
+    d.rows = min(s_off[e + 1] - d.m0, kTileRows);
+    d.n0 = nt * 128;
 }
 
 // One element's gradients from its gate, up and da values. The fast exponential
@@ -448,9 +411,7 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float &a,
 // TMEM columns: da of even and odd units in 0..127 and 128..255, gate and up
 // in 256..383 and 384..511. A unit's da comes first, so that it can be
 // multiplied while the unit before is still being read out: a third of the
-// unit's MMAs, which hides that unit's epilogue. A swapped unit has 256
-// columns of the intermediate size on the MMA's M side and its rows on N, each
-// of da, gate and up a phase of its own.
+// unit's MMAs, which hides that unit's epilogue.
 __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const __grid_constant__ ActArgs args)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -458,12 +419,11 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ int s_off[kMaxExperts + 1];
-    __shared__ int s_up[kMaxExperts + 1];
+    __shared__ int s_tp[kMaxExperts + 1];
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int NT = (args.I + 127) / 128, NT2 = (args.I + 255) / 256;
-    const PairState st = pair_begin<ActConfig>(smem_raw, bars, s_tmem, s_abort, s_off, s_up, args.offsets, args.E, args.cap,
-                                               [&](int rows) { return act_units_of(rows, NT, NT2, args.swaps != 0); });
+    const int NT = (args.I + 127) / 128;
+    const PairState st = pair_begin<ActConfig>(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap);
     volatile int *abort_flag = &s_abort;
     const int k_blocks = args.H / kBK;
     pdl_trigger();    // the products' CTAs need this kernel's shared memory: each starts as one here ends
@@ -485,14 +445,12 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
             UnitReader units(s_units, bars.ufull, bars.uempty);
             bool ok = true;
             while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
-                const int swap = t->swap, half = swap >> 1, n0 = t->n0;
-                const int a_row = t->m0 + (swap ? half : 128) * rank;
+                const int n0 = t->n0;
+                const int a_row = t->m0 + 128 * rank;
                 const int boxed = boxed_rows(t->rows - 128 * rank);
                 const int w2_row = t->e * args.H;
-                const int gate = t->e * 2 * args.I + n0;
-                int phase = 0, kp = 0;
-                const int total = (swap ? 3 : 2) * k_blocks;
-                for (int kb = 0; kb < total; ++kb, r.next()) {
+                const int w13_row = t->e * 2 * args.I + n0 + (rank ? args.I : 0);
+                for (int kb = 0; kb < 2 * k_blocks; ++kb, r.next()) {
                     if (!mbar_wait_bounded(smem_u32(&bars.empty[r.stage]), r.phase ^ 1u, abort_flag,
                                            args.wait_limit_ns)) {
                         ok = false;
@@ -501,32 +459,16 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
                     const uint32_t full = map_to_cta(smem_u32(&bars.full[r.stage]), 0);
                     const uint32_t a_dst = smem_u32(st.smem + r.stage * kStageBytes);
                     const uint32_t b_dst = a_dst + kHalf;
-                    const int kc = kp * kBK;
-                    if (!swap) {
-                        if (phase == 0) {
-                            mbar_arrive_expect_tx_cluster(full, boxed * 128 + kAtom);
-                            load_rows(a_dst, &args.dy, &args.dy32, full, kc, a_row, boxed, pol_a);
-                            tma_load_2d_pair(b_dst, &args.w2, full, n0 + 64 * rank, w2_row + kc, pol_w);
-                        } else {
-                            mbar_arrive_expect_tx_cluster(full, boxed * 128 + kHalf);
-                            load_rows(a_dst, &args.x, &args.x32, full, kc, a_row, boxed, pol_a);
-                            tma_load_2d_pair(b_dst, &args.w13, full, kc, gate + (rank ? args.I : 0), pol_w);
-                        }
+                    if (kb < k_blocks) {
+                        const int kc = kb * kBK;
+                        mbar_arrive_expect_tx_cluster(full, boxed * 128 + kAtom);
+                        load_rows(a_dst, &args.dy, &args.dy32, full, kc, a_row, boxed, pol_a);
+                        tma_load_2d_pair(b_dst, &args.w2, full, n0 + 64 * rank, w2_row + kc, pol_w);
                     } else {
-                        mbar_arrive_expect_tx_cluster(full, kHalf + half * 128);
-                        if (phase == 0) {
-                            tma_load_2d_pair(a_dst, &args.w2, full, n0 + 128 * rank, w2_row + kc, pol_w);
-                            tma_load_2d_pair(a_dst + kAtom, &args.w2, full, n0 + 128 * rank + 64, w2_row + kc, pol_w);
-                        } else {
-                            tma_load_2d_pair(a_dst, &args.w13, full, kc, gate + (phase == 2 ? args.I : 0) + 128 * rank, pol_w);
-                        }
-                        const CUtensorMap *m = phase == 0 ? &args.dy32 : &args.x32;
-                        for (int i = 0; i < half; i += kSwapBox)
-                            tma_load_2d_pair(b_dst + i * 128, m, full, kc, a_row + i, pol_a);
-                    }
-                    if (++kp == k_blocks) {
-                        kp = 0;
-                        ++phase;
+                        const int kc = (kb - k_blocks) * kBK;
+                        mbar_arrive_expect_tx_cluster(full, boxed * 128 + kHalf);
+                        load_rows(a_dst, &args.x, &args.x32, full, kc, a_row, boxed, pol_a);
+                        tma_load_2d_pair(b_dst, &args.w13, full, kc, w13_row, pol_w);
                     }
                 }
             }
@@ -538,10 +480,8 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
             UnitReader units(s_units, bars.ufull, bars.uempty);
             bool ok = true;
             int local = 0;
-            while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
-                const int swap = t->swap;
-                const int phases = swap ? 3 : 2;
-                for (int phase = 0; ok && phase < phases; ++phase) {
+            while (ok && units.next(abort_flag, args.wait_limit_ns)) {
+                for (int phase = 0; ok && phase < 2; ++phase) {
                     // gate and up of the unit before have been read (and with them the da before that)
                     if (phase == 1 && !mbar_wait_bounded(smem_u32(&bars.tempty[0]), (local & 1) ^ 1u, abort_flag,
                                                          args.wait_limit_ns)) {
@@ -549,11 +489,10 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d = st.tmem + (phase == 0 ? 128 * (local & 1) : 128 + 128 * phase);
+                    const uint32_t d = st.tmem + (phase == 0 ? 128 * (local & 1) : 256);
                     // K advances 16 elements a step: 32 bytes of a K-major tile, 2048 of an MN-major one
-                    const bool a_mn = swap && phase == 0, b_mn = !swap && phase == 0;
-                    const uint32_t idesc = swap ? idesc_bf16_f32(256, swap) | (a_mn ? kMajorA : 0u)
-                                                : (b_mn ? idesc_bf16_f32(256, 128) | kMajorB : idesc_bf16_f32(256, 256));
+                    const bool b_mn = phase == 0;
+                    const uint32_t idesc = b_mn ? idesc_bf16_f32(256, 128) | kMajorB : idesc_bf16_f32(256, 256);
                     for (int kb = 0; kb < k_blocks; ++kb, r.next()) {
                         if (!mbar_wait_bounded(smem_u32(&bars.full[r.stage]), r.phase, abort_flag, args.wait_limit_ns)) {
                             ok = false;
@@ -562,12 +501,12 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
                         tc_fence_after();
                         const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
                         const uint32_t b_addr = a_addr + kHalf;
-                        const uint64_t a0 = a_mn ? smem_desc_mnmajor_sw128(a_addr) : smem_desc_kmajor_sw128(a_addr);
+                        const uint64_t a0 = smem_desc_kmajor_sw128(a_addr);
                         const uint64_t b0 = b_mn ? smem_desc_mnmajor_sw128(b_addr) : smem_desc_kmajor_sw128(b_addr);
-                        const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+                        const uint32_t sb = b_mn ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
                         for (int kk = 0; kk < kBK / kUmmaK; ++kk)
-                            umma_bf16_pair(d, a0 + kk * sa, b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                            umma_bf16_pair(d, a0 + kk * (32 >> 4), b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
                         umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                     }
                 }
@@ -580,8 +519,8 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
         }
         __syncwarp();
     } else if (warp == 2) {
-        publish_units(st, bars, s_units, s_up[args.E], abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
-            act_unit(u, d, s_off, s_up, args.E, NT, args.swaps != 0);
+        publish_units(st, bars, s_units, s_tp[args.E] * NT, abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
+            act_unit(u, d, s_off, s_tp, args.E, NT);
         });
     } else if (warp >= 4) {
         const int q = warp & 3, half = (warp - 4) >> 2;
@@ -597,61 +536,34 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
             tc_fence_after();
             const uint32_t lanes = st.tmem + (static_cast<uint32_t>(q * 32) << 16);
             const uint32_t t_da = lanes + 128 * (local & 1), t_gu = lanes + 256;
-            if (!t.swap) {
-                const int r = 128 * rank + q * 32 + lane;
-                const bool valid = r < t.rows;
-                const int cols = min(args.I - t.n0, 128);     // a multiple of 64
-                __nv_bfloat16 *const act = args.act + static_cast<size_t>(t.m0 + r) * args.I + t.n0;
-                __nv_bfloat16 *const dgu = args.dgu + static_cast<size_t>(t.m0 + r) * 2 * args.I + t.n0;
+            const int r = 128 * rank + q * 32 + lane;
+            const bool valid = r < t.rows;
+            const int cols = min(args.I - t.n0, 128);     // a multiple of 64
+            __nv_bfloat16 *const act = args.act + static_cast<size_t>(t.m0 + r) * args.I + t.n0;
+            __nv_bfloat16 *const dgu = args.dgu + static_cast<size_t>(t.m0 + r) * 2 * args.I + t.n0;
 #pragma unroll 1
-                for (int c = 64 * half; c < cols && c < 64 * half + 64; c += 16) {
-                    uint32_t vg[16], vu[16], vd[16];
-                    tmem_ld_32x32b_x16(t_gu + c, vg);
-                    tmem_ld_32x32b_x16(t_gu + 128 + c, vu);
-                    tmem_ld_32x32b_x16(t_da + c, vd);
-                    tmem_wait_ld();
-                    uint32_t o[3][8];
+            for (int c = 64 * half; c < cols && c < 64 * half + 64; c += 16) {
+                uint32_t vg[16], vu[16], vd[16];
+                tmem_ld_32x32b_x16(t_gu + c, vg);
+                tmem_ld_32x32b_x16(t_gu + 128 + c, vu);
+                tmem_ld_32x32b_x16(t_da + c, vd);
+                tmem_wait_ld();
+                uint32_t o[3][8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float a[2], g[2], w[2];
+                for (int i = 0; i < 8; ++i) {
+                    float a[2], g[2], w[2];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            swiglu_grad(__uint_as_float(vg[2 * i + j]), __uint_as_float(vu[2 * i + j]),
-                                        __uint_as_float(vd[2 * i + j]), a[j], g[j], w[j]);
-                        o[0][i] = pack_bf16x2(a[0], a[1]);
-                        o[1][i] = pack_bf16x2(g[0], g[1]);
-                        o[2][i] = pack_bf16x2(w[0], w[1]);
-                    }
-                    if (valid) {   // the workspace is 256-byte aligned, its rows whole 128-byte lines
-                        store32(act + c, o[0]);
-                        store32(dgu + c, o[1]);
-                        store32(dgu + args.I + c, o[2]);
-                    }
+                    for (int j = 0; j < 2; ++j)
+                        swiglu_grad(__uint_as_float(vg[2 * i + j]), __uint_as_float(vu[2 * i + j]),
+                                    __uint_as_float(vd[2 * i + j]), a[j], g[j], w[j]);
+                    o[0][i] = pack_bf16x2(a[0], a[1]);
+                    o[1][i] = pack_bf16x2(g[0], g[1]);
+                    o[2][i] = pack_bf16x2(w[0], w[1]);
                 }
-            } else {
-                // lane = column, TMEM columns = the unit's rows
-                const int n = t.n0 + 128 * rank + q * 32 + lane;
-                const bool col_ok = n < args.I;
-                __nv_bfloat16 *const act = args.act + static_cast<size_t>(t.m0) * args.I + n;
-                __nv_bfloat16 *const dgu = args.dgu + static_cast<size_t>(t.m0) * 2 * args.I + n;
-#pragma unroll 1
-                for (int c = 16 * half; c < t.rows; c += 32) {
-                    uint32_t vg[16], vu[16], vd[16];
-                    tmem_ld_32x32b_x16(t_gu + c, vg);
-                    tmem_ld_32x32b_x16(t_gu + 128 + c, vu);
-                    tmem_ld_32x32b_x16(t_da + c, vd);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float a, g, w;
-                        swiglu_grad(__uint_as_float(vg[i]), __uint_as_float(vu[i]), __uint_as_float(vd[i]), a, g, w);
-                        if (col_ok && c + i < t.rows) {
-                            const size_t r = static_cast<size_t>(c + i);
-                            act[r * args.I] = __float2bfloat16_rn(a);
-                            dgu[r * 2 * args.I] = __float2bfloat16_rn(g);
-                            dgu[r * 2 * args.I + args.I] = __float2bfloat16_rn(w);
-                        }
-                    }
+                if (valid) {   // the workspace is 256-byte aligned, its rows whole 128-byte lines
+                    store32(act + c, o[0]);
+                    store32(dgu + c, o[1]);
+                    store32(dgu + args.I + c, o[2]);
                 }
             }
             tc_fence_before();
@@ -704,7 +616,6 @@ __device__ __forceinline__ void product_unit(int u, UnitDesc &d, const ProductAr
         d.rows = min(s_off[d.e + 1] - d.m0, kTileRows);
         d.total = j.k_blocks;
         d.period = j.wrap;
-        d.swap = swap_rows(d.rows);
     } else {
         const int MT = (j.M + 255) / 256;
         d.e = u / (MT * NT);
@@ -712,12 +623,7 @@ __device__ __forceinline__ void product_unit(int u, UnitDesc &d, const ProductAr
         const int mt = u / NT;
         d.m0 = mt * 256;
         d.n0 = (u - mt * NT) * tile_n;
-        if (j.rows_on_n) {
-            d.rows = min(j.N - d.n0, 128);
-            d.swap = 128;
-        } else {
-            d.rows = min(j.M - d.m0, 256);
-        }
+        d.rows = j.rows_on_n ? min(j.N - d.n0, 128) : min(j.M - d.m0, 256);
         const int k = max(s_off[d.e + 1] - s_off[d.e], 0);
         d.period = (k + kBK - 1) / kBK;
         d.total = d.period;
@@ -776,8 +682,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
     __shared__ int s_tp[kMaxExperts + 1];
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap,
-                                       [](int rows) { return (rows + kTileRows - 1) / kTileRows; });
+    const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap);
     volatile int *abort_flag = &s_abort;
     const int rank = static_cast<int>(st.rank);
 
@@ -792,11 +697,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                 const ProductJob &j = args.job[t.job];
                 const CUtensorMap *ma = &args.a[t.job], *mb = &args.b[t.job], *ma32 = &args.a32[t.job];
                 const bool by_rows = j.by_rows != 0;
-                const int half = t.swap >> 1;
                 const bool on_n = j.rows_on_n != 0;
                 // B's two blocks of 64 columns in this CTA: neighbours, or the two parts of 64 columns
                 const int b_col = t.n0 + (on_n ? 64 : 128) * rank, b_next = on_n ? j.part_cols : 64;
-                const int a_row = t.m0 + (t.swap ? half : 128) * rank;    // rows kind
+                const int a_row = t.m0 + 128 * rank;                      // rows kind
                 const int b_row0 = t.e * j.b_expert_rows;
                 const int boxed = boxed_rows(t.rows - 128 * rank);
                 const int a_col = t.m0 + 128 * rank;                      // weights kind
@@ -812,16 +716,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                     const uint32_t b_dst = a_dst + kHalf;
                     if (by_rows) {
                         const int b_row = b_row0 + kp * kBK;
-                        // swapped: B's columns on the MMA's M side
-                        const uint32_t w_dst = t.swap ? a_dst : b_dst;
-                        mbar_arrive_expect_tx_cluster(full, kHalf + (t.swap ? half : boxed) * 128);
-                        tma_load_2d_pair(w_dst, mb, full, b_col, b_row, pol);
-                        tma_load_2d_pair(w_dst + kAtom, mb, full, b_col + 64, b_row, pol);
-                        if (!t.swap)
-                            load_rows(a_dst, ma, ma32, full, kb * kBK, a_row, boxed, pol);
-                        else
-                            for (int i = 0; i < half; i += kSwapBox)
-                                tma_load_2d_pair(b_dst + i * 128, ma32, full, kb * kBK, a_row + i, pol);
+                        mbar_arrive_expect_tx_cluster(full, kHalf + boxed * 128);
+                        tma_load_2d_pair(b_dst, mb, full, b_col, b_row, pol);
+                        tma_load_2d_pair(b_dst + kAtom, mb, full, b_col + 64, b_row, pol);
+                        load_rows(a_dst, ma, ma32, full, kb * kBK, a_row, boxed, pol);
                     } else {
                         const int row = t.k_row0 + kp * kBK;
                         if (t.rem && kp + 1 == t.period) {
@@ -877,13 +775,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
             bool ok = true;
             int local = 0;
             while (const UnitDesc *tp = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
-                const int total = tp->total, rem = tp->rem, swap = tp->swap;
+                const int total = tp->total, rem = tp->rem;
                 const bool by_rows = args.job[tp->job].by_rows != 0, on_n = args.job[tp->job].rows_on_n != 0;
-                // rows kind: A K-major, B MN-major, or the other way round when swapped; weights kind: both MN-major
-                const bool a_mn = !by_rows || swap, b_mn = !by_rows || !swap;
-                const uint32_t idesc =
-                    idesc_bf16_f32(256, swap ? swap : 256) | (a_mn ? kMajorA : 0u) | (b_mn ? kMajorB : 0u);
-                const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+                // rows kind: A K-major, B MN-major; weights kind: both MN-major. K steps as above
+                const uint32_t idesc = idesc_bf16_f32(256, on_n ? 128 : 256) | (by_rows ? 0u : kMajorA) | kMajorB;
+                const uint32_t sa = by_rows ? 32 >> 4 : 2048 >> 4, sb = 2048 >> 4;
                 const int buf = local & 1;
                 if (!mbar_wait_bounded(smem_u32(&bars.tempty[buf]), ((local >> 1) & 1) ^ 1u, abort_flag,
                                        args.wait_limit_ns)) {
@@ -900,8 +796,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
                     const uint32_t b_addr = a_addr + kHalf;
-                    const uint64_t a0 = a_mn ? smem_desc_mnmajor_sw128(a_addr) : smem_desc_kmajor_sw128(a_addr);
-                    const uint64_t b0 = b_mn ? smem_desc_mnmajor_sw128(b_addr) : smem_desc_kmajor_sw128(b_addr);
+                    const uint64_t a0 = by_rows ? smem_desc_kmajor_sw128(a_addr) : smem_desc_mnmajor_sw128(a_addr);
+                    const uint64_t b0 = smem_desc_mnmajor_sw128(b_addr);
                     const int steps = (rem && kb + 1 == total) ? (rem + kUmmaK - 1) / kUmmaK : kBK / kUmmaK;
 #pragma unroll
                     for (int kk = 0; kk < kBK / kUmmaK; ++kk)
@@ -944,16 +840,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                 break;
             tc_fence_after();
             const uint32_t t_row = st.tmem + buf * 256 + (static_cast<uint32_t>(q * 32) << 16);
-            if (!t.swap) {
+            if (!j.rows_on_n) {
                 const int r0 = t.m0 + (j.by_rows ? 0 : t.e * j.M);
                 if (t.total || !j.accumulate)
                     store_tile(t_row, box, j, &args.out[t.job], r0, 128 * rank + q * 32, t.rows, t.n0, half * 128,
                                kHalves == 1 ? 256 : half * 128 + 128, t.total == 0);
             } else {
-                // lane = column, TMEM columns = the unit's rows
-                const int col = (j.by_rows ? t.n0 : t.m0) + 128 * rank + q * 32 + lane;
-                const int cols = j.by_rows ? j.N : j.M;
-                const size_t row0 = j.by_rows ? static_cast<size_t>(t.m0) : static_cast<size_t>(t.e) * j.N + t.n0;
+                // lane = column (a row of the MMA's M side), TMEM columns = the unit's rows
+                const int col = t.m0 + 128 * rank + q * 32 + lane, cols = j.M;
+                const size_t row0 = static_cast<size_t>(t.e) * j.N + t.n0;
                 const bool col_ok = col < cols;
 #pragma unroll 1
                 for (int c = 16 * half; c < t.rows; c += 16 * kHalves) {
@@ -1049,7 +944,7 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
                             int num_sms, cudaStream_t stream)
 {
     ProductArgs a = {};
-    long long units = 0, live = 0, blocks = 0;
+    long long units = 0, live = 0;
     for (int i = 0; i < n; ++i) {
         const ProductJob &j = jobs[i];
         a.job[i] = j;
@@ -1057,7 +952,7 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
         const uint64_t out_rows = j.by_rows ? static_cast<uint64_t>(cap) : static_cast<uint64_t>(E) * j.M;
         const uint64_t b_rows = j.b_rows, b_cols = j.b_cols;
         if (!make_tile_map(&a.a[i], j.a, a_rows, a_cols, j.by_rows ? 128 : 64) ||
-            (j.by_rows && !make_tile_map(&a.a32[i], j.a, a_rows, a_cols, kSwapBox)) ||
+            (j.by_rows && !make_tile_map(&a.a32[i], j.a, a_rows, a_cols, kRowBox)) ||
             (!j.by_rows && (!make_tile_map(&a.a16[i], j.a, a_rows, a_cols, kUmmaK) ||
                             !make_tile_map(&a.b16[i], j.b, b_rows, b_cols, kUmmaK) ||
                             !make_tile_map(&a.a1[i], j.a, a_rows, a_cols, 1) ||
@@ -1067,11 +962,9 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
                         : make_tile_map(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32))))
             return cudaErrorInvalidValue;
         units += product_units(j, E, cap);
-        // units with rows spread evenly, and their K blocks
-        const long long n_live = j.by_rows ? (tiles_of(cap) > E ? tiles_of(cap) : (cap < E ? cap : E)) * tiles_of(j.N)
-                                           : product_units(j, E, cap);
-        live += n_live;
-        blocks += n_live * (j.by_rows ? j.k_blocks : (cap / E + kBK - 1) / kBK);
+        // as many as there are with rows spread evenly
+        live += j.by_rows ? (tiles_of(cap) > E ? tiles_of(cap) : (cap < E ? cap : E)) * tiles_of(j.N)
+                          : product_units(j, E, cap);
     }
     a.jobs = n;
     a.offsets = offsets;
@@ -1079,7 +972,7 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
     a.cap = cap;
     a.err = err;
     a.wait_limit_ns = kWaitLimitNs;
-    if (blocks < kWideBlocks * live)
+    if (live <= kWideUnits * (num_sms / 2))
         return launch_pair<WideConfig>(products_kernel<WideConfig>, a, units, num_sms, stream);
     return launch_pair<DeepConfig>(products_kernel<DeepConfig>, a, units, num_sms, stream);
 }
@@ -1091,7 +984,7 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
     ActArgs a = {};
     const uint64_t rows = cap, h = H, i = I, e = E;
     if (!make_tile_map(&a.x, x, rows, h, 128) || !make_tile_map(&a.dy, dy, rows, h, 128) ||
-        !make_tile_map(&a.x32, x, rows, h, kSwapBox) || !make_tile_map(&a.dy32, dy, rows, h, kSwapBox) ||
+        !make_tile_map(&a.x32, x, rows, h, kRowBox) || !make_tile_map(&a.dy32, dy, rows, h, kRowBox) ||
         !make_tile_map(&a.w13, W13, e * 2 * i, h, 128) || !make_tile_map(&a.w2, W2, e * h, i, 64))
         return cudaErrorInvalidValue;
     a.offsets = offsets;
@@ -1103,10 +996,6 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
     a.cap = cap;
     a.H = H;
     a.I = I;
-    // Swapped units are half as many: not while the others leave CTA pairs idle
-    // (E=16, 64 tokens of 4 experts, H=1024, I=512: @@ us so, @@ swapped)
-    const long long tiles = tiles_of(cap) > E ? tiles_of(cap) : (cap < E ? cap : E);
-    a.swaps = tiles * ((I + 127) / 128) > num_sms / 2;
     return launch_pair<ActConfig>(act_grad_kernel, a, (tiles_of(cap) + E) * ((I + 127) / 128), num_sms, stream);
 }
 
