@@ -799,13 +799,18 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                     const uint64_t a0 = by_rows ? smem_desc_kmajor_sw128(a_addr) : smem_desc_mnmajor_sw128(a_addr);
                     const uint64_t b0 = smem_desc_mnmajor_sw128(b_addr);
                     const int steps = (rem && kb + 1 == total) ? (rem + kUmmaK - 1) / kUmmaK : kBK / kUmmaK;
-#pragma unroll
-                    for (int kk = 0; kk < kBK / kUmmaK; ++kk)
-                        if (kk < steps) {
+                    // two loops: with the second part's MMA as a branch inside one, the rows kind took a third longer
+                    if (on_n) {
+                        for (int kk = 0; kk < steps; ++kk) {
                             umma_bf16_pair(d, a0 + kk * sa, b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-                            if (on_n)     // B's second part
-                                umma_bf16_pair(d, a0 + kk * sa, b0 + (kAtom >> 4) + kk * sb, idesc, 1u);
+                            umma_bf16_pair(d, a0 + kk * sa, b0 + (kAtom >> 4) + kk * sb, idesc, 1u);
                         }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < kBK / kUmmaK; ++kk)
+                            if (kk < steps)
+                                umma_bf16_pair(d, a0 + kk * sa, b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                    }
                     umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (ok)
