@@ -513,7 +513,8 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
  *   moe_route_backward     d_weights       -> dx (the router's part), dw_router
  *   moe_dispatch_backward  dx_sorted       -> dx (all of it)
  *   moe_norm_backward      dx              -> dh, dw
- * Every operator is deterministic: sums go in a fixed order, no atomics.
+ * Every operator is deterministic: sums go in a fixed order, no atomics. Buffers
+ * do not overlap but where an entry point says so.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -521,7 +522,8 @@ moe_status_t moe_layer(const moe_layer_problem_t *problem, const void *h, const 
  *   dy_sorted[r, m]  = bf16( w[t, j] * d_out[t, m] )
  *   d_weights[t, j]  = sum_m d_out[t, m] y_sorted[r, m]       (fp32)
  *   d_out[T_max, H] bf16, y_sorted[cap, H] fp32 (NULL without d_weights),
- *   inv[T_max*k] and topk_weights[T_max, k] as for moe_combine,
+ *   inv[T_max*k] and topk_weights[T_max, k] as for moe_combine (no two slots
+ *   with one row; a row outside [0, cap) counts as dropped),
  *   dy_sorted[cap, H] bf16 out: rows that no slot holds are not written,
  *   d_weights[T_max, k] fp32 out, 0 for a dropped slot, or NULL (not wanted).
  * Slots of tokens >= T are not read or written.
@@ -536,7 +538,7 @@ moe_status_t moe_combine_backward(const moe_problem_t *problem, const void *d_ou
  * in fp32, j ascending, dropped slots skipped, dx_add last.
  *   dx_sorted[cap, H] of dx_dtype (moe_dtype_t), dx_add[T_max, H] bf16 or NULL
  *   (the gradient that reaches x on another path, the router's), dx[T_max, H]
- *   bf16 out, rows >= T untouched. dx may be dx_add.
+ *   bf16 out, rows >= T untouched. dx may be dx_add; inv as above.
  */
 moe_status_t moe_dispatch_backward(const moe_problem_t *problem, int32_t dx_dtype, const void *dx_sorted,
                                    const int32_t *inv, const void *dx_add, const int32_t *d_num_tokens, void *dx,
@@ -568,7 +570,8 @@ moe_status_t moe_expert_backward_workspace_size(const moe_expert_grad_problem_t 
  *   moe_expert_compute; dx_sorted[cap, H], dW13[E, 2I, H], dW2[E, H, I] out, each
  *   NULL if not wanted, not all. Rows of dx_sorted at and past
  *   expert_offsets[E] are not written; rows of the inputs there do not count,
- *   whatever they hold.
+ *   whatever they hold. A row that is not finite leaves its own expert's weight
+ *   gradients not finite (an infinity may come out as NaN), no other's.
  */
 moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const void *x_sorted,
                                  const int32_t *expert_offsets, const void *W13, const void *W2, const void *dy_sorted,
@@ -587,7 +590,8 @@ moe_status_t moe_norm_backward_workspace_size(const moe_norm_problem_t *problem,
  *   weight); dx[T_max, H] bf16, rows x_stride apart; dh_add[T_max, H] of
  *   h_dtype, rows y_stride apart, or NULL (the gradient that reaches h past the
  *   block); dh[T_max, H] of h_dtype out, rows out_stride apart; dw[H] of
- *   w_dtype out, or NULL. dh may be h or dh_add, with the same stride.
+ *   w_dtype out, or NULL. dh may be h or dh_add, with the same stride; no other
+ *   buffers may overlap.
  * norm_block, gate and residual_scale are not read. ws: only its device error
  * word has to start at zero (a wait inside the kernel that gave up sets
  * MOE_DEVERR_WAIT_TIMEOUT).

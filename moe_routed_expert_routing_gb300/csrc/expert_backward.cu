@@ -31,8 +31,8 @@
 // that the workspace keeps behind a, [dg du] and the router's gradient, against
 // the expert's own last row in the other operand. (Zeroing the rows in shared
 // memory instead, by a warp between the copy and the MMAs, cost about 1 us for
-// every tile of 256 x 256, in a loop that waits for its copies: weight
-// gradients of 512 rows an expert, E=128, H=4096, I=1536, @@.)
+// every tile of 256 x 256, in a loop that waits for its copies: dW13 at T=8192,
+// E=128, H=4096, I=1536 1.69 ms, so 1.27.)
 #include <cuda_bf16.h>
 
 #include "moe_internal.h"
@@ -224,6 +224,29 @@ __device__ __forceinline__ void pair_end(const PairState &st, int &s_abort, int3
         atomicOr(err, MOE_DEVERR_WAIT_TIMEOUT);
 }
 
+// The MMAs of `steps` times 16 K elements of one stage. The majors are known when
+// it is compiled: one thread issues a pair's MMAs, in 256 to 512 cycles a stage,
+// and a branch between the steps (the router's second part beside the plain
+// step) cost the products a third of their rate: dx at E=16, T=8192, H=4096, I=1536
+// 1.29 ms and 0.93.
+template <bool kAMn, bool kBMn>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t a_addr, uint32_t idesc, bool first, int steps)
+{
+    constexpr uint32_t kA = kAMn ? 2048 >> 4 : 32 >> 4, kB = kBMn ? 2048 >> 4 : 32 >> 4;
+    const uint32_t b_addr = a_addr + kHalf;
+    const uint64_t a0 = kAMn ? smem_desc_mnmajor_sw128(a_addr) : smem_desc_kmajor_sw128(a_addr);
+    const uint64_t b0 = kBMn ? smem_desc_mnmajor_sw128(b_addr) : smem_desc_kmajor_sw128(b_addr);
+    if (steps == kBK / kUmmaK) {
+        umma_bf16_pair(d, a0, b0, idesc, first ? 0u : 1u);
+#pragma unroll
+        for (int kk = 1; kk < kBK / kUmmaK; ++kk)
+            umma_bf16_pair(d, a0 + kk * kA, b0 + kk * kB, idesc, 1u);
+    } else {
+        for (int kk = 0; kk < steps; ++kk)
+            umma_bf16_pair(d, a0 + kk * kA, b0 + kk * kB, idesc, (first && kk == 0) ? 0u : 1u);
+    }
+}
+
 template <int kStages>
 struct Ring {
     int stage = 0;
@@ -242,8 +265,8 @@ struct Ring {
 // A unit of work, decoded. A warp of its own decodes 32 units at a time, one a
 // lane, into one of two batches in shared memory, and every role reads them
 // from there: decoding takes some 2 us of divisions and searches, which each
-// role spent between two units before (weight gradients of 512 rows an expert,
-// E=128, H=4096, I=1536: 2.8 ms, and with the batches @@).
+// role spent between two units before (with it and TMA stores: T=8192,
+// E=128, H=4096, I=1536 6.25 -> 5.63 ms; E=50, T=1000 1.00 -> 0.73 ms).
 struct __align__(16) UnitDesc {
     int job;             // products: which; -1: no more units
     int e;
@@ -481,34 +504,31 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
             bool ok = true;
             int local = 0;
             while (ok && units.next(abort_flag, args.wait_limit_ns)) {
-                for (int phase = 0; ok && phase < 2; ++phase) {
-                    // gate and up of the unit before have been read (and with them the da before that)
-                    if (phase == 1 && !mbar_wait_bounded(smem_u32(&bars.tempty[0]), (local & 1) ^ 1u, abort_flag,
-                                                         args.wait_limit_ns)) {
+                // da, then gate and up, once those of the unit before have been read (and with them the da before that)
+                constexpr uint32_t kIdescDa = idesc_bf16_f32(256, 128) | kMajorB, kIdescGu = idesc_bf16_f32(256, 256);
+                const uint32_t d_da = st.tmem + 128 * (local & 1), d_gu = st.tmem + 256;
+                for (int kb = 0; kb < k_blocks; ++kb, r.next()) {
+                    if (!mbar_wait_bounded(smem_u32(&bars.full[r.stage]), r.phase, abort_flag, args.wait_limit_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d = st.tmem + (phase == 0 ? 128 * (local & 1) : 256);
-                    // K advances 16 elements a step: 32 bytes of a K-major tile, 2048 of an MN-major one
-                    const bool b_mn = phase == 0;
-                    const uint32_t idesc = b_mn ? idesc_bf16_f32(256, 128) | kMajorB : idesc_bf16_f32(256, 256);
-                    for (int kb = 0; kb < k_blocks; ++kb, r.next()) {
-                        if (!mbar_wait_bounded(smem_u32(&bars.full[r.stage]), r.phase, abort_flag, args.wait_limit_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
-                        const uint32_t b_addr = a_addr + kHalf;
-                        const uint64_t a0 = smem_desc_kmajor_sw128(a_addr);
-                        const uint64_t b0 = b_mn ? smem_desc_mnmajor_sw128(b_addr) : smem_desc_kmajor_sw128(b_addr);
-                        const uint32_t sb = b_mn ? 2048 >> 4 : 32 >> 4;
-#pragma unroll
-                        for (int kk = 0; kk < kBK / kUmmaK; ++kk)
-                            umma_bf16_pair(d, a0 + kk * (32 >> 4), b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
+                    mma_stage<false, true>(d_da, smem_u32(st.smem + r.stage * kStageBytes), kIdescDa, kb == 0, 4);
+                    umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
+                }
+                if (!ok || !mbar_wait_bounded(smem_u32(&bars.tempty[0]), (local & 1) ^ 1u, abort_flag,
+                                              args.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                for (int kb = 0; kb < k_blocks; ++kb, r.next()) {
+                    if (!mbar_wait_bounded(smem_u32(&bars.full[r.stage]), r.phase, abort_flag, args.wait_limit_ns)) {
+                        ok = false;
+                        break;
                     }
+                    tc_fence_after();
+                    mma_stage<false, false>(d_gu, smem_u32(st.smem + r.stage * kStageBytes), kIdescGu, kb == 0, 4);
+                    umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (ok)
                     umma_commit_pair(smem_u32(&bars.tfull[0]), 0x3);
@@ -777,9 +797,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
             while (const UnitDesc *tp = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
                 const int total = tp->total, rem = tp->rem;
                 const bool by_rows = args.job[tp->job].by_rows != 0, on_n = args.job[tp->job].rows_on_n != 0;
-                // rows kind: A K-major, B MN-major; weights kind: both MN-major. K steps as above
-                const uint32_t idesc = idesc_bf16_f32(256, on_n ? 128 : 256) | (by_rows ? 0u : kMajorA) | kMajorB;
-                const uint32_t sa = by_rows ? 32 >> 4 : 2048 >> 4, sb = 2048 >> 4;
                 const int buf = local & 1;
                 if (!mbar_wait_bounded(smem_u32(&bars.tempty[buf]), ((local >> 1) & 1) ^ 1u, abort_flag,
                                        args.wait_limit_ns)) {
@@ -795,21 +812,19 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                     }
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
-                    const uint32_t b_addr = a_addr + kHalf;
-                    const uint64_t a0 = by_rows ? smem_desc_kmajor_sw128(a_addr) : smem_desc_mnmajor_sw128(a_addr);
-                    const uint64_t b0 = smem_desc_mnmajor_sw128(b_addr);
                     const int steps = (rem && kb + 1 == total) ? (rem + kUmmaK - 1) / kUmmaK : kBK / kUmmaK;
-                    // two loops: with the second part's MMA as a branch inside one, the rows kind took a third longer
-                    if (on_n) {
-                        for (int kk = 0; kk < steps; ++kk) {
-                            umma_bf16_pair(d, a0 + kk * sa, b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-                            umma_bf16_pair(d, a0 + kk * sa, b0 + (kAtom >> 4) + kk * sb, idesc, 1u);
-                        }
+                    if (by_rows) {
+                        mma_stage<false, true>(d, a_addr, idesc_bf16_f32(256, 256) | kMajorB, kb == 0, kBK / kUmmaK);
+                    } else if (!on_n) {
+                        mma_stage<true, true>(d, a_addr, idesc_bf16_f32(256, 256) | kMajorA | kMajorB, kb == 0, steps);
                     } else {
-#pragma unroll
-                        for (int kk = 0; kk < kBK / kUmmaK; ++kk)
-                            if (kk < steps)
-                                umma_bf16_pair(d, a0 + kk * sa, b0 + kk * sb, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        // both parts of B
+                        constexpr uint32_t kIdesc = idesc_bf16_f32(256, 128) | kMajorA | kMajorB;
+                        const uint64_t a0 = smem_desc_mnmajor_sw128(a_addr), b0 = smem_desc_mnmajor_sw128(a_addr + kHalf);
+                        for (int kk = 0; kk < steps; ++kk) {
+                            umma_bf16_pair(d, a0 + kk * 128, b0 + kk * 128, kIdesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                            umma_bf16_pair(d, a0 + kk * 128, b0 + (kAtom >> 4) + kk * 128, kIdesc, 1u);
+                        }
                     }
                     umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }

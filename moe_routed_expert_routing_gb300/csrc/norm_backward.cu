@@ -9,7 +9,9 @@
 // it in registers; a thread meets the same columns in every row of its
 // persistent block, so dw grows in registers, one fp32 sum a column, and each
 // block ends with one row of partial sums. A second kernel adds those rows in
-// order (deterministic: no atomics).
+// order (deterministic: no atomics). T=8192, H=4096 bf16 with dh_add 46.7 us (5.7
+// TB/s, 0.86 of the copy rate; 3 us of it the second kernel); T=2047, H=7168 fp32
+// 34.4 us (0.89). Up to 16 rows one cluster does it all: T=7, H=7168 6.6 us.
 #include "moe_internal.h"
 #include "norm_ops.cuh"
 #include "ptx.cuh"
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
 // Rows over 8192 columns: one row a block of 1024 threads, 16 or 32 columns and
 // 64 registers each, so the weights come out of L1 and dw grows in shared
-// memory. (T=170, H=12288 measures @@.)
+// memory (T=170, H=12288 bf16 10.6 us in a graph).
 template <bool kF32, bool kWF32, int kV>
 __global__ void __launch_bounds__(1024, 1) norm_backward_wide_kernel(const __grid_constant__ NormGradArgs a, int tpr,
                                                                      float inv_H)
