@@ -159,12 +159,11 @@ struct PairBars {
     uint64_t ufull[2], uempty[2];   // batches of units
 };
 
-// Barriers, TMEM, the experts' offsets (clamped to the batch) and their row tiles.
+// Barriers and TMEM. The offsets are read and the units decoded by one warp
+// (load_offsets), while the others wait for the first units.
 template <class C>
-__device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::kStages> &bars, uint32_t &s_tmem, int &s_abort,
-                                                int *s_off, int *s_tp, const int32_t *offsets, int E, int cap)
+__device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::kStages> &bars, uint32_t &s_tmem, int &s_abort)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     PairState st;
     st.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     st.rank = cluster_ctarank();
@@ -185,24 +184,30 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::k
         s_abort = 0;
         fence_barrier_init();
     }
-    if (warp == 2) {
+    if ((threadIdx.x >> 5) == 2) {
         tmem_alloc_pair(smem_u32(&s_tmem), 512);
         tmem_relinquish_pair();
     }
-    pdl_wait();
-    for (int i = threadIdx.x; i <= E; i += C::kThreads) {
-        const int o = offsets[i];
-        s_off[i] = o < 0 ? 0 : (o > cap ? cap : o);
-    }
-    __syncthreads();
-    if (warp == 3)
-        build_tile_prefix(s_off, s_tp, E, kTileRows, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // both CTAs' barriers initialised before any remote arrive
     tc_fence_after();
     st.tmem = s_tmem;
+    pdl_wait();       // nothing above reads global memory
     return st;
+}
+
+// A warp: the experts' offsets, clamped to the batch, and their row tiles.
+__device__ __forceinline__ void load_offsets(const int32_t *offsets, int E, int cap, int *s_off, int *s_tp)
+{
+    const int lane = threadIdx.x & 31;
+    for (int i = lane; i <= E; i += 32) {
+        const int o = offsets[i];
+        s_off[i] = o < 0 ? 0 : (o > cap ? cap : o);
+    }
+    __syncwarp();
+    build_tile_prefix(s_off, s_tp, E, kTileRows, lane);
+    __syncwarp();
 }
 
 __device__ __forceinline__ void pair_end(const PairState &st, int &s_abort, int32_t *err)
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int NT = (args.I + 127) / 128;
-    const PairState st = pair_begin<ActConfig>(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap);
+    const PairState st = pair_begin<ActConfig>(smem_raw, bars, s_tmem, s_abort);
     volatile int *abort_flag = &s_abort;
     const int k_blocks = args.H / kBK;
     pdl_trigger();    // the products' CTAs need this kernel's shared memory: each starts as one here ends
@@ -539,6 +544,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
         }
         __syncwarp();
     } else if (warp == 2) {
+        load_offsets(args.offsets, args.E, args.cap, s_off, s_tp);
         publish_units(st, bars, s_units, s_tp[args.E] * NT, abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
             act_unit(u, d, s_off, s_tp, args.E, NT);
         });
@@ -702,7 +708,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
     __shared__ int s_tp[kMaxExperts + 1];
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort, s_off, s_tp, args.offsets, args.E, args.cap);
+    const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort);
     volatile int *abort_flag = &s_abort;
     const int rank = static_cast<int>(st.rank);
 
@@ -837,6 +843,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
         }
         __syncwarp();
     } else if (warp == 2) {
+        load_offsets(args.offsets, args.E, args.cap, s_off, s_tp);
         int units = 0;
         for (int j = 0; j < args.jobs; ++j)
             units += job_units(args.job[j], s_tp, args.E);
