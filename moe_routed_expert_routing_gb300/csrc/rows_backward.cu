@@ -140,39 +140,48 @@ __global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(const
 }
 
 constexpr int kDispatchBwdThreads = 128;
+constexpr long long kGridPerSm = 8;
 
-// One item = one token x 1024 columns; eight slots' rows are loaded together.
+// One item = one token x 1024 columns. The rows of eight slots (fp32: four) are
+// loaded together, and while they are on their way the next item's first slots
+// are read, so that no trip for the routing stands between one item's rows and
+// the next's (T=1021, k=6, H=7168 with inputs from HBM 22.9 -> 20.7 us).
 template <bool kF32>
-__global__ void __launch_bounds__(kDispatchBwdThreads) dispatch_backward_kernel(const void *__restrict__ dx_sorted,
-                                                                                const int32_t *__restrict__ inv,
-                                                                                const uint4 *add,
-                                                                                const int32_t *d_num_tokens, int T_max,
-                                                                                int k, int cap, int vec, uint4 *dx)
+__global__ void __launch_bounds__(kDispatchBwdThreads, 8) dispatch_backward_kernel(const void *__restrict__ dx_sorted,
+                                                                                   const int32_t *__restrict__ inv,
+                                                                                   const uint4 *add,
+                                                                                   const int32_t *d_num_tokens,
+                                                                                   int T_max, int k, int cap, int vec,
+                                                                                   uint4 *dx)
 {
     constexpr int kRows = kF32 ? 4 : 8;
     const int groups = (vec + kDispatchBwdThreads - 1) / kDispatchBwdThreads;
     const long long items = static_cast<long long>(token_count(d_num_tokens, T_max)) * groups;
+    int next[kRows];
+    auto slots = [&](long long item, int j0) {
+        const int32_t *inv_t = inv + item / groups * k;
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+            next[q] = item < items && j0 + q < k ? checked_row(__ldg(inv_t + j0 + q), cap) : -1;
+    };
+    slots(blockIdx.x, 0);
     for (long long item = blockIdx.x; item < items; item += gridDim.x) {
         const int t = static_cast<int>(item / groups);
-        const int c = static_cast<int>(item % groups) * kDispatchBwdThreads + threadIdx.x;
-        if (c >= vec)
-            continue;
+        const int c = static_cast<int>(item - static_cast<long long>(t) * groups) * kDispatchBwdThreads + threadIdx.x;
+        const bool mine = c < vec;
         const size_t at = static_cast<size_t>(t) * vec + c;
         uint4 more = make_uint4(0u, 0u, 0u, 0u);
-        if (add)
-            more = add[at];
+        if (add && mine)
+            more = ld_stream(add + at);
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        const int32_t *inv_t = inv + static_cast<size_t>(t) * k;
         for (int j0 = 0; j0 < k; j0 += kRows) {
-            int row[kRows];
             uint4 a[kRows], b[kF32 ? kRows : 1];
+            unsigned on = 0;
 #pragma unroll
             for (int q = 0; q < kRows; ++q)
-                row[q] = j0 + q < k ? checked_row(__ldg(inv_t + j0 + q), cap) : -1;
-#pragma unroll
-            for (int q = 0; q < kRows; ++q)
-                if (row[q] >= 0) {
-                    const size_t i = static_cast<size_t>(row[q]) * vec + c;
+                if (mine && next[q] >= 0) {
+                    on |= 1u << q;
+                    const size_t i = static_cast<size_t>(next[q]) * vec + c;
                     if constexpr (kF32) {
                         a[q] = ld_stream(static_cast<const float *>(dx_sorted) + i * 8);
                         b[q] = ld_stream(static_cast<const float *>(dx_sorted) + i * 8 + 4);
@@ -180,9 +189,13 @@ __global__ void __launch_bounds__(kDispatchBwdThreads) dispatch_backward_kernel(
                         a[q] = ld_stream(static_cast<const uint4 *>(dx_sorted) + i);
                     }
                 }
+            if (j0 + kRows < k)
+                slots(item, j0 + kRows);
+            else
+                slots(item + gridDim.x, 0);
 #pragma unroll
             for (int q = 0; q < kRows; ++q) {
-                if (row[q] < 0)
+                if (!(on >> q & 1u))
                     continue;
                 float f[8];
                 if constexpr (kF32) {
@@ -198,6 +211,8 @@ __global__ void __launch_bounds__(kDispatchBwdThreads) dispatch_backward_kernel(
                     acc[i] += f[i];
             }
         }
+        if (!mine)
+            continue;
         if (add) {
             float f[8];
             widen8(more, f);
@@ -228,7 +243,7 @@ cudaError_t launch_dispatch_backward(const void *dx_sorted, bool f32, const int3
 {
     const int vec = H / 8;
     const long long items = static_cast<long long>(T_max) * ((vec + kDispatchBwdThreads - 1) / kDispatchBwdThreads);
-    const long long most = num_sms * 16LL;
+    const long long most = num_sms * kGridPerSm;
     const dim3 grid(static_cast<unsigned>(items < most ? items : most));
     auto kern = f32 ? dispatch_backward_kernel<true> : dispatch_backward_kernel<false>;
     return launch_k(kern, grid, dim3(kDispatchBwdThreads), 0, stream, false, dx_sorted, inv,
