@@ -49,18 +49,27 @@ constexpr int kTileRows = 256;               // rows of a CTA pair's tile
 constexpr int kRowBox = 32;                  // rows of a box of a partial tile
 constexpr int kHalf = 128 * 128;             // bytes of one operand's half tile: 128 x 64 bf16
 constexpr int kAtom = 64 * 128;              // bytes of an MN-major block: 64 K rows x 64 columns
-constexpr int kStageBytes = 2 * kHalf;
 constexpr int kBox = 32 * 128;               // bytes of an output box: 32 rows x 128 bytes
 
 // A kernel's pipeline stages and epilogue warps: four, one for each quarter of
 // the TMEM lanes, or eight, each with half the columns.
-template <int kStages_, int kWarps_, bool kBoxes>
+template <int kStages_, int kWarps_, bool kBoxes, int kRows_ = kTileRows>
 struct Config {
     static constexpr int kStages = kStages_, kWarps = kWarps_;
+    static constexpr int kRows = kRows_;                                    // of a row tile
+    static constexpr int kABytes = kRows == kTileRows ? kHalf : kRows * 128;    // of A's half in a stage
+    static constexpr int kStageBytes = kABytes + kHalf;
     static constexpr int kThreads = 128 + 32 * kWarps;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + (kBoxes ? kWarps * kBox : 0);
 };
 using ActConfig = Config<6, 8, false>;
+// Few rows an expert: tiles of 32 rows, all in the even CTA, whose A takes 4 KB of
+// a stage, so that ten stages of weights are on their way. The MMAs still read 128 rows of
+// A: what lies behind those 32 (the stage's B) gives rows that are not stored.
+// E=5, 25 tokens of 2 experts, H=3904, I=960 87.0 us (91.6 with ActConfig); E=32, H=2048,
+// I=1024 222.1 us (227.1) at 16 rows an expert, 222.8 (229.2) at 24, 229.4 (230.1) at 32.
+using ThinConfig = Config<10, 8, false, 32>;
+constexpr int kThinRows = 24;                // up to so many rows an expert on average
 using DeepConfig = Config<6, 4, true>;       // products: more copies in flight
 // Small problems, where each unit's way from its first copy to its last store
 // counts: E=16, 64 tokens of 4 experts, H=1024, I=512 (5.9 units a pair) 38.5 us, with
@@ -198,7 +207,7 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::k
 }
 
 // A warp: the experts' offsets, clamped to the batch, and their row tiles.
-__device__ __forceinline__ void load_offsets(const int32_t *offsets, int E, int cap, int *s_off, int *s_tp)
+__device__ __forceinline__ void load_offsets(const int32_t *offsets, int E, int cap, int tile_rows, int *s_off, int *s_tp)
 {
     const int lane = threadIdx.x & 31;
     for (int i = lane; i <= E; i += 32) {
@@ -206,7 +215,7 @@ __device__ __forceinline__ void load_offsets(const int32_t *offsets, int E, int 
         s_off[i] = o < 0 ? 0 : (o > cap ? cap : o);
     }
     __syncwarp();
-    build_tile_prefix(s_off, s_tp, E, kTileRows, lane);
+    build_tile_prefix(s_off, s_tp, E, tile_rows, lane);
     __syncwarp();
 }
 
@@ -234,11 +243,11 @@ __device__ __forceinline__ void pair_end(const PairState &st, int &s_abort, int3
 // and a branch between the steps (the router's second part beside the plain
 // step) cost the products a third of their rate: dx at E=16, T=8192, H=4096, I=1536
 // 1.29 ms and 0.93.
-template <bool kAMn, bool kBMn>
+template <bool kAMn, bool kBMn, int kABytes = kHalf>
 __device__ __forceinline__ void mma_stage(uint32_t d, uint32_t a_addr, uint32_t idesc, bool first, int steps)
 {
     constexpr uint32_t kA = kAMn ? 2048 >> 4 : 32 >> 4, kB = kBMn ? 2048 >> 4 : 32 >> 4;
-    const uint32_t b_addr = a_addr + kHalf;
+    const uint32_t b_addr = a_addr + kABytes;
     const uint64_t a0 = kAMn ? smem_desc_mnmajor_sw128(a_addr) : smem_desc_kmajor_sw128(a_addr);
     const uint64_t b0 = kBMn ? smem_desc_mnmajor_sw128(b_addr) : smem_desc_kmajor_sw128(b_addr);
     if (steps == kBK / kUmmaK) {
@@ -412,7 +421,7 @@ struct ActArgs {
 // tiles that load only their rows it does not pay: 256 rows an expert, E=128, H=4096,
 // I=1536 3.48 ms with it and 3.35 without, 120 rows 702 us and 690; only very few long
 // ones gain, 10 rows of each of 5 experts, H=3904, I=960 92 us and 100.)
-__device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, const int *s_tp, int E, int NT)
+__device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, const int *s_tp, int E, int NT, int tile_rows)
 {
     const int e = find_expert(s_tp, E, u, NT);
     const int local = u - s_tp[e] * NT;
@@ -420,8 +429,8 @@ __device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, c
     const int nt = local / tiles;
     d.job = 0;
     d.e = e;
-    d.m0 = s_off[e] + (local - nt * tiles) * kTileRows;
-    d.rows = min(s_off[e + 1] - d.m0, kTileRows);
+    d.m0 = s_off[e] + (local - nt * tiles) * tile_rows;
+    d.rows = min(s_off[e + 1] - d.m0, tile_rows);
     d.n0 = nt * 128;
 }
 
@@ -440,10 +449,11 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float &a,
 // in 256..383 and 384..511. A unit's da comes first, so that it can be
 // multiplied while the unit before is still being read out: a third of the
 // unit's MMAs, which hides that unit's epilogue.
-__global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const __grid_constant__ ActArgs args)
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_constant__ ActArgs args)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) PairBars<ActConfig::kStages> bars;
+    __shared__ __align__(8) PairBars<C::kStages> bars;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ int s_off[kMaxExperts + 1];
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int NT = (args.I + 127) / 128;
-    const PairState st = pair_begin<ActConfig>(smem_raw, bars, s_tmem, s_abort);
+    const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort);
     volatile int *abort_flag = &s_abort;
     const int k_blocks = args.H / kBK;
     pdl_trigger();    // the products' CTAs need this kernel's shared memory: each starts as one here ends
@@ -469,7 +479,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
         if (lane == 0) {
             const uint64_t pol_w = l2_policy_evict_normal();
             const uint64_t pol_a = l2_policy_evict_last();
-            Ring<ActConfig::kStages> r;
+            Ring<C::kStages> r;
             UnitReader units(s_units, bars.ufull, bars.uempty);
             bool ok = true;
             while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
@@ -485,8 +495,8 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
                         break;
                     }
                     const uint32_t full = map_to_cta(smem_u32(&bars.full[r.stage]), 0);
-                    const uint32_t a_dst = smem_u32(st.smem + r.stage * kStageBytes);
-                    const uint32_t b_dst = a_dst + kHalf;
+                    const uint32_t a_dst = smem_u32(st.smem + r.stage * C::kStageBytes);
+                    const uint32_t b_dst = a_dst + C::kABytes;
                     if (kb < k_blocks) {
                         const int kc = kb * kBK;
                         mbar_arrive_expect_tx_cluster(full, boxed * 128 + kAtom);
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0 && st.rank == 0) {
-            Ring<ActConfig::kStages> r;
+            Ring<C::kStages> r;
             UnitReader units(s_units, bars.ufull, bars.uempty);
             bool ok = true;
             int local = 0;
@@ -518,7 +528,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
                         break;
                     }
                     tc_fence_after();
-                    mma_stage<false, true>(d_da, smem_u32(st.smem + r.stage * kStageBytes), kIdescDa, kb == 0, 4);
+                    mma_stage<false, true, C::kABytes>(d_da, smem_u32(st.smem + r.stage * C::kStageBytes), kIdescDa, kb == 0, 4);
                     umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (!ok || !mbar_wait_bounded(smem_u32(&bars.tempty[0]), (local & 1) ^ 1u, abort_flag,
@@ -532,7 +542,7 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
                         break;
                     }
                     tc_fence_after();
-                    mma_stage<false, false>(d_gu, smem_u32(st.smem + r.stage * kStageBytes), kIdescGu, kb == 0, 4);
+                    mma_stage<false, false, C::kABytes>(d_gu, smem_u32(st.smem + r.stage * C::kStageBytes), kIdescGu, kb == 0, 4);
                     umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (ok)
@@ -544,9 +554,9 @@ __global__ void __launch_bounds__(ActConfig::kThreads, 1) act_grad_kernel(const 
         }
         __syncwarp();
     } else if (warp == 2) {
-        load_offsets(args.offsets, args.E, args.cap, s_off, s_tp);
+        load_offsets(args.offsets, args.E, args.cap, C::kRows, s_off, s_tp);
         publish_units(st, bars, s_units, s_tp[args.E] * NT, abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
-            act_unit(u, d, s_off, s_tp, args.E, NT);
+            act_unit(u, d, s_off, s_tp, args.E, NT, C::kRows);
         });
     } else if (warp >= 4) {
         const int q = warp & 3, half = (warp - 4) >> 2;
@@ -738,7 +748,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                         break;
                     }
                     const uint32_t full = map_to_cta(smem_u32(&bars.full[r.stage]), 0);
-                    const uint32_t a_dst = smem_u32(st.smem + r.stage * kStageBytes);
+                    const uint32_t a_dst = smem_u32(st.smem + r.stage * C::kStageBytes);
                     const uint32_t b_dst = a_dst + kHalf;
                     if (by_rows) {
                         const int b_row = b_row0 + kp * kBK;
@@ -781,7 +791,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                                 }
                             }
                         } else {
-                            mbar_arrive_expect_tx_cluster(full, kStageBytes);
+                            mbar_arrive_expect_tx_cluster(full, C::kStageBytes);
                             tma_load_2d_pair(a_dst, ma, full, a_col, row, pol);
                             tma_load_2d_pair(a_dst + kAtom, ma, full, a_col + 64, row, pol);
                             tma_load_2d_pair(b_dst, mb, full, b_col, row, pol);
@@ -817,7 +827,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
+                    const uint32_t a_addr = smem_u32(st.smem + r.stage * C::kStageBytes);
                     const int steps = (rem && kb + 1 == total) ? (rem + kUmmaK - 1) / kUmmaK : kBK / kUmmaK;
                     if (by_rows) {
                         mma_stage<false, true>(d, a_addr, idesc_bf16_f32(256, 256) | kMajorB, kb == 0, kBK / kUmmaK);
@@ -843,7 +853,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
         }
         __syncwarp();
     } else if (warp == 2) {
-        load_offsets(args.offsets, args.E, args.cap, s_off, s_tp);
+        load_offsets(args.offsets, args.E, args.cap, kTileRows, s_off, s_tp);
         int units = 0;
         for (int j = 0; j < args.jobs; ++j)
             units += job_units(args.job[j], s_tp, args.E);
@@ -853,7 +863,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
     } else if (warp >= 4) {
         const int q = warp & 3, half = (warp - 4) >> 2;
         constexpr int kHalves = C::kWarps / 4;
-        uint8_t *const box = st.smem + C::kStages * kStageBytes + (warp - 4) * kBox;
+        uint8_t *const box = st.smem + C::kStages * C::kStageBytes + (warp - 4) * kBox;
         UnitReader units(s_units, bars.ufull, bars.uempty);
         int local = 0;
         for (; const UnitDesc *tp = units.next_warp(lane, abort_flag, args.wait_limit_ns); ++local) {
@@ -1023,7 +1033,10 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
     a.cap = cap;
     a.H = H;
     a.I = I;
-    return launch_pair<ActConfig>(act_grad_kernel, a, (tiles_of(cap) + E) * ((I + 127) / 128), num_sms, stream);
+    const long long nt = (I + 127) / 128;
+    if (cap <= static_cast<long long>(kThinRows) * E)
+        return launch_pair<ThinConfig>(act_grad_kernel<ThinConfig>, a, (cap / ThinConfig::kRows + E) * nt, num_sms, stream);
+    return launch_pair<ActConfig>(act_grad_kernel<ActConfig>, a, (tiles_of(cap) + E) * nt, num_sms, stream);
 }
 
 }  // namespace moe
