@@ -345,7 +345,10 @@ __global__ void __launch_bounds__(kFewThreads) route_grad_few_kernel(const __gri
         int found = 0;
         for (int s0 = 0; s0 < slots; s0 += kFewThreads) {
             const int s = s0 + static_cast<int>(threadIdx.x);
-            const bool hit = s < slots && a.ids[s] == e;
+            const int id = s < slots ? a.ids[s] : -1;
+            if (e == 0 && (id < -1 || id >= E))
+                atomicOr(a.err, MOE_DEVERR_BAD_EXPERT_ID);     // slot_term does not report it
+            const bool hit = id == e;
             const unsigned hits = __ballot_sync(0xffffffffu, hit);
             if (lane == 0)
                 s_count[warp] = __popc(hits);

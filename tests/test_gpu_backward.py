@@ -511,6 +511,41 @@ def test_route_backward_masks(B):
             check(dl2, want, 300 * U * mag, "dl")
 
 
+@pytest.mark.parametrize("T", [5, 400])
+def test_route_backward_reports_invalid_ids_for_every_output(B, T):
+    E, k, H = 16, 2, 64
+    x, w, logits, ids, dwt = route_inputs(B, 6, T, E, k, H, "softmax", True)
+    p = B.RouterProblem.make(T, E, k, H)
+    for wanted in (("dx",), ("dw",), ("dl",)):
+        for bad in (E, -2, 1 << 30):
+            wrong = ids.clone()
+            wrong[T - 1, 1] = bad
+            assert run_route(B, p, x, w, logits, wrong, dwt, wanted=wanted)[3] == B.MOE_DEVERR_BAD_EXPERT_ID
+        assert run_route(B, p, x, w, logits, ids, dwt, wanted=wanted)[3] == 0
+
+
+@pytest.mark.parametrize("T,E,k", [(128, 64, 8), (200, 8, 1), (250, 16, 1), (256, 300, 4), (1, 1, 1)])
+def test_route_backward_hot_experts(B, T, E, k):
+    """Few slots, most of them of one expert; some tokens without any."""
+    H = 1088
+    x, w, logits, ids, dwt = route_inputs(B, 7, T, E, k, H, "sigmoid", True)
+    hot = ids.clone()
+    hot[:, 0] = E - 1
+    for j in range(1, k):
+        hot[:, j] = torch.where(hot[:, j] == E - 1, E - 2, hot[:, j])
+    hot[T // 2] = -1
+    p = B.RouterProblem.make(T, E, k, H, score=1)
+    dx, dw, dl, err = run_route(B, p, x, w, logits, hot, dwt, dtype=F32)
+    assert err == 0
+    want, mag = back.route(ref.f64(logits), ref.f64(hot).astype(int), ref.f64(dwt), "sigmoid", True)
+    check(dl, want, 64 * U * mag, "dl")
+    d, xx, ww = ref.f64(dl), ref.f64(x), ref.f64(w)
+    Ep = (E + 63) // 64 * 64
+    check(dx, d @ ww, (2.0 ** -16 + back.mma_rel(2 * Ep)) * (np.abs(d) @ np.abs(ww)), "dx")
+    check(dw, d.T @ xx, (2.0 ** -16 + back.mma_rel(2 * T) + 152 * U) * (np.abs(d).T @ np.abs(xx)), "dw")
+    assert (dx[T // 2] == 0).all()
+
+
 def test_route_backward_token_count_and_single_outputs(B):
     T, E, k, H = 300, 40, 4, 192
     x, w, logits, ids, dwt = route_inputs(B, 4, T, E, k, H, "softmax", True)
