@@ -53,22 +53,33 @@ constexpr int kBox = 32 * 128;               // bytes of an output box: 32 rows 
 
 // A kernel's pipeline stages and epilogue warps: four, one for each quarter of
 // the TMEM lanes, or eight, each with half the columns.
-template <int kStages_, int kWarps_, bool kBoxes, int kRows_ = kTileRows>
+template <int kStages_, int kWarps_, bool kBoxes, int kRows_ = kTileRows, bool kSplit_ = false>
 struct Config {
     static constexpr int kStages = kStages_, kWarps = kWarps_;
-    static constexpr int kRows = kRows_;                                    // of a row tile
-    static constexpr int kABytes = kRows == kTileRows ? kHalf : kRows * 128;    // of A's half in a stage
+    static constexpr bool kSplit = kSplit_;      // tiles of up to 128 rows in halves
+    static constexpr int kRows = kRows_;         // of a row tile
+    // A's half of a stage: one K block, or two of half the rows
+    static constexpr int kABytes = kRows == kTileRows ? kHalf : 2 * kRows * 128;
     static constexpr int kStageBytes = kABytes + kHalf;
     static constexpr int kThreads = 128 + 32 * kWarps;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + (kBoxes ? kWarps * kBox : 0);
 };
 using ActConfig = Config<6, 8, false>;
-// Few rows an expert: tiles of 32 rows, all in the even CTA, whose A takes 4 KB of
-// a stage, so that ten stages of weights are on their way. The MMAs still read 128 rows of
+// At most 128 rows an expert on average: a tile of up to 128 rows is split between the
+// CTAs, in one box of 32 or 64 rows each. Its rows then take at most half of a stage's A,
+// and two K blocks of da go into one stage: each brings 8 KB of W2 only, too little on
+// its way at six stages. act_grad_kernel, E=50, 1000 tokens of 6 experts, H=2880, I=1472
+// 261 -> 250 us; E=32, 32 rows an expert, H=2048, I=1024 107.5 -> 98.5. With whole tiles beside
+// them such halves cost (E=128, 256 rows an expert, H=4096, I=1536, both kernels 3.40 and
+// 3.51 ms).
+using SplitConfig = Config<6, 8, false, kTileRows, true>;
+constexpr int kSplitRows = 128;
+// Few rows an expert: tiles of 32 rows, all in the even CTA, whose A takes 8 KB of
+// a stage, so that eight stages of weights are on their way. The MMAs still read 128 rows of
 // A: what lies behind those 32 (the stage's B) gives rows that are not stored.
-// E=5, 25 tokens of 2 experts, H=3904, I=960 87.0 us (91.6 with ActConfig); E=32, H=2048,
-// I=1024 222.1 us (227.1) at 16 rows an expert, 222.8 (229.2) at 24, 229.4 (230.1) at 32.
-using ThinConfig = Config<10, 8, false, 32>;
+// Both kernels, E=5, 25 tokens of 2 experts, H=3904, I=960 85.3 us (88.2 with SplitConfig);
+// E=32, H=2048, I=1024 219.0 us (220.0) at 16 rows an expert, 219.2 (220.5) at 24.
+using ThinConfig = Config<8, 8, false, 32, true>;
 constexpr int kThinRows = 24;                // up to so many rows an expert on average
 using DeepConfig = Config<6, 4, true>;       // products: more copies in flight
 // Small problems, where each unit's way from its first copy to its last store
@@ -134,6 +145,13 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Rows of a tile in the first CTA of its pair.
+template <bool kSplit>
+__device__ __forceinline__ int first_rows(int rows)
+{
+    return kSplit && rows <= 128 ? (rows <= 64 ? 32 : 64) : 128;
+}
 
 // The rows of a tile that this CTA's half of A needs, `n` of 128, as whole 32-row
 // boxes, or one box where all are there. MMA rows past them keep whatever the
@@ -407,6 +425,7 @@ struct ActArgs {
     CUtensorMap x32, dy32;   // the same in boxes of 64 x 32 rows
     CUtensorMap w13;         // [E * 2I, H], boxes of 64 x 128 rows
     CUtensorMap w2;          // [E * H, I], boxes of 64 x 64 rows
+    CUtensorMap x64, dy64, w2_two;   // split tiles: boxes of 64 x 64 rows, of 64 x 128 rows
     const int32_t *offsets;
     int32_t *err;
     __nv_bfloat16 *act;      // [cap + 1, I]: the last row is zeros
@@ -484,11 +503,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
             bool ok = true;
             while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
                 const int n0 = t->n0;
-                const int a_row = t->m0 + 128 * rank;
-                const int boxed = boxed_rows(t->rows - 128 * rank);
+                const int split = first_rows<C::kSplit>(t->rows);
+                const int a_row = t->m0 + split * rank;
+                const int boxed = split == 64 ? 64 : boxed_rows(rank ? t->rows - split : min(t->rows, split));
+                const int per = split < 128 ? 2 : 1;               // K blocks of da in a stage
                 const int w2_row = t->e * args.H;
                 const int w13_row = t->e * 2 * args.I + n0 + (rank ? args.I : 0);
-                for (int kb = 0; kb < 2 * k_blocks; ++kb, r.next()) {
+                for (int kb = 0; kb < 2 * k_blocks; kb += kb < k_blocks ? min(per, k_blocks - kb) : 1, r.next()) {
                     if (!mbar_wait_bounded(smem_u32(&bars.empty[r.stage]), r.phase ^ 1u, abort_flag,
                                            args.wait_limit_ns)) {
                         ok = false;
@@ -499,13 +520,25 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
                     const uint32_t b_dst = a_dst + C::kABytes;
                     if (kb < k_blocks) {
                         const int kc = kb * kBK;
-                        mbar_arrive_expect_tx_cluster(full, boxed * 128 + kAtom);
-                        load_rows(a_dst, &args.dy, &args.dy32, full, kc, a_row, boxed, pol_a);
-                        tma_load_2d_pair(b_dst, &args.w2, full, n0 + 64 * rank, w2_row + kc, pol_w);
+                        if (C::kSplit && split < 128) {
+                            const int n = min(per, k_blocks - kb);
+                            const CUtensorMap *const part = split == 64 ? &args.dy64 : &args.dy32;
+                            mbar_arrive_expect_tx_cluster(full, n * (boxed * 128 + kAtom));
+                            tma_load_2d_pair(b_dst, n == 2 ? &args.w2_two : &args.w2, full, n0 + 64 * rank, w2_row + kc, pol_w);
+                            for (int i = 0; boxed && i < n; ++i)
+                                tma_load_2d_pair(a_dst + i * (C::kABytes / 2), part, full, kc + i * kBK, a_row, pol_a);
+                        } else {
+                            mbar_arrive_expect_tx_cluster(full, boxed * 128 + kAtom);
+                            load_rows(a_dst, &args.dy, &args.dy32, full, kc, a_row, boxed, pol_a);
+                            tma_load_2d_pair(b_dst, &args.w2, full, n0 + 64 * rank, w2_row + kc, pol_w);
+                        }
                     } else {
                         const int kc = (kb - k_blocks) * kBK;
                         mbar_arrive_expect_tx_cluster(full, boxed * 128 + kHalf);
-                        load_rows(a_dst, &args.x, &args.x32, full, kc, a_row, boxed, pol_a);
+                        if (C::kSplit && split == 64)
+                            tma_load_2d_pair(a_dst, &args.x64, full, kc, a_row, pol_a);
+                        else
+                            load_rows(a_dst, &args.x, &args.x32, full, kc, a_row, boxed, pol_a);
                         tma_load_2d_pair(b_dst, &args.w13, full, kc, w13_row, pol_w);
                     }
                 }
@@ -518,17 +551,21 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
             UnitReader units(s_units, bars.ufull, bars.uempty);
             bool ok = true;
             int local = 0;
-            while (ok && units.next(abort_flag, args.wait_limit_ns)) {
+            while (const UnitDesc *t = ok ? units.next(abort_flag, args.wait_limit_ns) : nullptr) {
+                const int per = first_rows<C::kSplit>(t->rows) < 128 ? 2 : 1;
                 // da, then gate and up, once those of the unit before have been read (and with them the da before that)
                 constexpr uint32_t kIdescDa = idesc_bf16_f32(256, 128) | kMajorB, kIdescGu = idesc_bf16_f32(256, 256);
                 const uint32_t d_da = st.tmem + 128 * (local & 1), d_gu = st.tmem + 256;
-                for (int kb = 0; kb < k_blocks; ++kb, r.next()) {
+                for (int kb = 0; kb < k_blocks; kb += per, r.next()) {
                     if (!mbar_wait_bounded(smem_u32(&bars.full[r.stage]), r.phase, abort_flag, args.wait_limit_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    mma_stage<false, true, C::kABytes>(d_da, smem_u32(st.smem + r.stage * C::kStageBytes), kIdescDa, kb == 0, 4);
+                    const uint32_t a_addr = smem_u32(st.smem + r.stage * C::kStageBytes);
+                    mma_stage<false, true, C::kABytes>(d_da, a_addr, kIdescDa, kb == 0, 4);
+                    if (per == 2 && kb + 1 < k_blocks)
+                        mma_stage<false, true, C::kABytes / 2 + kAtom>(d_da, a_addr + C::kABytes / 2, kIdescDa, false, 4);
                     umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (!ok || !mbar_wait_bounded(smem_u32(&bars.tempty[0]), (local & 1) ^ 1u, abort_flag,
@@ -572,8 +609,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
             tc_fence_after();
             const uint32_t lanes = st.tmem + (static_cast<uint32_t>(q * 32) << 16);
             const uint32_t t_da = lanes + 128 * (local & 1), t_gu = lanes + 256;
-            const int r = 128 * rank + q * 32 + lane;
-            const bool valid = r < t.rows;
+            const int split = first_rows<C::kSplit>(t.rows);
+            const int r = split * rank + q * 32 + lane;
+            const bool valid = r < (rank ? t.rows : min(t.rows, split));
             const int cols = min(args.I - t.n0, 128);     // a multiple of 64
             __nv_bfloat16 *const act = args.act + static_cast<size_t>(t.m0 + r) * args.I + t.n0;
             __nv_bfloat16 *const dgu = args.dgu + static_cast<size_t>(t.m0 + r) * 2 * args.I + t.n0;
@@ -1034,8 +1072,14 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
     a.H = H;
     a.I = I;
     const long long nt = (I + 127) / 128;
-    if (cap <= static_cast<long long>(kThinRows) * E)
-        return launch_pair<ThinConfig>(act_grad_kernel<ThinConfig>, a, (cap / ThinConfig::kRows + E) * nt, num_sms, stream);
+    if (cap <= static_cast<long long>(kSplitRows) * E) {
+        if (!make_tile_map(&a.x64, x, rows, h, 64) || !make_tile_map(&a.dy64, dy, rows, h, 64) ||
+            !make_tile_map(&a.w2_two, W2, e * h, i, 128))
+            return cudaErrorInvalidValue;
+        if (cap <= static_cast<long long>(kThinRows) * E)
+            return launch_pair<ThinConfig>(act_grad_kernel<ThinConfig>, a, (cap / ThinConfig::kRows + E) * nt, num_sms, stream);
+        return launch_pair<SplitConfig>(act_grad_kernel<SplitConfig>, a, (tiles_of(cap) + E) * nt, num_sms, stream);
+    }
     return launch_pair<ActConfig>(act_grad_kernel<ActConfig>, a, (tiles_of(cap) + E) * nt, num_sms, stream);
 }
 

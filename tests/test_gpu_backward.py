@@ -216,6 +216,24 @@ def test_expert_backward(B, counts, H, I, spare, kind):
     assert (out["dx_sorted"][n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("H,I", [(64, 64), (192, 128), (384, 320)])
+def test_expert_backward_halved_tiles(B, H, I):
+    """Up to 128 rows an expert on average: tiles split between the CTAs of a pair at 32 or 64 rows, whole
+    ones beside them, even and odd numbers of K blocks."""
+    counts = [1, 31, 32, 33, 63, 64, 65, 96, 127, 128, 129, 255, 256, 257, 0, 320]
+    assert 24 * len(counts) < sum(counts) + 5 <= 128 * len(counts)
+    x, dy, W13, W2, bounds = expert_inputs(H + I, counts, H, I, 5)
+    p = expert_problem(B, counts, H, I, 5, dx_dtype=F32, dw_dtype=F32)
+    out = run_experts(B, p, x, dy, W13, W2, bounds, dx_sorted=empty(x.shape, F32), dW13=empty(W13.shape, F32),
+                      dW2=empty(W2.shape, F32))
+    n = int(bounds[-1])
+    want, tol = back.experts(ref.f64(x[:n]), ref.f64(dy[:n]), ref.f64(W13), ref.f64(W2), bounds)
+    check(out["dx_sorted"][:n], want["dx"], tol["dx"], "dx")
+    check(out["dW13"], want["dW13"], tol["dW13"], "dW13")
+    check(out["dW2"], want["dW2"], tol["dW2"], "dW2")
+    assert (out["dx_sorted"][n:] == 7.0).all()
+
+
 def test_expert_backward_one_output_at_a_time(B):
     counts, H, I = [70, 0, 130], 256, 192
     x, dy, W13, W2, bounds = expert_inputs(5, counts, H, I)
