@@ -84,10 +84,14 @@ constexpr int kThinRows = 24;                // up to so many rows an expert on 
 using DeepConfig = Config<6, 4, true>;       // products: more copies in flight
 // Small problems, where each unit's way from its first copy to its last store
 // counts: E=16, 64 tokens of 4 experts, H=1024, I=512 (5.9 units a pair) 38.5 us, with
-// DeepConfig 41.7; E=50, 1000 tokens (150 units) 691.6 and 690.9; T=8192, E=128, H=4096,
-// I=1536 5.71 and 5.60 ms.
+// DeepConfig 41.7. And few rows an expert, where the weight gradients' tiles have one or two
+// K blocks and wait for their epilogue: E=32, H=2048, I=1024 at 16, 32 and 64 rows an expert
+// 201, 207 and 212 us, with DeepConfig 219, 221 and 225; E=50, 120 rows, H=2880, I=1472 679
+// and 684; E=128, 128 rows, H=4096, I=1536 2521 and 2513, 180 rows 2820 and 2715, 512 rows
+// 5.71 and 5.60 ms.
 using WideConfig = Config<5, 8, true>;
 constexpr int kWideUnits = 6;                // up to so many units a CTA pair
+constexpr int kWideRows = 128;               // or rows an expert on average
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;   // instruction descriptor: operand is MN-major
 
 // Shared-memory descriptor of an MN-major bf16 tile: blocks of 64 K rows x 64
@@ -1047,7 +1051,7 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
     a.cap = cap;
     a.err = err;
     a.wait_limit_ns = kWaitLimitNs;
-    if (live <= kWideUnits * (num_sms / 2))
+    if (live <= kWideUnits * (num_sms / 2) || cap <= static_cast<long long>(kWideRows) * E)
         return launch_pair<WideConfig>(products_kernel<WideConfig>, a, units, num_sms, stream);
     return launch_pair<DeepConfig>(products_kernel<DeepConfig>, a, units, num_sms, stream);
 }
