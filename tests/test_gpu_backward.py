@@ -234,6 +234,21 @@ def test_expert_backward_halved_tiles(B, H, I):
     assert (out["dx_sorted"][n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_expert_backward_many_units(B, kind):
+    """More than 128 rows an expert and more than six tiles of the products for each CTA pair."""
+    counts, H, I = [200, 0, 513], 4096, 704
+    tiles = 3 * (6 * 16 + 16 * 3) + 3 * 16
+    assert tiles > 6 * 76 and sum(counts) > 128 * len(counts)
+    x, dy, W13, W2, bounds = expert_inputs(12, counts, H, I)
+    p = expert_problem(B, counts, H, I, dx_dtype=DT[kind], dw_dtype=DT[kind])
+    out = run_experts(B, p, x, dy, W13, W2, bounds, dx_sorted=empty(x.shape, DT[kind]),
+                      dW13=empty(W13.shape, DT[kind], float("nan")), dW2=empty(W2.shape, DT[kind], float("nan")))
+    want, tol = back.experts(ref.f64(x), ref.f64(dy), ref.f64(W13), ref.f64(W2), bounds)
+    for n, key in (("dx_sorted", "dx"), ("dW13", "dW13"), ("dW2", "dW2")):
+        check(out[n], want[key], tol[key], n)
+
+
 def test_expert_backward_one_output_at_a_time(B):
     counts, H, I = [70, 0, 130], 256, 192
     x, dy, W13, W2, bounds = expert_inputs(5, counts, H, I)
