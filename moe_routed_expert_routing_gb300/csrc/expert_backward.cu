@@ -88,10 +88,12 @@ using DeepConfig = Config<6, 4, true>;       // products: more copies in flight
 // K blocks and wait for their epilogue: E=32, H=2048, I=1024 at 16, 32 and 64 rows an expert
 // 201, 207 and 212 us, with DeepConfig 219, 221 and 225; E=50, 120 rows, H=2880, I=1472 679
 // and 684; E=128, 128 rows, H=4096, I=1536 2521 and 2513, 180 rows 2820 and 2715, 512 rows
-// 5.71 and 5.60 ms.
+// 5.71 and 5.60 ms. The router's gradient likewise at few K blocks (its dx's, twice E / 64):
+// T=8192, H=4096 with E=64, 128 and 256 42.5, 48.0 and 66.4 us, with DeepConfig 44.8, 49.0 and 64.8.
 using WideConfig = Config<5, 8, true>;
 constexpr int kWideUnits = 6;                // up to so many units a CTA pair
 constexpr int kWideRows = 128;               // or rows an expert on average
+constexpr int kWideBlocks = 4;               // or K blocks of a tile of rows
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;   // instruction descriptor: operand is MN-major
 
 // Shared-memory descriptor of an MN-major bf16 tile: blocks of 64 K rows x 64
@@ -1024,6 +1026,7 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
 {
     ProductArgs a = {};
     long long units = 0, live = 0;
+    bool shallow = false;
     for (int i = 0; i < n; ++i) {
         const ProductJob &j = jobs[i];
         a.job[i] = j;
@@ -1040,6 +1043,7 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
             (!j.rows_on_n && !(j.out_f32 ? make_tile_map_f32(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32)
                         : make_tile_map(&a.out[i], j.out, out_rows, static_cast<uint64_t>(j.N), 32))))
             return cudaErrorInvalidValue;
+        shallow |= j.by_rows && j.k_blocks <= kWideBlocks;
         units += product_units(j, E, cap);
         // as many as there are with rows spread evenly
         live += j.by_rows ? (tiles_of(cap) > E ? tiles_of(cap) : (cap < E ? cap : E)) * tiles_of(j.N)
@@ -1051,7 +1055,7 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
     a.cap = cap;
     a.err = err;
     a.wait_limit_ns = kWaitLimitNs;
-    if (live <= kWideUnits * (num_sms / 2) || cap <= static_cast<long long>(kWideRows) * E)
+    if (live <= kWideUnits * (num_sms / 2) || cap <= static_cast<long long>(kWideRows) * E || shallow)
         return launch_pair<WideConfig>(products_kernel<WideConfig>, a, units, num_sms, stream);
     return launch_pair<DeepConfig>(products_kernel<DeepConfig>, a, units, num_sms, stream);
 }
