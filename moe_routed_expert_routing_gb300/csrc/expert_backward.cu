@@ -193,7 +193,7 @@ struct PairBars {
 };
 
 // Barriers and TMEM. The offsets are read and the units decoded by one warp
-// (load_offsets), while the others wait for the first units.
+// (load_offsets), while the others wait for the first units. Reads no global memory.
 template <class C>
 __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::kStages> &bars, uint32_t &s_tmem, int &s_abort)
 {
@@ -226,7 +226,6 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::k
     cluster_sync();   // both CTAs' barriers initialised before any remote arrive
     tc_fence_after();
     st.tmem = s_tmem;
-    pdl_wait();       // nothing above reads global memory
     return st;
 }
 
@@ -370,6 +369,8 @@ __device__ __forceinline__ void publish_units(const PairState &st, PairBars<kSta
     for (int batch = 0;; ++batch, u += static_cast<long long>(kBatch) * st.clusters) {
         const int b = batch & 1;
         int ok = 0;
+        if (batch == 2)
+            pdl_wait();    // the first two wait for nobody: no limit runs while the kernel ahead does
         if (lane == 0)
             ok = mbar_wait_bounded(smem_u32(&bars.uempty[b]), ((batch >> 1) & 1) ^ 1u, abort, limit_ns) ? 1 : 0;
         if (!__shfl_sync(kFull, ok, 0))
@@ -487,6 +488,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int NT = (args.I + 127) / 128;
     const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort);
+    pdl_wait();
     volatile int *abort_flag = &s_abort;
     const int k_blocks = args.H / kBK;
     pdl_trigger();    // the products' CTAs need this kernel's shared memory: each starts as one here ends
@@ -667,6 +669,7 @@ struct ProductArgs {
     int32_t *err;
     uint64_t wait_limit_ns;
     int jobs, E, cap;
+    int offsets_early;              // complete before the kernel ahead lets this one start
 };
 
 __device__ __forceinline__ int job_units(const ProductJob &j, const int *s_tp, int E)
@@ -763,6 +766,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
     __shared__ UnitDesc s_units[2 * kBatch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort);
+    // The decoding warp need not wait, so that the first units are ready when the kernel ahead ends
+    // (E=6, 1884 tokens of 3 experts, H=256, I=128 20.1 -> 18.4 us, E=32, 16 rows an expert,
+    // H=2048, I=1024 200.1 -> 197.8).
+    if (warp != 2 || !args.offsets_early)
+        pdl_wait();
     volatile int *abort_flag = &s_abort;
     const int rank = static_cast<int>(st.rank);
 
@@ -1022,7 +1030,7 @@ long long product_units(const ProductJob &j, int E, int cap)
 }
 
 cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offsets, int E, int cap, int32_t *err,
-                            int num_sms, cudaStream_t stream)
+                            int num_sms, bool offsets_early, cudaStream_t stream)
 {
     ProductArgs a = {};
     long long units = 0, live = 0;
@@ -1050,6 +1058,7 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
                           : product_units(j, E, cap);
     }
     a.jobs = n;
+    a.offsets_early = offsets_early;
     a.offsets = offsets;
     a.E = E;
     a.cap = cap;

@@ -275,7 +275,7 @@ moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const
         j.out = dW2;
         jobs[n++] = j;
     }
-    return cuda_status(launch_products(jobs, n, expert_offsets, p.E, cap, err, sms, s));
+    return cuda_status(launch_products(jobs, n, expert_offsets, p.E, cap, err, sms, true, s));
 }
 
 moe_status_t moe_norm_backward_workspace_size(const moe_norm_problem_t *problem, size_t *bytes)
@@ -430,7 +430,7 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
         j.out = dx;
         jobs[n++] = j;
     }
-    if (n && (st = cuda_status(launch_products(jobs, n, a.offsets, seg.segments, p.T_max, a.err, sms, s))) != MOE_OK)
+    if (n && (st = cuda_status(launch_products(jobs, n, a.offsets, seg.segments, p.T_max, a.err, sms, false, s))) != MOE_OK)
         return st;
     if (dw_router && seg.segments > 1)
         return cuda_status(launch_sum_parts(at<float>(ws, L.sums), seg.segments, static_cast<size_t>(p.E) * p.H,

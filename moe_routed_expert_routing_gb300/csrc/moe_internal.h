@@ -414,8 +414,11 @@ struct ProductJob {
 long long product_units(const ProductJob &j, int E, int cap);   // at most, for any offsets
 
 // Up to three products in one launch; their rows are the same batch of `cap` rows.
+// offsets_early: the kernel launched just before (act_grad_kernel) lets this one start only
+// once all before itself have ended, and writes no offsets: they are read, and the
+// units decoded, while it still runs.
 cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offsets, int E, int cap, int32_t *err,
-                            int num_sms, cudaStream_t stream);
+                            int num_sms, bool offsets_early, cudaStream_t stream);
 
 struct NormGradArgs {
     const void *h;             // bf16 or fp32
