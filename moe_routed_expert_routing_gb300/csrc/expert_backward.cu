@@ -669,7 +669,8 @@ struct ProductArgs {
     int32_t *err;
     uint64_t wait_limit_ns;
     int jobs, E, cap;
-    int offsets_early;              // complete before the kernel ahead lets this one start
+    const int32_t *num_rows;        // segments: as many rows as there are (null: cap)
+    int segment_rows;               // 0: ranges by `offsets`; else E segments of so many rows
 };
 
 __device__ __forceinline__ int job_units(const ProductJob &j, const int *s_tp, int E)
@@ -768,8 +769,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
     const PairState st = pair_begin<C>(smem_raw, bars, s_tmem, s_abort);
     // The decoding warp need not wait, so that the first units are ready when the kernel ahead ends
     // (E=6, 1884 tokens of 3 experts, H=256, I=128 20.1 -> 18.4 us, E=32, 16 rows an expert,
-    // H=2048, I=1024 200.1 -> 197.8).
-    if (warp != 2 || !args.offsets_early)
+    // H=2048, I=1024 200.1 -> 197.8; the router's, T=8192, E=128, H=4096 48.2 -> 46.1).
+    if (warp != 2)
         pdl_wait();
     volatile int *abort_flag = &s_abort;
     const int rank = static_cast<int>(st.rank);
@@ -905,7 +906,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
         }
         __syncwarp();
     } else if (warp == 2) {
-        load_offsets(args.offsets, args.E, args.cap, kTileRows, s_off, s_tp);
+        if (args.segment_rows) {
+            const int n = args.num_rows ? min(max(*args.num_rows, 0), args.cap) : args.cap;
+            for (int i = lane; i <= args.E; i += 32)
+                s_off[i] = static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(i) * args.segment_rows));
+            __syncwarp();
+            build_tile_prefix(s_off, s_tp, args.E, kTileRows, lane);
+            __syncwarp();
+        } else {
+            load_offsets(args.offsets, args.E, args.cap, kTileRows, s_off, s_tp);
+        }
         int units = 0;
         for (int j = 0; j < args.jobs; ++j)
             units += job_units(args.job[j], s_tp, args.E);
@@ -1029,8 +1039,8 @@ long long product_units(const ProductJob &j, int E, int cap)
                      : E * tiles_of(j.M) * (j.rows_on_n ? (j.N + 127LL) / 128 : tiles_of(j.N));
 }
 
-cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offsets, int E, int cap, int32_t *err,
-                            int num_sms, bool offsets_early, cudaStream_t stream)
+cudaError_t launch_products(const ProductJob *jobs, int n, const ProductRows &rows, int E, int cap, int32_t *err,
+                            int num_sms, cudaStream_t stream)
 {
     ProductArgs a = {};
     long long units = 0, live = 0;
@@ -1058,8 +1068,9 @@ cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offset
                           : product_units(j, E, cap);
     }
     a.jobs = n;
-    a.offsets_early = offsets_early;
-    a.offsets = offsets;
+    a.offsets = rows.offsets;
+    a.num_rows = rows.num_rows;
+    a.segment_rows = rows.segment_rows;
     a.E = E;
     a.cap = cap;
     a.err = err;

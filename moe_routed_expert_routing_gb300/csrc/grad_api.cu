@@ -112,7 +112,7 @@ RouteSplitK route_segments(const moe_router_problem_t &p)
 }
 
 struct RouteGradLayout {
-    size_t offsets, parts, sums, total;
+    size_t parts, sums, total;
 };
 
 moe_status_t check_route_grad(const moe_router_problem_t *p)
@@ -133,8 +133,7 @@ RouteGradLayout route_grad_layout(const moe_router_problem_t &p)
     const RouteSplitK s = route_segments(p);
     const size_t Ep = (p.E + 63) / 64 * 64;
     RouteGradLayout L;
-    L.offsets = workspace_header_bytes();
-    L.parts = align_up(L.offsets + sizeof(int32_t) * (s.segments + 1));
+    L.parts = align_up(workspace_header_bytes());
     L.sums = align_up(L.parts + 4 * Ep * (static_cast<size_t>(p.T_max) + 1));
     const size_t sums = s.segments > 1 ? sizeof(float) * s.segments * p.E * static_cast<size_t>(p.H) : 0;
     L.total = align_up(L.sums + sums);
@@ -275,7 +274,7 @@ moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const
         j.out = dW2;
         jobs[n++] = j;
     }
-    return cuda_status(launch_products(jobs, n, expert_offsets, p.E, cap, err, sms, true, s));
+    return cuda_status(launch_products(jobs, n, {expert_offsets, nullptr, 0}, p.E, cap, err, sms, s));
 }
 
 moe_status_t moe_norm_backward_workspace_size(const moe_norm_problem_t *problem, size_t *bytes)
@@ -372,7 +371,6 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
     a.d_num_tokens = d_num_tokens;
     a.d_logits = d_logits;
     a.parts = at<void>(ws, L.parts);
-    a.offsets = at<int32_t>(ws, L.offsets);
     a.err = at<int32_t>(ws, 0);
     a.T_max = p.T_max;
     a.E = p.E;
@@ -380,8 +378,6 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
     a.sigmoid = p.score == MOE_SCORE_SIGMOID;
     a.renormalize = p.renormalize;
     a.scale = p.scale;
-    a.segments = seg.segments;
-    a.segment_rows = seg.rows;
     if (route_grad_few(a)) {
         RouteFewArgs f = {};
         f.x = static_cast<const __nv_bfloat16 *>(x);
@@ -430,7 +426,8 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
         j.out = dx;
         jobs[n++] = j;
     }
-    if (n && (st = cuda_status(launch_products(jobs, n, a.offsets, seg.segments, p.T_max, a.err, sms, false, s))) != MOE_OK)
+    const ProductRows rows = {nullptr, d_num_tokens, seg.rows};
+    if (n && (st = cuda_status(launch_products(jobs, n, rows, seg.segments, p.T_max, a.err, sms, s))) != MOE_OK)
         return st;
     if (dw_router && seg.segments > 1)
         return cuda_status(launch_sum_parts(at<float>(ws, L.sums), seg.segments, static_cast<size_t>(p.E) * p.H,

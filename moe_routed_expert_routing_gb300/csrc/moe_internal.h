@@ -413,12 +413,19 @@ struct ProductJob {
 
 long long product_units(const ProductJob &j, int E, int cap);   // at most, for any offsets
 
-// Up to three products in one launch; their rows are the same batch of `cap` rows.
-// offsets_early: the kernel launched just before (act_grad_kernel) lets this one start only
-// once all before itself have ended, and writes no offsets: they are read, and the
-// units decoded, while it still runs.
-cudaError_t launch_products(const ProductJob *jobs, int n, const int32_t *offsets, int E, int cap, int32_t *err,
-                            int num_sms, bool offsets_early, cudaStream_t stream);
+// The ranges of rows: by offsets [E + 1], or E segments of segment_rows up to *num_rows (null: cap).
+struct ProductRows {
+    const int32_t *offsets;
+    const int32_t *num_rows;
+    int segment_rows;
+};
+
+// Up to three products in one launch; their rows are the same batch of `cap` rows. The
+// kernel launched just before must let this one start only after a wait of its own for what
+// came before it, and write neither offsets nor num_rows: they are read, and the units
+// decoded, while it still runs.
+cudaError_t launch_products(const ProductJob *jobs, int n, const ProductRows &rows, int E, int cap, int32_t *err,
+                            int num_sms, cudaStream_t stream);
 
 struct NormGradArgs {
     const void *h;             // bf16 or fp32
@@ -448,11 +455,9 @@ struct RouteGradArgs {
     float *d_logits;           // [T_max, E] or null
     void *parts;               // [T_max + 1, 2 Ep] bf16, Ep = E rounded up to 64: leading parts, then rests;
                                // the last row is set to zeros
-    int32_t *offsets;          // [segments + 1]: the segments' token ranges
     int32_t *err;
     int T_max, E, k;
     int sigmoid, renormalize;
-    int segments, segment_rows;
     float scale;
 };
 

@@ -17,7 +17,7 @@
 // leading part and rest, so it counts with 16 bits, a relative 2^-16 off at
 // most; both products' sums stay fp32. One part would cost a gradient 1.7e-3 of
 // its rms, as much as a bf16 output's own rounding; a third part (24 bits) would
-// show in an fp32 dw_router only. T=8192, E=128, H=4096 48 us in a graph (0.15 GB, 22 us
+// show in an fp32 dw_router only. T=8192, E=128, H=4096 46 us in a graph (0.15 GB, 22 us
 // at the copy rate): 6 us for dl, then the two products, 19 and 17 us on their own,
 // which end in epilogues of a few K blocks' work each, then 4 for the sum of
 // dw_router's four token ranges. A few slots go another way (route_grad_few_kernel).
@@ -165,9 +165,6 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
     pdl_wait();
     pdl_trigger();
     const int T = token_count(a);
-    if (blockIdx.x == 0)
-        for (int s = threadIdx.x; s <= a.segments; s += kThreads)
-            a.offsets[s] = static_cast<int>(min(static_cast<long long>(T), static_cast<long long>(s) * a.segment_rows));
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < Ep; i += kThreads)     // 2 Ep bf16 zeros
             reinterpret_cast<uint32_t *>(a.parts)[static_cast<size_t>(a.T_max) * Ep + i] = 0u;
