@@ -983,6 +983,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
             bulk_wait_all();
         __syncwarp();
     }
+    // The decoding warp may get here while the kernel ahead still runs, and one thread's trigger
+    // counts for its CTA: no dependent may start before that kernel has completed.
+    pdl_wait();
     pdl_trigger();
     pair_end(st, s_abort, args.err);
 }
