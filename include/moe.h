@@ -562,7 +562,9 @@ moe_status_t moe_expert_backward_workspace_size(const moe_expert_grad_problem_t 
  *   da[r]  = dy_sorted[r] W2[e],  du = da g s,  dg = da u s (1 + g (1 - s))
  *   dx_sorted[r] = [dg du][r] W13[e]
  *   dW2[e]  = sum_r dy_sorted[r]^T a[r],  dW13[e] = sum_r [dg du][r]^T x_sorted[r]
- * fp32 sums on the tensor cores; a and [dg du] are rounded to bf16 once, as
+ * fp32 sums on the tensor cores, whose additions truncate (a sum of n products is
+ * off by up to (n / 16 + 32) 2^-23 of the sum of their |values|: n rows of an expert
+ * for its weight gradients); a and [dg du] are rounded to bf16 once, as
  * their operands, and each output once. An expert without rows gets zero
  * weight gradients (none added with `accumulate`).
  *   x_sorted, dy_sorted [cap, H] bf16; expert_offsets[E+1] of moe_dispatch (or
@@ -611,7 +613,11 @@ moe_status_t moe_route_backward_workspace_size(const moe_router_problem_t *probl
  *   dx[t, m]       = bf16( sum_e d_logits[t, e] w_router[e, m] )
  *   dw_router[e,m] = sum_{t < T} d_logits[t, e] x[t, m]
  * The choice of experts and the selection bias have no gradient. The products
- * take d_logits with 16 bits (two bf16 parts; a relative 2^-16) and sum in fp32.
+ * take d_logits with 16 bits (two bf16 parts; a relative 2^-16) and sum in fp32
+ * on the tensor cores, whose additions truncate: dx is off by up to (E / 8 + 32) 2^-23
+ * of the sum of its |terms|, dw_router by up to 6.5e-5 of its own, since no such sum
+ * goes over more than 4096 tokens (T / 1024 past 4 million): those of the ranges
+ * are added in fp32, 2^-24 each.
  * Logits that are NaN or +inf count as -inf, whose gradient is 0; an id of -1
  * adds nothing, an id outside [0, E) neither and sets MOE_DEVERR_BAD_EXPERT_ID.
  *   x[T_max, H] bf16 (NULL without dw_router), w_router[E, H] bf16 (NULL without

@@ -91,7 +91,17 @@ NormGradLayout norm_layout(const moe_norm_problem_t &p)
 // ---- router ----
 
 // Token ranges whose products for dw_router are summed apart, so that a
-// [E, H] result with few tiles still fills the GPU.
+// [E, H] result with few tiles still fills the GPU: a unit for each of a
+// GB300's 76 CTA pairs, or two where that leaves one range. A range is one
+// unbroken sum on the tensor cores, whose additions truncate: (2 rows / 16) of them, 2^-23 of
+// the sum each at most, so ranges have kRangeRows tokens at most and their sums are
+// added in fp32. Same-signed terms with T=262144, E=128, H=4096 were off by 4.5e-4 of
+// dw in four ranges, and by 1.7e-5 in 64. The call's time at T=65536 with E=128, H=4096
+// 255 us in four ranges, 269 in 16, with E=384, H=7168 1044 in two and 975 in 16; T=8192,
+// E=1024, H=7168 289 in one and 306 in two. (More than kRangeRows * kMaxExperts
+// tokens, 4.2 million, go in kMaxExperts longer ranges.)
+constexpr int kRangeRows = 4096;
+
 struct RouteSplitK {
     int segments, rows;
 };
@@ -99,15 +109,14 @@ struct RouteSplitK {
 RouteSplitK route_segments(const moe_router_problem_t &p)
 {
     const long long tiles = ((p.E + 255LL) / 256) * ((p.H + 255LL) / 256);
-    long long want = 76 / tiles;       // a unit for each CTA pair, or two where that leaves one range
+    long long want = 76 / tiles;
     if (want < 2)
         want = 152 / tiles;
     if (want < 1)
         want = 1;
-    long long rows = (p.T_max + want - 1) / want;
-    rows = (rows + 255) / 256 * 256;
-    if (rows > (1 << 30))
-        rows = 1 << 30;
+    const long long fill = (p.T_max + want - 1) / want, least = (p.T_max + kMaxExperts - 1LL) / kMaxExperts;
+    long long rows = fill < kRangeRows ? fill : kRangeRows;
+    rows = ((rows > least ? rows : least) + 255) / 256 * 256;
     return {static_cast<int>((p.T_max + rows - 1) / rows), static_cast<int>(rows)};
 }
 
@@ -122,7 +131,7 @@ moe_status_t check_route_grad(const moe_router_problem_t *p)
         return st;
     // units of the products are counted in 32 bits
     const RouteSplitK s = route_segments(*p);
-    const long long nh = (p->H + 255LL) / 256, ne = (p->E + 255LL) / 256;
+    const long long nh = (p->H + 255LL) / 256, ne = (p->E + 127LL) / 128;
     if (((p->T_max + 255LL) / 256 + s.segments + s.segments * ne) * nh > (1LL << 31) - 1)
         return MOE_ERR_SHAPE;
     return MOE_OK;
