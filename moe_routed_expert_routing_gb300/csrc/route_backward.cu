@@ -153,6 +153,13 @@ __device__ __forceinline__ void add_terms(float *dl, const Chosen &c, int k)
     }
 }
 
+// The leading bf16 part of an element of dl. One that would round up to infinity is
+// cut off instead, its rest then holds what is missing; an infinite one has no rest.
+__device__ __forceinline__ __nv_bfloat16 leading_part(float v)
+{
+    return fabsf(v) > 3.38953139e38f ? __float2bfloat16_rz(v) : __float2bfloat16_rn(v);     // the largest bf16
+}
+
 // One warp per token. Its row of dl grows in shared memory: base values, then
 // the chosen experts' terms.
 __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_constant__ RouteGradArgs a)
@@ -215,8 +222,8 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
             __align__(8) __nv_bfloat16 hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                hi[i] = __float2bfloat16_rn(v[i]);
-                lo[i] = __float2bfloat16_rn(v[i] - __bfloat162float(hi[i]));
+                hi[i] = leading_part(v[i]);
+                lo[i] = isinf(v[i]) ? __float2bfloat16_rn(0.f) : __float2bfloat16_rn(v[i] - __bfloat162float(hi[i]));
             }
             *reinterpret_cast<uint2 *>(parts + e) = *reinterpret_cast<const uint2 *>(hi);
             *reinterpret_cast<uint2 *>(parts + Ep + e) = *reinterpret_cast<const uint2 *>(lo);
