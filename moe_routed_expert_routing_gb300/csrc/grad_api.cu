@@ -248,13 +248,11 @@ moe_status_t moe_expert_backward(const moe_expert_grad_problem_t *problem, const
         j.N = p.H;
         j.k_blocks = j.wrap = 2 * p.I / 64;
         j.b_expert_rows = 2 * p.I;
-        j.parts = 1;
         j.out = dx_sorted;
         j.out_f32 = problem->dx_dtype == MOE_DTYPE_FP32;
         jobs[n++] = j;
     }
     ProductJob w = {};
-    w.parts = w.wrap = 1;
     w.a_rows = w.b_rows = cap;
     w.out_f32 = problem->dw_dtype == MOE_DTYPE_FP32;
     w.accumulate = problem->accumulate;
@@ -412,8 +410,6 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
         j.b_cols = 2LL * Ep;
         j.M = p.H;
         j.N = p.E;
-        j.wrap = 1;
-        j.parts = 2;
         j.part_cols = Ep;
         j.out = seg.segments > 1 ? at<void>(ws, L.sums) : dw_router;
         j.out_f32 = seg.segments > 1 || dw_dtype == MOE_DTYPE_FP32;
@@ -431,7 +427,6 @@ moe_status_t moe_route_backward(const moe_router_problem_t *problem, int32_t dw_
         j.N = p.H;
         j.k_blocks = 2 * Ep / 64;
         j.wrap = Ep / 64;
-        j.parts = 1;
         j.out = dx;
         jobs[n++] = j;
     }

@@ -395,7 +395,7 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
 // [offsets[e], offsets[e + 1]):
 //  by_rows:  out[r, n] = sum_k a[r, k] b[e * b_expert_rows + k mod (64 wrap), n], r in R_e, k < 64 k_blocks
 //  else:     out[e, m, n] = sum_{r in R_e} a[r, m] b[r, n], m < M
-//  rows_on_n: out[e, n, m] = sum_{p < parts} sum_{r in R_e} a[r, m] b[r, n + p part_cols], m < M: as above with
+//  rows_on_n: out[e, n, m] = sum_{p < 2} sum_{r in R_e} a[r, m] b[r, n + p part_cols], m < M: as above with
 //            the output transposed, for an N below 256 columns: the MMAs and B's loads follow it in steps of 128
 // for n < N. a [a_rows, a_cols], b [b_rows, b_cols] and out ([cap, N], [E, M, N] or [E, N, M]) row-major.
 struct ProductJob {
@@ -403,8 +403,8 @@ struct ProductJob {
     const void *a, *b;
     long long a_rows, a_cols, b_rows, b_cols;
     int M, N;
-    int k_blocks, wrap, b_expert_rows;
-    int parts, part_cols;
+    int k_blocks, wrap, b_expert_rows;      // by_rows
+    int part_cols;          // rows_on_n: from one part of b's columns to the next
     int zero_in_a;          // not by_rows: row `cap` of a (else of b) exists and holds zeros
     void *out;
     int out_f32;            // fp32, else bf16
