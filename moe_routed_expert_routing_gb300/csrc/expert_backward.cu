@@ -48,19 +48,16 @@ constexpr int kUmmaK = 16;
 constexpr int kTileRows = 256;               // rows of a CTA pair's tile
 constexpr int kRowBox = 32;                  // rows of a box of a partial tile
 constexpr int kHalf = 128 * 128;             // bytes of one operand's half tile: 128 x 64 bf16
+constexpr int kStageBytes = 2 * kHalf;        // A, then B
 constexpr int kAtom = 64 * 128;              // bytes of an MN-major block: 64 K rows x 64 columns
 constexpr int kBox = 32 * 128;               // bytes of an output box: 32 rows x 128 bytes
 
 // A kernel's pipeline stages and epilogue warps: four, one for each quarter of
 // the TMEM lanes, or eight, each with half the columns.
-template <int kStages_, int kWarps_, bool kBoxes, int kRows_ = kTileRows, bool kSplit_ = false>
+template <int kStages_, int kWarps_, bool kBoxes, bool kSplit_ = false>
 struct Config {
     static constexpr int kStages = kStages_, kWarps = kWarps_;
     static constexpr bool kSplit = kSplit_;      // tiles of up to 128 rows in halves
-    static constexpr int kRows = kRows_;         // of a row tile
-    // A's half of a stage: one K block, or two of half the rows
-    static constexpr int kABytes = kRows == kTileRows ? kHalf : 2 * kRows * 128;
-    static constexpr int kStageBytes = kABytes + kHalf;
     static constexpr int kThreads = 128 + 32 * kWarps;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + (kBoxes ? kWarps * kBox : 0);
 };
@@ -71,16 +68,13 @@ using ActConfig = Config<6, 8, false>;
 // its way at six stages. act_grad_kernel, E=50, 1000 tokens of 6 experts, H=2880, I=1472
 // 261 -> 250 us; E=32, 32 rows an expert, H=2048, I=1024 107.5 -> 98.5. With whole tiles beside
 // them such halves cost (E=128, 256 rows an expert, H=4096, I=1536, both kernels 3.40 and
-// 3.51 ms).
-using SplitConfig = Config<6, 8, false, kTileRows, true>;
+// 3.51 ms). (Tiles of 32 rows up to 24 rows an expert, with more stages of weights on their way,
+// gained 1 to 3% where every expert has as many rows, but an expert of many rows then fetches its
+// weights for every 32 of them, and the host does not know: E=128, H=2048, I=1024, 16 rows on average 702
+// and 710 us, with shares of 1 / rank^1.2 734 and 691; E=64, H=4096, I=1536, 24 rows 1067 and
+// 1078, 1200 and 1107.)
+using SplitConfig = Config<6, 8, false, true>;
 constexpr int kSplitRows = 128;
-// Few rows an expert: tiles of 32 rows, all in the even CTA, whose A takes 8 KB of
-// a stage, so that eight stages of weights are on their way. The MMAs still read 128 rows of
-// A: what lies behind those 32 (the stage's B) gives rows that are not stored.
-// Both kernels, E=5, 25 tokens of 2 experts, H=3904, I=960 85.3 us (88.2 with SplitConfig);
-// E=32, H=2048, I=1024 219.0 us (220.0) at 16 rows an expert, 219.2 (220.5) at 24.
-using ThinConfig = Config<8, 8, false, 32, true>;
-constexpr int kThinRows = 24;                // up to so many rows an expert on average
 using DeepConfig = Config<6, 4, true>;       // products: more copies in flight
 // Small problems, where each unit's way from its first copy to its last store
 // counts: E=16, 64 tokens of 4 experts, H=1024, I=512 (5.9 units a pair) 38.5 us, with
@@ -230,7 +224,7 @@ __device__ __forceinline__ PairState pair_begin(uint8_t *smem_raw, PairBars<C::k
 }
 
 // A warp: the experts' offsets, clamped to the batch, and their row tiles.
-__device__ __forceinline__ void load_offsets(const int32_t *offsets, int E, int cap, int tile_rows, int *s_off, int *s_tp)
+__device__ __forceinline__ void load_offsets(const int32_t *offsets, int E, int cap, int *s_off, int *s_tp)
 {
     const int lane = threadIdx.x & 31;
     for (int i = lane; i <= E; i += 32) {
@@ -238,7 +232,7 @@ __device__ __forceinline__ void load_offsets(const int32_t *offsets, int E, int 
         s_off[i] = o < 0 ? 0 : (o > cap ? cap : o);
     }
     __syncwarp();
-    build_tile_prefix(s_off, s_tp, E, tile_rows, lane);
+    build_tile_prefix(s_off, s_tp, E, kTileRows, lane);
     __syncwarp();
 }
 
@@ -266,11 +260,11 @@ __device__ __forceinline__ void pair_end(const PairState &st, int &s_abort, int3
 // and a branch between the steps (the router's second part beside the plain
 // step) cost the products a third of their rate: dx at E=16, T=8192, H=4096, I=1536
 // 1.29 ms and 0.93.
-template <bool kAMn, bool kBMn, int kABytes = kHalf>
+template <bool kAMn, bool kBMn>
 __device__ __forceinline__ void mma_stage(uint32_t d, uint32_t a_addr, uint32_t idesc, bool first, int steps)
 {
     constexpr uint32_t kA = kAMn ? 2048 >> 4 : 32 >> 4, kB = kBMn ? 2048 >> 4 : 32 >> 4;
-    const uint32_t b_addr = a_addr + kABytes;
+    const uint32_t b_addr = a_addr + kHalf;
     const uint64_t a0 = kAMn ? smem_desc_mnmajor_sw128(a_addr) : smem_desc_kmajor_sw128(a_addr);
     const uint64_t b0 = kBMn ? smem_desc_mnmajor_sw128(b_addr) : smem_desc_kmajor_sw128(b_addr);
     if (steps == kBK / kUmmaK) {
@@ -442,7 +436,7 @@ struct ActArgs {
 // tiles that load only their rows it does not pay: 256 rows an expert, E=128, H=4096,
 // I=1536 3.48 ms with it and 3.35 without, 120 rows 702 us and 690; only very few long
 // ones gain, 10 rows of each of 5 experts, H=3904, I=960 92 us and 100.)
-__device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, const int *s_tp, int E, int NT, int tile_rows)
+__device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, const int *s_tp, int E, int NT)
 {
     const int e = find_expert(s_tp, E, u, NT);
     const int local = u - s_tp[e] * NT;
@@ -450,8 +444,8 @@ __device__ __forceinline__ void act_unit(int u, UnitDesc &d, const int *s_off, c
     const int nt = local / tiles;
     d.job = 0;
     d.e = e;
-    d.m0 = s_off[e] + (local - nt * tiles) * tile_rows;
-    d.rows = min(s_off[e + 1] - d.m0, tile_rows);
+    d.m0 = s_off[e] + (local - nt * tiles) * kTileRows;
+    d.rows = min(s_off[e + 1] - d.m0, kTileRows);
     d.n0 = nt * 128;
 }
 
@@ -520,8 +514,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
                         break;
                     }
                     const uint32_t full = map_to_cta(smem_u32(&bars.full[r.stage]), 0);
-                    const uint32_t a_dst = smem_u32(st.smem + r.stage * C::kStageBytes);
-                    const uint32_t b_dst = a_dst + C::kABytes;
+                    const uint32_t a_dst = smem_u32(st.smem + r.stage * kStageBytes);
+                    const uint32_t b_dst = a_dst + kHalf;
                     if (kb < k_blocks) {
                         const int kc = kb * kBK;
                         if (C::kSplit && split < 128) {
@@ -530,7 +524,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
                             mbar_arrive_expect_tx_cluster(full, n * (boxed * 128 + kAtom));
                             tma_load_2d_pair(b_dst, n == 2 ? &args.w2_two : &args.w2, full, n0 + 64 * rank, w2_row + kc, pol_w);
                             for (int i = 0; boxed && i < n; ++i)
-                                tma_load_2d_pair(a_dst + i * (C::kABytes / 2), part, full, kc + i * kBK, a_row, pol_a);
+                                tma_load_2d_pair(a_dst + i * kAtom, part, full, kc + i * kBK, a_row, pol_a);
                         } else {
                             mbar_arrive_expect_tx_cluster(full, boxed * 128 + kAtom);
                             load_rows(a_dst, &args.dy, &args.dy32, full, kc, a_row, boxed, pol_a);
@@ -566,10 +560,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(st.smem + r.stage * C::kStageBytes);
-                    mma_stage<false, true, C::kABytes>(d_da, a_addr, kIdescDa, kb == 0, 4);
-                    if (per == 2 && kb + 1 < k_blocks)
-                        mma_stage<false, true, C::kABytes / 2 + kAtom>(d_da, a_addr + C::kABytes / 2, kIdescDa, false, 4);
+                    const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
+                    mma_stage<false, true>(d_da, a_addr, kIdescDa, kb == 0, 4);
+                    if (per == 2 && kb + 1 < k_blocks)      // A's second half tile is 64 rows behind, as B's is
+                        mma_stage<false, true>(d_da, a_addr + kAtom, kIdescDa, false, 4);
                     umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (!ok || !mbar_wait_bounded(smem_u32(&bars.tempty[0]), (local & 1) ^ 1u, abort_flag,
@@ -583,7 +577,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
                         break;
                     }
                     tc_fence_after();
-                    mma_stage<false, false, C::kABytes>(d_gu, smem_u32(st.smem + r.stage * C::kStageBytes), kIdescGu, kb == 0, 4);
+                    mma_stage<false, false>(d_gu, smem_u32(st.smem + r.stage * kStageBytes), kIdescGu, kb == 0, 4);
                     umma_commit_pair(smem_u32(&bars.empty[r.stage]), 0x3);
                 }
                 if (ok)
@@ -595,9 +589,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) act_grad_kernel(const __grid_c
         }
         __syncwarp();
     } else if (warp == 2) {
-        load_offsets(args.offsets, args.E, args.cap, C::kRows, s_off, s_tp);
+        load_offsets(args.offsets, args.E, args.cap, s_off, s_tp);
         publish_units(st, bars, s_units, s_tp[args.E] * NT, abort_flag, args.wait_limit_ns, [&](int u, UnitDesc &d) {
-            act_unit(u, d, s_off, s_tp, args.E, NT, C::kRows);
+            act_unit(u, d, s_off, s_tp, args.E, NT);
         });
     } else if (warp >= 4) {
         const int q = warp & 3, half = (warp - 4) >> 2;
@@ -797,7 +791,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                         break;
                     }
                     const uint32_t full = map_to_cta(smem_u32(&bars.full[r.stage]), 0);
-                    const uint32_t a_dst = smem_u32(st.smem + r.stage * C::kStageBytes);
+                    const uint32_t a_dst = smem_u32(st.smem + r.stage * kStageBytes);
                     const uint32_t b_dst = a_dst + kHalf;
                     if (by_rows) {
                         const int b_row = b_row0 + kp * kBK;
@@ -840,7 +834,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                                 }
                             }
                         } else {
-                            mbar_arrive_expect_tx_cluster(full, C::kStageBytes);
+                            mbar_arrive_expect_tx_cluster(full, kStageBytes);
                             tma_load_2d_pair(a_dst, ma, full, a_col, row, pol);
                             tma_load_2d_pair(a_dst + kAtom, ma, full, a_col + 64, row, pol);
                             tma_load_2d_pair(b_dst, mb, full, b_col, row, pol);
@@ -876,7 +870,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(st.smem + r.stage * C::kStageBytes);
+                    const uint32_t a_addr = smem_u32(st.smem + r.stage * kStageBytes);
                     const int steps = (rem && kb + 1 == total) ? (rem + kUmmaK - 1) / kUmmaK : kBK / kUmmaK;
                     if (by_rows) {
                         mma_stage<false, true>(d, a_addr, idesc_bf16_f32(256, 256) | kMajorB, kb == 0, kBK / kUmmaK);
@@ -910,7 +904,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
             build_tile_prefix(s_off, s_tp, args.E, kTileRows, lane);
             __syncwarp();
         } else {
-            load_offsets(args.offsets, args.E, args.cap, kTileRows, s_off, s_tp);
+            load_offsets(args.offsets, args.E, args.cap, s_off, s_tp);
         }
         int units = 0;
         for (int j = 0; j < args.jobs; ++j)
@@ -921,7 +915,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) products_kernel(const __grid_c
     } else if (warp >= 4) {
         const int q = warp & 3, half = (warp - 4) >> 2;
         constexpr int kHalves = C::kWarps / 4;
-        uint8_t *const box = st.smem + C::kStages * C::kStageBytes + (warp - 4) * kBox;
+        uint8_t *const box = st.smem + C::kStages * kStageBytes + (warp - 4) * kBox;
         UnitReader units(s_units, bars.ufull, bars.uempty);
         int local = 0;
         for (; const UnitDesc *tp = units.next_warp(lane, abort_flag, args.wait_limit_ns); ++local) {
@@ -1103,8 +1097,6 @@ cudaError_t launch_act_grad(const void *x, const void *dy, const void *W13, cons
         if (!make_tile_map(&a.x64, x, rows, h, 64) || !make_tile_map(&a.dy64, dy, rows, h, 64) ||
             !make_tile_map(&a.w2_two, W2, e * h, i, 128))
             return cudaErrorInvalidValue;
-        if (cap <= static_cast<long long>(kThinRows) * E)
-            return launch_pair<ThinConfig>(act_grad_kernel<ThinConfig>, a, (cap / ThinConfig::kRows + E) * nt, num_sms, stream);
         return launch_pair<SplitConfig>(act_grad_kernel<SplitConfig>, a, (tiles_of(cap) + E) * nt, num_sms, stream);
     }
     return launch_pair<ActConfig>(act_grad_kernel<ActConfig>, a, (tiles_of(cap) + E) * nt, num_sms, stream);

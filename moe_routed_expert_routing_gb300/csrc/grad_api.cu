@@ -67,8 +67,7 @@ moe_status_t check_expert_grad(const moe_expert_grad_problem_t *p)
     const long long cap = capacity_of(p->experts), E = p->experts.E, H = p->experts.H, I = p->experts.I;
     const long long nh = (H + 255) / 256, ni = (I + 255) / 256, n2i = (2 * I + 255) / 256;
     const long long tiles = (cap + 255) / 256 + E;
-    // (the first kernel's row tiles may have 32 rows)
-    if (tiles * nh + E * nh * ni + E * n2i * nh > (1LL << 31) - 1 || (cap / 32 + E) * ((I + 127) / 128) > (1LL << 31) - 1)
+    if (tiles * nh + E * nh * ni + E * n2i * nh > (1LL << 31) - 1 || tiles * ((I + 127) / 128) > (1LL << 31) - 1)
         return MOE_ERR_SHAPE;
     return MOE_OK;
 }
