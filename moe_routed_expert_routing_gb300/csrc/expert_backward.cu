@@ -76,17 +76,22 @@ using ActConfig = Config<6, 8, false>;
 using SplitConfig = Config<6, 8, false, true>;
 constexpr int kSplitRows = 128;
 using DeepConfig = Config<6, 4, true>;       // products: more copies in flight
-// Small problems, where each unit's way from its first copy to its last store
-// counts: E=16, 64 tokens of 4 experts, H=1024, I=512 (5.9 units a pair) 38.5 us, with
-// DeepConfig 41.7. And few rows an expert, where the weight gradients' tiles have one or two
-// K blocks and wait for their epilogue: E=32, H=2048, I=1024 at 16, 32 and 64 rows an expert
-// 201, 207 and 212 us, with DeepConfig 219, 221 and 225; E=50, 120 rows, H=2880, I=1472 679
-// and 684; E=128, 128 rows, H=4096, I=1536 2521 and 2513, 180 rows 2820 and 2715, 512 rows
-// 5.71 and 5.60 ms. The router's gradient likewise at few K blocks (its dx's, twice E / 64):
-// T=8192, H=4096 with E=64, 128 and 256 42.5, 48.0 and 66.4 us, with DeepConfig 44.8, 49.0 and 64.8.
+// Products with eight epilogue warps, us beside those with DeepConfig:
+//  * few rows an expert, where the weight gradients' tiles have one or two K blocks and wait for
+//    their epilogue: E=32, H=2048, I=1024 at 16, 32 and 64 rows an expert 201 / 219, 207 / 221 and
+//    212 / 225; E=50, 120 rows, H=2880, I=1472 679 / 684; E=128, H=4096, I=1536 at 128 rows 2521 /
+//    2513, 180 rows 2820 / 2715, 512 rows 5710 / 5600;
+//  * small problems, where each unit's way from its first copy to its last store counts: H=1024, I=512,
+//    160 rows an expert with 1.5, 4.4, 5.9 and 8.8 units a pair 26.6 / 27.3, 36.3 / 37.6, 43.9 / 44.4 and
+//    63.6 / 63.9; the router's E=384, H=7168 at T=257, 500, 1000 and 2000 20.7 / 21.7, 22.1 / 22.9, 28.7 / 28.5
+//    and 46.2 / 44.9. More rows an expert give some of it back: 256 rows with 1.5, 2.9, 5.9 and 8.8 units 25.9 /
+//    26.8, 33.0 / 32.9, 57.8 / 56.2 and 70.5 / 68.6, 512 rows with 0.8, 1.7 and 5.1 25.7 / 25.9, 29.5 / 29.0
+//    and 58.7 / 56.7;
+//  * few K blocks of a tile of rows, the router's dx (twice E / 64): T=8192, H=4096 with E=64, 128 and
+//    256 42.5 / 44.8, 48.0 / 49.0 and 66.4 / 64.8.
 using WideConfig = Config<5, 8, true>;
-constexpr int kWideUnits = 6;                // up to so many units a CTA pair
-constexpr int kWideRows = 128;               // or rows an expert on average
+constexpr int kWideRows = 128;               // up to so many rows an expert on average
+constexpr int kWideUnits = 6;                // or units a CTA pair
 constexpr int kWideBlocks = 4;               // or K blocks of a tile of rows
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;   // instruction descriptor: operand is MN-major
 
