@@ -28,13 +28,15 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // With `pdl` set, a kernel of the library may start while the kernel before
 // it on the stream is still finishing (cudaLaunchAttributeProgrammaticStream-
 // Serialization): it runs its prologue, then waits (griddepcontrol.wait) for
-// the previous grid's completion and memory before touching any global data,
+// the previous grid's completion and memory before touching any global data
+// (but for what a kernel two or more launches back wrote),
 // and releases its own dependents (griddepcontrol.launch_dependents), only
-// after that wait. Every kernel waits before it finishes, so completion stays
+// after that wait, by every thread: one thread's release counts for its block. Every
+// kernel waits before it finishes, so completion stays
 // transitive along the stream, and when a kernel starts, every kernel two or
 // more launches back has completed; without the attribute both instructions
-// are no-ops. The host turns
-// it on for the M-small (decode) path only: measured in one process, it saves
+// are no-ops. The norms, the router and the gradients of both and of the experts use it; of the expert GEMMs'
+// paths the host turns it on for the M-small (decode) one only: measured in one process, it saves
 // ~8 us per decode step and costs ~90 us per large-batch step, where the early
 // dependents share the SMs with the persistent GEMM.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
